@@ -1,9 +1,11 @@
 """MI355X-native dense GEMM on gfx950 matrix cores: C = A . B, and the
 generalised C = alpha * op(A) * op(B) + beta * C with fp32 or bf16 C; and 2-D
-convolution (forward and filter gradient) as im2col + that GEMM.
+convolution (forward and filter gradient) as im2col + that GEMM; and linear
+layers (bias, activation and residual in the product, dense or grouped by
+expert, with their gradients).
 
-A thin ctypes binding over the C ABI of ``include/gemm.h`` and
-``include/conv.h`` (library
+A thin ctypes binding over the C ABI of ``include/gemm.h``,
+``include/conv.h`` and ``include/gemm_linear.h`` (library
 ``libdense_gemm.so`` next to this file).  The functions of the same names take
 the same arguments as the C entry points -- sizes, device pointers as
 integers, leading dimensions and a stream handle -- and only marshal them;
@@ -106,6 +108,15 @@ SIGNATURES.update({
     "convnd_bwd_weight_implicit_ex": (_int, [_int, _pnd, _int, _p, _p, _p, _p]),
 })
 
+from .layers import (  # noqa: E402,F401
+    ACTIVATIONS, GEMM_ACT_GELU, GEMM_ACT_GELU_TANH, GEMM_ACT_NONE, GEMM_ACT_RELU, GEMM_ACT_SILU,
+    LinearParams, gemm_linear, gemm_linear_act_grad, gemm_linear_act_grad_workspace_size,
+    gemm_linear_config_forms, gemm_linear_config_name, gemm_linear_force_config,
+    gemm_linear_num_configs, gemm_linear_select_config, gemm_linear_weight_grad,
+    gemm_linear_weight_grad_workspace_size, gemm_linear_workspace_size, grouped_linear,
+    grouped_linear_grad, linear, linear_grad)
+from .layers import SIGNATURES as _LINEAR_SIGNATURES  # noqa: E402
+
 _lib = None
 
 
@@ -133,7 +144,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     except ImportError:  # pragma: no cover - C callers without torch
         pass
     lib = ctypes.CDLL(path)
-    for name, (res, args) in SIGNATURES.items():
+    for name, (res, args) in [*SIGNATURES.items(), *_LINEAR_SIGNATURES.items()]:
         fn = getattr(lib, name)
         fn.restype = res
         fn.argtypes = args

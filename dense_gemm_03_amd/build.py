@@ -27,12 +27,18 @@ LIB = os.path.join(HERE, "libdense_gemm.so")
 SOURCES = [("gemm_api.hip", "gemm_api", []),
            ("gemm_tables.hip", "gemm_tables", []),
            ("gemm_aux.hip", "gemm_aux", []),
-           ("conv.hip", "conv", [])]
+           ("conv.hip", "conv", []),
+           ("linear_api.hip", "linear_api", []),
+           ("linear_aux.hip", "linear_aux", [])]
 for _dtype in ("F32", "BF16"):
     for _layout in ("NN", "NT", "TN", "TT", "CF", "CW", "CFT", "CWT", "C3F", "C3W", "CFP", "CWP",
                     "C3FP", "C3WP", "CFW", "CWW", "C4F", "C4W", "C4FP", "C4WP"):
         SOURCES.append(("gemm_instances.hip", "gemm_%s_%s" % (_dtype.lower(), _layout.lower()),
                         ["DG_DTYPE_TABLE=DG_%s_TABLE" % _dtype, "DG_LAYOUT=" + _layout]))
+    # the linear layers: w as K x N, as N x K, and the weight gradient
+    for _form in ("N", "T", "W"):
+        SOURCES.append(("linear_instances.hip", "linear_%s_%s" % (_dtype.lower(), _form.lower()),
+                        ["DG_LIN_TABLE=DG_LIN_%s_TABLE" % _dtype, "DG_LIN_FORM=" + _form]))
 
 ARCH = "gfx950"
 HIPCC_FLAGS = [

@@ -790,6 +790,8 @@ int conv_result_buffer(hipStream_t stream, size_t bytes, void **out)
     return get_buffer(4, device, stream, bytes, out);
 }
 
+int device_compute_units() { return compute_units(); }
+
 int implicit_tile(int dtype, int64_t M, int *bn, int *bk, int *threads)
 {
     int count = 0;

@@ -52,4 +52,7 @@ int conv_result_buffer(hipStream_t stream, size_t bytes, void **out);
 // gemm_status (GEMM_ERR_INTERNAL if the entry is missing from the table).
 int implicit_tile(int dtype, int64_t M, int *bn, int *bk, int *threads);
 
+// Compute units of the current device (256, MI355X's count, without one).
+int device_compute_units();
+
 }  // namespace dg

@@ -1,0 +1,200 @@
+// The linear layers' kernel table and the kernels next to the products: the
+// reduce of partial sums, and the gradient through the epilogue (dz, dbias).
+#include "linear_configs.hpp"
+
+namespace dg {
+
+const LinearConfig *linear_configs(int dtype, int *count)
+{
+    static const LinearConfig f32[] = {DG_LIN_F32_TABLE(DG_LIN_ENTRY)};
+    static const LinearConfig bf16[] = {DG_LIN_BF16_TABLE(DG_LIN_ENTRY)};
+    *count = dtype == 0 ? (int)(sizeof(f32) / sizeof(f32[0])) : (int)(sizeof(bf16) / sizeof(bf16[0]));
+    return dtype == 0 ? f32 : bf16;
+}
+
+namespace {
+
+// Group of `row` (lo <= row < hi of exactly one group), or -1 outside all.
+__device__ __forceinline__ int group_of_row(const int32_t *offsets, int groups, int rows, int row)
+{
+    int a = 0, b = groups;   // the last g in [a, b) with offsets[g] <= row
+    if (row < clamp_row(offsets[0], rows) || row >= clamp_row(offsets[groups], rows)) return -1;
+    while (b - a > 1) {
+        const int mid = (a + b) >> 1;
+        if (clamp_row(offsets[mid], rows) <= row)
+            a = mid;
+        else
+            b = mid;
+    }
+    return a;
+}
+
+// One thread finishes pieces of V consecutive columns: the slices' sums in
+// slice order, then the epilogue of the product kernels.
+template <int V, bool WGRAD>
+__global__ void __launch_bounds__(256) linear_reduce_kernel(LinearArgs p)
+{
+    const int pieces = (p.N + V - 1) / V;
+    const int64_t out_rows = WGRAD ? (int64_t)p.groups * p.M : p.rows;
+    const int64_t total = out_rows * pieces, slice = out_rows * p.N;
+    for (int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x; id < total; id += (int64_t)gridDim.x * 256) {
+        const int64_t row = id / pieces;
+        const int col = (int)(id - row * pieces) * V, n = p.N - col;
+        int group = 0;
+        if (WGRAD)
+            group = (int)(row / p.M);
+        else if (p.offsets != nullptr && (group = group_of_row(p.offsets, p.groups, p.rows, (int)row)) < 0)
+            continue;
+        float v[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = 0.0f;
+        const float *w = p.ws + row * p.N + col;
+        if ((p.N & 3) == 0) {
+            for (int z = 0; z < p.splits; ++z, w += slice)
+#pragma unroll
+                for (int h = 0; h < V; h += 4)
+                    if (h < n) {
+                        const u32x4 q = load16(w + h);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) v[h + i] += __uint_as_float(q[i]);
+                    }
+        } else {
+            for (int z = 0; z < p.splits; ++z, w += slice)
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    if (i < n) v[i] += w[i];
+        }
+        float bias[V];
+        load_bias<V>(p.e, group * p.stride_bias + col, n, bias);
+        finish_piece<V>(p.e, WGRAD ? group * p.stride_c : 0, WGRAD ? row - (int64_t)group * p.M : row,
+                        col, n, bias, v);
+    }
+}
+
+// dz = dy act'(pre), and each column's sum over the chunk's rows.  A block
+// takes one chunk of kActGradRows rows of one group and 64 V columns: its four
+// waves walk the rows in turn, a lane holding V columns (16 bytes of a row),
+// so a wave reads 1 KiB of a row at a time and every byte once; the sums meet
+// in LDS.  Bound by HBM: 2 reads and 1 write of rows x N.
+template <bool BF16>
+__global__ void __launch_bounds__(256) act_grad_kernel(ActGradArgs p, int col_blocks)
+{
+    constexpr int V = BF16 ? 8 : 4;
+    __shared__ float sums[4][64 * V];
+    const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
+    const GroupRows list(p.offsets, p.groups, p.rows, kActGradRows, lane);
+    const int tile = (int)blockIdx.x / col_blocks, cb = (int)blockIdx.x - tile * col_blocks;
+    if (tile >= list.total) return;
+    int group, lo, m, tm;
+    list.find(p.offsets, p.groups, p.rows, kActGradRows, lane, tile, group, lo, m, tm);
+    const int col = (cb * 64 + lane) * V, n = p.N - col;
+    const int first = tm * kActGradRows, count = min(kActGradRows, m - first);
+    float s[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) s[i] = 0.0f;
+    if (n > 0) {
+#pragma unroll 4
+        for (int r = wave; r < count; r += 4) {
+            const int64_t row = lo + first + r;
+            float g[V], z[V];
+            load_out<V>(p.dy, row * p.lddy + col, n, BF16, p.vec != 0, g);
+            if (p.act != ACT_NONE) {
+                if (BF16 == (p.pre_bf16 != 0))
+                    load_out<V>(p.pre, row * p.ldp + col, n, BF16, p.vec != 0, z);
+                else   // another type than dy's: element by element
+                    load_out<V>(p.pre, row * p.ldp + col, n, !BF16, false, z);
+                act_slope<V>(p.act, z);
+#pragma unroll
+                for (int i = 0; i < V; ++i) g[i] *= z[i];
+            }
+#pragma unroll
+            for (int i = 0; i < V; ++i) s[i] += i < n ? g[i] : 0.0f;
+            if (p.dz != nullptr) store_outs<V>(p.dz, row * p.lddz + col, n, BF16, p.vec != 0, g);
+        }
+    }
+    if (p.dbias == nullptr) return;
+#pragma unroll
+    for (int i = 0; i < V; ++i) sums[wave][lane * V + i] = s[i];
+    __syncthreads();
+    // one chunk in all (dense, few rows): the sums are the result
+    float *out = p.ws != nullptr ? p.ws + (int64_t)tile * p.N : p.dbias;
+    for (int i = (int)threadIdx.x; i < 64 * V; i += 256) {
+        const int j = cb * 64 * V + i;
+        if (j < p.N) out[j] = sums[0][i] + sums[1][i] + sums[2][i] + sums[3][i];
+    }
+}
+
+// dbias of one group: its chunks' sums in order (none: zero).
+__global__ void __launch_bounds__(256) bias_reduce_kernel(ActGradArgs p, int col_blocks)
+{
+    const int lane = (int)threadIdx.x & 63;
+    const int group = (int)blockIdx.x / col_blocks, cb = (int)blockIdx.x - group * col_blocks;
+    int first = 0, mine = 0;   // the group's first chunk, and its chunks
+    if (p.offsets == nullptr) {
+        mine = (p.rows + kActGradRows - 1) / kActGradRows;
+    } else {
+        for (int base = 0; base <= group; base += 64) {
+            int lo, m;
+            const int t = GroupRows::lane_tiles(p.offsets, base + lane, p.groups, p.rows, kActGradRows, lo, m);
+            const int upto = GroupRows::scan(t, lane);
+            const int at = min(63, group - base);   // the group itself, or the last of these 64
+            first += __builtin_amdgcn_readlane(upto, at);
+            mine = __builtin_amdgcn_readlane(t, at);
+        }
+        first -= mine;
+        // offsets that fall can give rows to several groups, and more chunks
+        // than there is room for
+        first = min(first, p.chunks);
+        mine = min(mine, p.chunks - first);
+    }
+    const int j = cb * 256 + (int)threadIdx.x;
+    if (j >= p.N) return;
+    const float *w = p.ws + (int64_t)first * p.N + j;
+    float s = 0.0f;
+#pragma unroll 8
+    for (int t = 0; t < mine; ++t) s += w[(int64_t)t * p.N];
+    p.dbias[(int64_t)group * p.N + j] = s;
+}
+
+unsigned grid_of(int64_t work)
+{
+    const int64_t blocks = (work + 255) / 256;
+    return (unsigned)(blocks < 1 ? 1 : blocks > 65536 ? 65536 : blocks);   // the loop covers the rest
+}
+
+}  // namespace
+
+hipError_t launch_linear_reduce(const LinearArgs &a, bool weight_grad, hipStream_t stream)
+{
+    const int V = a.e.out_bf16 ? 8 : 4;
+    const int64_t rows = weight_grad ? (int64_t)a.groups * a.M : a.rows;
+    const dim3 grid(grid_of(rows * ((a.N + V - 1) / V)));
+    if (weight_grad)
+        hipLaunchKernelGGL((V == 8 ? linear_reduce_kernel<8, true> : linear_reduce_kernel<4, true>),
+                           grid, dim3(256), 0, stream, a);
+    else
+        hipLaunchKernelGGL((V == 8 ? linear_reduce_kernel<8, false> : linear_reduce_kernel<4, false>),
+                           grid, dim3(256), 0, stream, a);
+    return hipGetLastError();
+}
+
+hipError_t launch_act_grad(const ActGradArgs &a, hipStream_t stream)
+{
+    const int V = a.bf16 ? 8 : 4;
+    const int64_t tiles = a.chunks;
+    const int col_blocks = (a.N + 64 * V - 1) / (64 * V);
+    if (tiles > 0) {
+        hipLaunchKernelGGL((a.bf16 ? act_grad_kernel<true> : act_grad_kernel<false>),
+                           dim3((unsigned)(tiles * col_blocks)), dim3(256), 0, stream, a, col_blocks);
+        const hipError_t err = hipGetLastError();
+        if (err != hipSuccess) return err;
+    }
+    if (a.dbias != nullptr && a.ws != nullptr) {
+        const int cb = (a.N + 255) / 256;
+        hipLaunchKernelGGL(bias_reduce_kernel, dim3((unsigned)(cb * a.groups)), dim3(256), 0, stream, a, cb);
+        return hipGetLastError();
+    }
+    return hipSuccess;
+}
+
+}  // namespace dg

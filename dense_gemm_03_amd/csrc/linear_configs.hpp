@@ -1,0 +1,85 @@
+// Kernel table of the linear layers: one entry per tile shape, with launchers
+// for y = x . w (w as K x N, or as N x K) and for dw = x^T . dz, each for
+// 16-byte aligned rows and for any alignment of the element type.
+//
+//   X(NAME, BF16, BM, BN, BK, WM, WN, STAGES, GROUP_M, FORMS)
+//
+// FORMS = FWD (both forms of x . w), WG (x^T . dz) or ALL.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "linear_kernel.hpp"
+
+namespace dg {
+
+typedef hipError_t (*linear_fn)(const LinearArgs &args, int blocks, hipStream_t stream);
+
+enum { FORM_N = 0, FORM_T = 1, FORM_WGRAD = 2 };
+
+struct LinearConfig {
+    const char *name;
+    int bm, bn, bk, threads, stages, group_m;
+    linear_fn fn[3][2];   // by form; [0] aligned, [1] not; nullptr where there is none
+};
+
+template <bool BF16, int BM, int BN, int BK, int WM, int WN, int STAGES, int LA, int LB, bool ALIGNED>
+hipError_t launch_linear(const LinearArgs &args, int blocks, hipStream_t stream);
+
+#define DG_LIN_LA_N ::dg::KMAJOR
+#define DG_LIN_LB_N ::dg::MNMAJOR
+#define DG_LIN_LA_T ::dg::KMAJOR
+#define DG_LIN_LB_T ::dg::KMAJOR
+#define DG_LIN_LA_W ::dg::MNMAJOR
+#define DG_LIN_LB_W ::dg::MNMAJOR
+
+#define DG_LIN_F32_TABLE(X)                                                  \
+    X("f32_256x256x32_w4x2_s2", false, 256, 256, 32, 4, 2, 2, 8, ALL)        \
+    X("f32_128x128x32_w2x2_s2", false, 128, 128, 32, 2, 2, 2, 8, ALL)        \
+    X("f32_64x64x32_w2x2_s3", false, 64, 64, 32, 2, 2, 3, 8, ALL)            \
+    X("f32_32x128x32_w1x4_s3", false, 32, 128, 32, 1, 4, 3, 1, FWD)
+
+#define DG_LIN_BF16_TABLE(X)                                                 \
+    X("bf16_256x256x64_w4x2_s2", true, 256, 256, 64, 4, 2, 2, 8, FWD)        \
+    X("bf16_256x256x32_w4x2_s4", true, 256, 256, 32, 4, 2, 4, 8, WG)         \
+    X("bf16_128x128x64_w2x2_s2", true, 128, 128, 64, 2, 2, 2, 8, ALL)        \
+    X("bf16_64x64x64_w2x2_s4", true, 64, 64, 64, 2, 2, 4, 8, ALL)            \
+    X("bf16_32x256x64_w1x4_s3", true, 32, 256, 64, 1, 4, 3, 1, FWD)
+
+#define DG_LIN_FNS(BF16, BM, BN, BK, WM, WN, S, F)                                              \
+    {&launch_linear<BF16, BM, BN, BK, WM, WN, S, DG_LIN_LA_##F, DG_LIN_LB_##F, true>,           \
+     &launch_linear<BF16, BM, BN, BK, WM, WN, S, DG_LIN_LA_##F, DG_LIN_LB_##F, false>}
+#define DG_LIN_NOFNS {nullptr, nullptr}
+#define DG_LIN_FNS_ALL(...) \
+    {DG_LIN_FNS(__VA_ARGS__, N), DG_LIN_FNS(__VA_ARGS__, T), DG_LIN_FNS(__VA_ARGS__, W)}
+#define DG_LIN_FNS_FWD(...) {DG_LIN_FNS(__VA_ARGS__, N), DG_LIN_FNS(__VA_ARGS__, T), DG_LIN_NOFNS}
+#define DG_LIN_FNS_WG(...) {DG_LIN_NOFNS, DG_LIN_NOFNS, DG_LIN_FNS(__VA_ARGS__, W)}
+#define DG_LIN_ENTRY(NAME, BF16, BM, BN, BK, WM, WN, S, GM, FORMS)                              \
+    LinearConfig{NAME, BM, BN, BK, 64 * (WM) * (WN), S, GM,                                     \
+                 DG_LIN_FNS_##FORMS(BF16, BM, BN, BK, WM, WN, S)},
+
+const LinearConfig *linear_configs(int dtype, int *count);
+
+// The reduce of `splits` slices of partial sums, in slice order, with the
+// epilogue: y (rows x N; rows outside the groups are left alone) or dw
+// (groups x M x N).
+hipError_t launch_linear_reduce(const LinearArgs &args, bool weight_grad, hipStream_t stream);
+
+// dz and dbias.
+struct ActGradArgs {
+    const void *dy, *pre;
+    void *dz;               // or nullptr
+    float *dbias;           // or nullptr
+    float *ws;              // per row chunk and column: partial sums of dbias
+    const int32_t *offsets;
+    int64_t lddy, ldp, lddz;
+    int rows, N, groups;
+    int act, bf16, pre_bf16;
+    int vec;                // rows of dy, pre and dz are 16-byte aligned
+    int chunks;             // chunks that ws has room for: all that there can be
+};
+// Rows of one chunk of the bias gradient's sum.
+constexpr int kActGradRows = 64;
+hipError_t launch_act_grad(const ActGradArgs &args, hipStream_t stream);
+
+}  // namespace dg

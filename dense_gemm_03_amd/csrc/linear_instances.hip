@@ -1,0 +1,43 @@
+// One slice of the linear-layer kernels: one input type and one form.  The
+// build compiles this file once per slice, with DG_LIN_TABLE set to
+// DG_LIN_F32_TABLE or DG_LIN_BF16_TABLE and DG_LIN_FORM to N, T or W (w as K x
+// N, w as N x K, weight gradient).
+#if !defined(DG_LIN_TABLE) || !defined(DG_LIN_FORM)
+#error "define DG_LIN_TABLE and DG_LIN_FORM"
+#endif
+#include "linear_configs.hpp"
+
+namespace dg {
+
+template <bool BF16, int BM, int BN, int BK, int WM, int WN, int STAGES, int LA, int LB, bool ALIGNED>
+hipError_t launch_linear(const LinearArgs &args, int blocks, hipStream_t stream)
+{
+    hipLaunchKernelGGL((linear_kernel<BF16, BM, BN, BK, WM, WN, STAGES, LA, LB, ALIGNED>),
+                       dim3(blocks), dim3(64 * WM * WN), 0, stream, args);
+    return hipGetLastError();
+}
+
+}  // namespace dg
+
+#define DG_LIN_INST(BF16, BM, BN, BK, WM, WN, S, F)                                              \
+    template hipError_t dg::launch_linear<BF16, BM, BN, BK, WM, WN, S, DG_LIN_LA_##F,            \
+                                          DG_LIN_LB_##F, true>(const dg::LinearArgs &, int,      \
+                                                               hipStream_t);                     \
+    template hipError_t dg::launch_linear<BF16, BM, BN, BK, WM, WN, S, DG_LIN_LA_##F,            \
+                                          DG_LIN_LB_##F, false>(const dg::LinearArgs &, int,     \
+                                                                hipStream_t);
+#define DG_LIN_INST_ALL_N(...) DG_LIN_INST(__VA_ARGS__, N)
+#define DG_LIN_INST_ALL_T(...) DG_LIN_INST(__VA_ARGS__, T)
+#define DG_LIN_INST_ALL_W(...) DG_LIN_INST(__VA_ARGS__, W)
+#define DG_LIN_INST_FWD_N(...) DG_LIN_INST(__VA_ARGS__, N)
+#define DG_LIN_INST_FWD_T(...) DG_LIN_INST(__VA_ARGS__, T)
+#define DG_LIN_INST_FWD_W(...)
+#define DG_LIN_INST_WG_N(...)
+#define DG_LIN_INST_WG_T(...)
+#define DG_LIN_INST_WG_W(...) DG_LIN_INST(__VA_ARGS__, W)
+#define DG_LIN_INST_SEL2(FORMS, F) DG_LIN_INST_##FORMS##_##F
+#define DG_LIN_INST_SEL(FORMS, F) DG_LIN_INST_SEL2(FORMS, F)
+#define DG_LIN_INST_ENTRY(NAME, BF16, BM, BN, BK, WM, WN, S, GM, FORMS) \
+    DG_LIN_INST_SEL(FORMS, DG_LIN_FORM)(BF16, BM, BN, BK, WM, WN, S)
+
+DG_LIN_TABLE(DG_LIN_INST_ENTRY)
