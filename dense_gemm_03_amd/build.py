@@ -29,7 +29,8 @@ SOURCES = [("gemm_api.hip", "gemm_api", []),
            ("gemm_aux.hip", "gemm_aux", []),
            ("conv.hip", "conv", []),
            ("linear_api.hip", "linear_api", []),
-           ("linear_aux.hip", "linear_aux", [])]
+           ("linear_aux.hip", "linear_aux", []),
+           ("linear_rows.hip", "linear_rows", [])]
 for _dtype in ("F32", "BF16"):
     for _layout in ("NN", "NT", "TN", "TT", "CF", "CW", "CFT", "CWT", "C3F", "C3W", "CFP", "CWP",
                     "C3FP", "C3WP", "CFW", "CWW", "C4F", "C4W", "C4FP", "C4WP"):

@@ -58,7 +58,7 @@ int index_of(int dtype, int bm, int bn, int form)
     int count = 0;
     const LinearConfig *tab = linear_configs(dtype, &count);
     for (int i = 0; i < count; ++i)
-        if (tab[i].bm == bm && tab[i].bn == bn && tab[i].fn[form][0] != nullptr) return i;
+        if (tab[i].bm == bm && (bn == 0 || tab[i].bn == bn) && tab[i].fn[form][0] != nullptr) return i;
     return -1;
 }
 
@@ -86,7 +86,14 @@ Plan make_plan(const gemm_linear_params &p, bool wgrad)
         if (pl.cfg < 0) return pl;
     } else {
         const int64_t per = wgrad ? M : grouped ? ceil_div(M, groups) : M;
-        if (!wgrad && per <= 32)
+        if (!wgrad && per <= 16 && !(grouped && per > 8)) {
+            // strips as wide as still give every compute unit a block
+            pl.cfg = index_of(p.dtype, 16, 0, pl.form);
+            for (int i = pl.cfg + 1; i > 0 && i < count; ++i)
+                if (tab[i].bm == 16 && tab[i].fn[pl.form][0] != nullptr &&
+                    row_tiles(16) * ceil_div(N, tab[i].bn) >= (pl.form == FORM_T ? 2 * cus : cus))
+                    pl.cfg = i;
+        } else if (!wgrad && per <= 32)
             pl.cfg = index_of(p.dtype, 32, p.dtype == GEMM_DTYPE_F32 ? 128 : 256, pl.form);
         else if (row_tiles(256) * ceil_div(N, 256) >= cus * 3 / 4 && (wgrad || per >= 192))
             pl.cfg = index_of(p.dtype, 256, 256, pl.form);
@@ -100,6 +107,7 @@ Plan make_plan(const gemm_linear_params &p, bool wgrad)
     pl.tiles_n = ceil_div(N, c.bn);
     pl.tiles_m = wgrad ? ceil_div(M, c.bm)
                        : grouped ? M / c.bm + std::min(groups, M) : ceil_div(M, c.bm);
+    if (c.stages == 0) return pl;
     const int64_t tiles = row_tiles(c.bm) * pl.tiles_n;
     const int64_t ktiles = ceil_div(K, c.bk);
     int64_t s = 1;

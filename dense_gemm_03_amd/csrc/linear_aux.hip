@@ -6,8 +6,8 @@ namespace dg {
 
 const LinearConfig *linear_configs(int dtype, int *count)
 {
-    static const LinearConfig f32[] = {DG_LIN_F32_TABLE(DG_LIN_ENTRY)};
-    static const LinearConfig bf16[] = {DG_LIN_BF16_TABLE(DG_LIN_ENTRY)};
+    static const LinearConfig f32[] = {DG_LIN_F32_TABLE(DG_LIN_ENTRY) DG_LIN_F32_ROWS(DG_LIN_ROWS_ENTRY)};
+    static const LinearConfig bf16[] = {DG_LIN_BF16_TABLE(DG_LIN_ENTRY) DG_LIN_BF16_ROWS(DG_LIN_ROWS_ENTRY)};
     *count = dtype == 0 ? (int)(sizeof(f32) / sizeof(f32[0])) : (int)(sizeof(bf16) / sizeof(bf16[0]));
     return dtype == 0 ? f32 : bf16;
 }

@@ -15,11 +15,14 @@ namespace dg {
 
 typedef hipError_t (*linear_fn)(const LinearArgs &args, int blocks, hipStream_t stream);
 
+template <bool BF16, int FORM, int W, int WV>
+hipError_t launch_few_rows(const LinearArgs &args, int blocks, hipStream_t stream);
+
 enum { FORM_N = 0, FORM_T = 1, FORM_WGRAD = 2 };
 
 struct LinearConfig {
     const char *name;
-    int bm, bn, bk, threads, stages, group_m;
+    int bm, bn, bk, threads, stages, group_m;   // stages == 0: the kernel for few rows
     linear_fn fn[3][2];   // by form; [0] aligned, [1] not; nullptr where there is none
 };
 
@@ -36,15 +39,54 @@ hipError_t launch_linear(const LinearArgs &args, int blocks, hipStream_t stream)
 #define DG_LIN_F32_TABLE(X)                                                  \
     X("f32_256x256x32_w4x2_s2", false, 256, 256, 32, 4, 2, 2, 8, ALL)        \
     X("f32_128x128x32_w2x2_s2", false, 128, 128, 32, 2, 2, 2, 8, ALL)        \
+    X("f32_256x128x32_w4x2_s2", false, 256, 128, 32, 4, 2, 2, 8, ALL)        \
+    X("f32_128x64x32_w2x2_s2", false, 128, 64, 32, 2, 2, 2, 8, ALL)        \
+    X("f32_64x64x32_w2x2_s2", false, 64, 64, 32, 2, 2, 2, 8, ALL)        \
+    X("f32_64x128x32_w2x2_s2", false, 64, 128, 32, 2, 2, 2, 8, ALL)        \
     X("f32_64x64x32_w2x2_s3", false, 64, 64, 32, 2, 2, 3, 8, ALL)            \
     X("f32_32x128x32_w1x4_s3", false, 32, 128, 32, 1, 4, 3, 1, FWD)
 
 #define DG_LIN_BF16_TABLE(X)                                                 \
-    X("bf16_256x256x64_w4x2_s2", true, 256, 256, 64, 4, 2, 2, 8, FWD)        \
-    X("bf16_256x256x32_w4x2_s4", true, 256, 256, 32, 4, 2, 4, 8, WG)         \
+    X("bf16_256x256x64_w2x2_s2", true, 256, 256, 64, 2, 2, 2, 8, ALL)        \
+    X("bf16_256x256x64_w2x4_s2", true, 256, 256, 64, 2, 4, 2, 8, ALL)        \
+    X("bf16_192x256x64_w2x2_s2", true, 192, 256, 64, 2, 2, 2, 8, FWD)        \
+    X("bf16_128x256x64_w2x2_s2", true, 128, 256, 64, 2, 2, 2, 8, ALL)        \
+    X("bf16_128x256x64_w1x4_s2", true, 128, 256, 64, 1, 4, 2, 8, ALL)        \
+    X("bf16_256x128x64_w2x2_s2", true, 256, 128, 64, 2, 2, 2, 8, ALL)        \
     X("bf16_128x128x64_w2x2_s2", true, 128, 128, 64, 2, 2, 2, 8, ALL)        \
+    X("bf16_64x128x64_w1x4_s2", true, 64, 128, 64, 1, 4, 2, 8, ALL)        \
+    X("bf16_64x128x64_w2x2_s2", true, 64, 128, 64, 2, 2, 2, 8, ALL)        \
+    X("bf16_64x64x64_w2x2_s2", true, 64, 64, 64, 2, 2, 2, 8, ALL)            \
     X("bf16_64x64x64_w2x2_s4", true, 64, 64, 64, 2, 2, 4, 8, ALL)            \
+    X("bf16_32x256x64_w1x4_s2", true, 32, 256, 64, 1, 4, 2, 1, FWD)          \
     X("bf16_32x256x64_w1x4_s3", true, 32, 256, 64, 1, 4, 3, 1, FWD)
+
+// Entries for few rows: X(NAME, BF16, FORM (N or T), W, waves); 16 rows, 16 W columns.
+#define DG_LIN_F32_ROWS(X)                       \
+    X("f32_rows_n_w2x8", false, N, 2, 8)         \
+    X("f32_rows_n_w4x8", false, N, 4, 8)         \
+    X("f32_rows_n_w2x16", false, N, 2, 16)       \
+    X("f32_rows_t_w1x16", false, T, 1, 16)       \
+    X("f32_rows_t_w1x8", false, T, 1, 8)         \
+    X("f32_rows_t_w2x8", false, T, 2, 8)
+
+#define DG_LIN_BF16_ROWS(X)                      \
+    X("bf16_rows_n_w2x8", true, N, 2, 8)         \
+    X("bf16_rows_n_w4x8", true, N, 4, 8)         \
+    X("bf16_rows_n_w2x16", true, N, 2, 16)       \
+    X("bf16_rows_t_w1x16", true, T, 1, 16)       \
+    X("bf16_rows_t_w1x8", true, T, 1, 8)         \
+    X("bf16_rows_t_w2x8", true, T, 2, 8)
+
+#define DG_LIN_FORM_ID_N 0
+#define DG_LIN_FORM_ID_T 1
+#define DG_LIN_ROWS_FN(BF16, F, W, WV)                     \
+    {&launch_few_rows<BF16, DG_LIN_FORM_ID_##F, W, WV>,    \
+     &launch_few_rows<BF16, DG_LIN_FORM_ID_##F, W, WV>}
+#define DG_LIN_ROWS_FNS_N(...) {DG_LIN_ROWS_FN(__VA_ARGS__), DG_LIN_NOFNS, DG_LIN_NOFNS}
+#define DG_LIN_ROWS_FNS_T(...) {DG_LIN_NOFNS, DG_LIN_ROWS_FN(__VA_ARGS__), DG_LIN_NOFNS}
+#define DG_LIN_ROWS_ENTRY(NAME, BF16, F, W, WV) \
+    LinearConfig{NAME, 16, 16 * (W), 1, 64 * (WV), 0, 1, DG_LIN_ROWS_FNS_##F(BF16, F, W, WV)},
 
 #define DG_LIN_FNS(BF16, BM, BN, BK, WM, WN, S, F)                                              \
     {&launch_linear<BF16, BM, BN, BK, WM, WN, S, DG_LIN_LA_##F, DG_LIN_LB_##F, true>,           \

@@ -11,7 +11,7 @@
 // an output matrix, and its blocks walk that group's rows only.
 #pragma once
 
-#include "gemm_kernel.hpp"
+#include "mma16.hpp"
 
 namespace dg {
 
@@ -344,28 +344,42 @@ struct FinishTile {
     static constexpr int PER_STAGE = G::STAGE_BYTES / SCRATCH;
     static_assert(PER_STAGE * G::STAGES >= G::NW, "one scratch per wave");
     static_assert(64 % CPR == 0 && 32 % RPI == 0, "whole rows per pass");
-    // the 32-column halves of a row swap places in rows with bit 2 set, so
-    // the two lane halves of a fragment write (rows 4 apart) use other banks
+    // Columns move in groups so that the lanes of a fragment write use other
+    // banks: 32 x 32 fragments (fp32) write rows 4 apart in two lane halves,
+    // 16 x 16 ones (bf16) in four quarters.
     static __device__ __forceinline__ int place(int row, int col)
     {
+        if (G::BF16) return col ^ (((row >> 2) & (G::WTN >= 64 ? 3 : 1)) << 4);
         return G::WTN >= 64 ? col ^ (((row >> 2) & 1) << 5) : col;
     }
-
-    template <class Out>
-    static __device__ __forceinline__ void run(unsigned char *scr, const BlockCtx<G> &c,
-                                               const floatx16 (&acc)[G::FM][G::FN], Out &&out)
+    static __device__ __forceinline__ void put(unsigned char *scr, int row, int col, float v)
     {
-        const int half = c.lane >> 5, l32 = c.lane & 31;
+        *reinterpret_cast<float *>(scr + 4 * (row * G::WTN + place(row, col))) = v;
+    }
+
+    template <class Acc, class Out>
+    static __device__ __forceinline__ void run(unsigned char *scr, const BlockCtx<G> &c, const Acc &acc,
+                                               Out &&out)
+    {
         const int cc = V * (c.lane % CPR), r0 = c.lane / CPR;
-        static_for<0, G::FM>([&](auto fm) {
+        static_for<0, G::WTM / 32>([&](auto fm) {
+            if constexpr (G::BF16) {
 #pragma unroll
-            for (int fn = 0; fn < G::FN; ++fn)
+                for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const int row = 8 * (r >> 2) + 4 * half + (r & 3);
-                    *reinterpret_cast<float *>(scr + 4 * (row * G::WTN + place(row, fn * 32 + l32))) =
-                        acc[fm][fn][r];
-                }
+                    for (int fn = 0; fn < G::FN; ++fn)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            put(scr, 16 * h + 4 * (c.lane >> 4) + r, fn * 16 + (c.lane & 15),
+                                acc[2 * fm + h][fn][r]);
+            } else {
+#pragma unroll
+                for (int fn = 0; fn < G::FN; ++fn)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        put(scr, 8 * (r >> 2) + 4 * (c.lane >> 5) + (r & 3), fn * 32 + (c.lane & 31),
+                            acc[fm][fn][r]);
+            }
             // a wave's LDS accesses complete in order: the reads see the
             // writes above, and the next rows' writes follow these reads
 #pragma unroll 2
@@ -389,8 +403,13 @@ struct FinishTile {
 template <bool BF16, int BM, int BN, int BK, int WM, int WN, int STAGES, int LA, int LB, bool ALIGNED>
 __global__ void __launch_bounds__(64 * WM * WN) linear_kernel(LinearArgs p)
 {
-    using G = Geo<BF16, BM, BN, BK, WM, WN, STAGES, LA, LB>;
+    using G = typename std::conditional<BF16, Geo16<BM, BN, BK, WM, WN, STAGES, LA, LB>,
+                                        Geo<BF16, BM, BN, BK, WM, WN, STAGES, LA, LB>>::type;
     using In = typename G::In;
+    using Sum = typename std::conditional<BF16, floatx4, floatx16>::type;
+    constexpr int SUMS = BF16 ? 4 : 16;
+    constexpr bool PINNED = BF16 && WM * WN == 4 && BK == 64 && STAGES == 2 && ALIGNED;
+    constexpr bool TWO = BF16 && WM * WN == 8 && STAGES == two_groups_stages(BM / WM / 16);
     constexpr bool WGRAD = LA == MNMAJOR;   // groups cut the summed axis
 
     __shared__ __attribute__((aligned(1024))) unsigned char lds0[G::STAGE_BYTES];
@@ -461,13 +480,27 @@ __global__ void __launch_bounds__(64 * WM * WN) linear_kernel(LinearArgs p)
     c.kend = min(K, kbeg + kps);
     const int ntiles = (c.kend - kbeg + BK - 1) / BK;
 
-    floatx16 acc[G::FM][G::FN];
+    Sum acc[G::FM][G::FN];
 #pragma unroll
     for (int fm = 0; fm < G::FM; ++fm)
 #pragma unroll
         for (int fn = 0; fn < G::FN; ++fn)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) acc[fm][fn][r] = 0.0f;
+            for (int r = 0; r < SUMS; ++r) acc[fm][fn][r] = 0.0f;
+    auto direct = [&](auto dw, int nfast, int kbeg) {
+        constexpr int DW = decltype(dw)::value;
+        if constexpr (BF16 && PINNED) {
+            static_assert(DW == 16, "aligned rows");
+            main_loop_pinned<G>(lds0, lds1, c, kbeg, nfast, acc);
+        } else if constexpr (BF16 && TWO) {
+            const bool busy = c.bm + c.wrow * G::WTM < c.M && c.bn + c.wcol * G::WTN < c.N;
+            main_loop_two_groups<G, DW>(lds0, lds1, lds2, c, kbeg, nfast,
+                                        __builtin_amdgcn_readfirstlane(busy), acc);
+        } else if constexpr (BF16)
+            main_loop16_direct<G, DW>(lds0, lds1, lds2, lds3, c, kbeg, nfast, acc);
+        else
+            main_loop_direct<G, decltype(dw)::value>(lds0, lds1, lds2, lds3, c, kbeg, nfast, acc);
+    };
 
     // The main loops and the choice between them are those of the dense
     // product, on the group's rows: whole k-tiles through direct loads of 16
@@ -480,22 +513,24 @@ __global__ void __launch_bounds__(64 * WM * WN) linear_kernel(LinearArgs p)
         const bool pairs_ok =
             !G::BF16 || (((p.lda | p.ldb) & 1) == 0 && (((uintptr_t)c.A | (uintptr_t)c.B) & 3) == 0 &&
                          (G::LA == KMAJOR || (c.M & 1) == 0) && (G::LB == KMAJOR || (c.N & 1) == 0));
-        const bool dw = G::DMA4 && p.direct_ok && pairs_ok && !x4;
+        const bool dw = G::DMA4 && !PINNED && p.direct_ok && pairs_ok && !x4;
         const int nfast = x4 || dw ? (c.kend - kbeg) / BK : 0;
         c.rot = (tm + tn) % 8;
-        if constexpr (G::DMA4) {
+        if constexpr (G::DMA4 && !PINNED) {
             c.a_end = operand_end_bytes<typename G::TA>(p.lda, c.M, K);
             c.b_end = operand_end_bytes<typename G::TB>(p.ldb, c.N, K);
-            if (dw && nfast > 0)
-                main_loop_direct<G, 4>(lds0, lds1, lds2, lds3, c, kbeg, nfast, acc);
+            if (dw && nfast > 0) direct(std::integral_constant<int, 4>(), nfast, kbeg);
         }
         if constexpr (ALIGNED) {
-            if (x4 && nfast > 0)
-                main_loop_direct<G, 16>(lds0, lds1, lds2, lds3, c, kbeg, nfast, acc);
+            if (x4 && nfast > 0) direct(std::integral_constant<int, 16>(), nfast, kbeg);
         }
-        if (ntiles > nfast)
-            main_loop_masked(lds0, lds1, c, kbeg + nfast * BK, ntiles - nfast, acc,
-                             [&](int k0, StageRegs<G> &r) { global_load_masked<ALIGNED>(c, k0, r); });
+        if (ntiles > nfast) {
+            auto load = [&](int k0, StageRegs<G> &r) { global_load_masked<ALIGNED>(c, k0, r); };
+            if constexpr (BF16)
+                main_loop16_masked(lds0, lds1, c, kbeg + nfast * BK, ntiles - nfast, acc, load);
+            else
+                main_loop_masked(lds0, lds1, c, kbeg + nfast * BK, ntiles - nfast, acc, load);
+        }
     }
 
     // Epilogue.  The waves' scratches share the stages: wait until the last
@@ -545,6 +580,222 @@ __global__ void __launch_bounds__(64 * WM * WN) linear_kernel(LinearArgs p)
         finish(std::integral_constant<int, 8>());
     else
         finish(std::integral_constant<int, 4>());
+}
+
+// ---------------------------------------------------------------- few rows --
+
+// y = act(alpha x . w + bias) + residual for groups of few rows (a decoding
+// step): the weights are read once and hardly reused, so what counts is how
+// many bytes of them are in flight.  A block owns 16 rows of one group and a
+// strip of columns over the whole of K; its waves take turns along K, each
+// streaming weights straight into registers (no LDS, no barrier in the loop,
+// the next step's loads in flight under this one's products), and their sums
+// meet in LDS once at the end, where the epilogue follows: one launch, no
+// partial sums in memory.
+//
+// The products are 16 x 16 MFMAs with the 16 rows of x as one operand (rows
+// past the group's last repeat it and are not stored).  Lane (q, c) = (lane /
+// 16, lane % 16) supplies KV values of k (16 bytes), k = kb + KV q + i, of row
+// c of x and of its column of w:
+//   w as N x K: 16 bytes of row n0 + 16 f + c, one load each (W = fragments f);
+//   w as K x N: KV loads of W consecutive columns n0 + W c .. of rows kb + KV q
+//     + i; bf16 pairs up the rows' halves with byte permutes.  MFMA j then has
+//     the columns n0 + W c + j.
+// Loads use the element's alignment, whatever the pitch.
+template <bool BF16, int FORM, int W, int WV>
+struct FewRows {
+    using In = typename std::conditional<BF16, uint16_t, float>::type;
+    static constexpr int KV = 16 / (int)sizeof(In);     // k values per lane and step
+    static constexpr bool T = FORM == 1;                // w as N x K
+    static constexpr int BN = 16 * W;
+    static constexpr int U = T ? 4 : 8 / W;             // steps per pass
+    static constexpr int KP = U * 4 * KV;               // k values per pass of a wave
+    // vectors at the element's alignment
+    typedef In chunk __attribute__((ext_vector_type(16 / sizeof(In)), aligned(sizeof(In))));
+    typedef In piece __attribute__((ext_vector_type(W), aligned(sizeof(In))));
+
+    static constexpr int PD = W * (int)sizeof(In) / 4;  // dwords per piece
+    struct Regs {
+        u32x4 x[U];
+        u32x4 w[T ? U * W : 1];
+        uint32_t v[T ? 1 : U * KV][T ? 1 : PD];
+    };
+
+    const In *xr;      // this lane's row of x
+    const In *w;       // the group's weights
+    int64_t ldw;
+    int q, c, n0, N, K;
+
+    static __device__ __forceinline__ u32x4 load_chunk(const In *p)
+    {
+        return __builtin_bit_cast(u32x4, *reinterpret_cast<const chunk *>(p));
+    }
+    // Elements e0 .. of a row, zero from `end` on.
+    static __device__ __forceinline__ u32x4 load_masked(const In *row, int e0, int end)
+    {
+        if (e0 + KV <= end) return load_chunk(row + e0);
+        union {
+            u32x4 v;
+            In e[KV];
+        } u;
+#pragma unroll
+        for (int i = 0; i < KV; ++i) u.e[i] = e0 + i < end ? row[e0 + i] : In(0);
+        return u.v;
+    }
+
+    // First of this lane's columns (w as K x N): the last pieces of a strip
+    // that N ends in move back to end with it, and repeat columns.
+    __device__ __forceinline__ int first_col() const { return min(n0 + W * c, max(N - W, 0)); }
+
+    // One pass.  TAIL: K may end in it.  NARROW (w as K x N): N < W.
+    template <bool TAIL, bool NARROW>
+    __device__ __forceinline__ void load(int pass, Regs &r) const
+    {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int k = pass * KP + (u * 4 + q) * KV;
+            r.x[u] = TAIL ? load_masked(xr, k, K) : load_chunk(xr + k);
+            if constexpr (T) {
+#pragma unroll
+                for (int f = 0; f < W; ++f) {
+                    const In *row = w + (int64_t)min(n0 + 16 * f + c, N - 1) * ldw;
+                    r.w[u * W + f] = TAIL ? load_masked(row, k, K) : load_chunk(row + k);
+                }
+            } else {
+                const int col = first_col();
+#pragma unroll
+                for (int i = 0; i < KV; ++i) {
+                    const In *row = w + (int64_t)(TAIL ? min(k + i, K - 1) : k + i) * ldw;
+                    union {
+                        piece v;
+                        In e[W];
+                        uint32_t d[PD];
+                    } t;
+                    if constexpr (NARROW) {
+#pragma unroll
+                        for (int j = 0; j < W; ++j) t.e[j] = row[min(col + j, N - 1)];
+                    } else {
+                        t.v = *reinterpret_cast<const piece *>(row + col);
+                    }
+#pragma unroll
+                    for (int d = 0; d < PD; ++d) r.v[u * KV + i][d] = !TAIL || k + i < K ? t.d[d] : 0u;
+                }
+            }
+        }
+    }
+
+    static __device__ __forceinline__ void mma(u32x4 a, u32x4 b, floatx4 &acc)
+    {
+        if constexpr (BF16) {
+            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
+                                                          __builtin_bit_cast(bf16x8, b), acc, 0, 0, 0);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                acc = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a[i]), __uint_as_float(b[i]),
+                                                           acc, 0, 0, 0);
+        }
+    }
+
+    __device__ __forceinline__ void compute(const Regs &r, floatx4 (&acc)[W]) const
+    {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int j = 0; j < W; ++j) {
+                u32x4 b;
+                if constexpr (T) {
+                    b = r.w[u * W + j];
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if constexpr (BF16)   // column j of two rows of k
+                            b[i] = __builtin_amdgcn_perm(r.v[u * KV + 2 * i + 1][j / 2], r.v[u * KV + 2 * i][j / 2],
+                                                         j & 1 ? 0x07060302u : 0x05040100u);
+                        else
+                            b[i] = r.v[u * KV + i][j];
+                    }
+                }
+                mma(r.x[u], b, acc[j]);
+            }
+    }
+
+    // This wave's passes: `wave`, `wave` + WV, ..; the last, cut one is
+    // whoever's turn it is.
+    template <bool NARROW>
+    __device__ __forceinline__ void run(int wave, floatx4 (&acc)[W]) const
+    {
+        const int whole = K / KP;
+        Regs cur, nxt;
+        int pass = wave;
+        if (pass < whole) load<false, NARROW>(pass, cur);
+        for (; pass < whole; pass += WV) {
+            if (pass + WV < whole) load<false, NARROW>(pass + WV, nxt);
+            compute(cur, acc);
+            cur = nxt;
+        }
+        if (pass == whole && whole * KP < K) {
+            load<true, NARROW>(whole, cur);
+            compute(cur, acc);
+        }
+    }
+};
+
+template <bool BF16, int FORM, int W, int WV>
+__global__ void __launch_bounds__(64 * WV) few_rows_kernel(LinearArgs p)
+{
+    using F = FewRows<BF16, FORM, W, WV>;
+    using In = typename F::In;
+    constexpr int BM = 16, BN = F::BN;
+    __shared__ float sums[WV][BM * BN];
+
+    const int lane = (int)threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const GroupRows list(p.offsets, p.groups, p.rows, BM, lane);
+    // a group's row tiles next to one another: the second finds the weights in L2
+    const int at = xcd_place(list.total * p.tiles_n);
+    if (at < 0) return;
+    const int tn = at / list.total;
+    int group, lo, m, tm;
+    list.find(p.offsets, p.groups, p.rows, BM, lane, at - tn * list.total, group, lo, m, tm);
+    const int row0 = lo + tm * BM, count = min(BM, m - tm * BM);
+
+    F f;
+    f.q = lane >> 4;
+    f.c = lane & 15;
+    f.n0 = tn * BN;
+    f.N = p.N;
+    f.K = p.K;
+    f.ldw = p.ldb;
+    f.w = static_cast<const In *>(p.B) + group * p.stride_b;
+    f.xr = static_cast<const In *>(p.A) + (int64_t)(row0 + min(f.c, count - 1)) * p.lda;
+
+    floatx4 acc[W];
+#pragma unroll
+    for (int j = 0; j < W; ++j) acc[j] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (F::T || p.N >= W)
+        f.template run<false>(wave, acc);
+    else
+        f.template run<true>(wave, acc);
+
+    // sum r of a 16 x 16 fragment is row 4 q + r, column c
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+        const int col = F::T ? 16 * j + f.c : f.first_col() - f.n0 + j;
+        if (F::T || col >= 0)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) sums[wave][(4 * f.q + r) * BN + col] = acc[j][r];
+    }
+    __syncthreads();
+    for (int id = (int)threadIdx.x; id < count * BN; id += 64 * WV) {
+        const int row = id / BN, col = f.n0 + id % BN;
+        if (col >= p.N) continue;
+        float v[1] = {0.0f}, bias[1];
+#pragma unroll
+        for (int z = 0; z < WV; ++z) v[0] += sums[z][id];
+        load_bias<1>(p.e, group * p.stride_bias + col, 1, bias);
+        finish_piece<1>(p.e, 0, row0 + row, col, 1, bias, v);
+    }
 }
 
 }  // namespace dg
