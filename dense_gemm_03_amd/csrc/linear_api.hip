@@ -133,26 +133,32 @@ int launch_plan(const Plan &pl, int dtype, LinearArgs &a, bool wgrad, void *work
 {
     int count = 0;
     const LinearConfig &c = linear_configs(dtype, &count)[pl.cfg];
-    const bool a16 = aligned16(a.A, a.lda, 0, dtype);
-    const bool b16 = aligned16(a.B, a.ldb, a.stride_b, dtype);
+    const bool x16 = aligned16(a.x, a.ldx, 0, dtype);
+    const bool w16 = aligned16(a.w, a.ldw, a.stride_w, dtype);
     const int vec = 16 / size_of(dtype);
     // outer-contiguous rows are read in whole 16-byte chunks past the edge:
     // inside the row's pitch, or on the page of the row's last element
-    a.m_load = wgrad && a16 ? (int)(ceil_div(a.M, vec) * vec) : a.M;
-    a.n_load = pl.form != FORM_T && b16 ? (int)(ceil_div(a.N, vec) * vec) : a.N;
+    a.m_load = wgrad && x16 ? (int)(ceil_div(a.M, vec) * vec) : a.M;
+    a.n_load = pl.form != FORM_T && w16 ? (int)(ceil_div(a.N, vec) * vec) : a.N;
     const int64_t es = size_of(dtype);
-    const int64_t a_rows = wgrad ? c.bk : c.bm, b_rows = pl.form == FORM_T ? c.bn : c.bk;
-    a.direct_ok = a_rows * a.lda * es < (int64_t(1) << 32) && b_rows * a.ldb * es < (int64_t(1) << 32);
+    const int64_t x_rows = wgrad ? c.bk : c.bm, w_rows = pl.form == FORM_T ? c.bn : c.bk;
+    a.direct_ok = x_rows * a.ldx * es < (int64_t(1) << 32) && w_rows * a.ldw * es < (int64_t(1) << 32);
     a.tiles_n = (int)pl.tiles_n;
     a.tiles_m = (int)pl.tiles_m;
     a.splits = pl.splits;
     a.group_m = c.group_m;
     a.k_per_split = (int)(ceil_div(ceil_div(a.K, c.bk), pl.splits) * c.bk);
     a.ws = pl.splits > 1 ? static_cast<float *>(workspace) : nullptr;
-    const int64_t tiles = pl.tiles_m * pl.tiles_n * (wgrad ? a.groups : 1);
-    if (tiles * pl.splits > INT32_MAX - 8) return GEMM_ERR_INVALID_ARG;
-    const int64_t blocks = ceil_div(tiles * pl.splits, 8) * 8;   // xcd_place
-    if (c.fn[pl.form][a16 && b16 ? 0 : 1](a, (int)blocks, stream) != hipSuccess) return GEMM_ERR_HIP;
+    // Blocks per XCD, for all eight: the tiles (or, grouped, the most there can
+    // be), rounded up for either list, and room for the pieces of a last round
+    // (xcd_piece): at most 3/2 of the slots more.
+    const int64_t tiles = pl.tiles_m * pl.tiles_n;
+    a.slots = c.bm == 256 && c.bn == 256 && dtype == GEMM_DTYPE_BF16 ? device_compute_units() / 8 : 0;
+    const int64_t per = (wgrad ? ceil_div(tiles, 8) * a.groups * pl.splits : tiles * pl.splits / 8 + 2) +
+                        ceil_div(a.slots * 3, 2);
+    if (per > INT32_MAX / 8) return GEMM_ERR_INVALID_ARG;
+    const int64_t blocks = per * 8;
+    if (c.fn[pl.form][x16 && w16 ? 0 : 1](a, (int)blocks, stream) != hipSuccess) return GEMM_ERR_HIP;
     if (pl.splits > 1 && launch_linear_reduce(a, wgrad, stream) != hipSuccess) return GEMM_ERR_HIP;
     return GEMM_OK;
 }
@@ -207,12 +213,12 @@ int linear(const gemm_linear_params *p, const void *x, const void *w, const int3
     if (empty) return GEMM_OK;
     if (const int rc = need_device()) return rc;
     LinearArgs a{};
-    a.A = x;
-    a.B = w;
+    a.x = x;
+    a.w = w;
     a.offsets = p->groups > 0 ? offsets : nullptr;
-    a.lda = p->ldx;
-    a.ldb = p->ldw;
-    a.stride_b = p->groups > 0 ? p->stride_w : 0;
+    a.ldx = p->ldx;
+    a.ldw = p->ldw;
+    a.stride_w = p->groups > 0 ? p->stride_w : 0;
     a.stride_bias = p->groups > 0 ? p->stride_bias : 0;
     a.rows = a.M = (int)p->rows;
     a.N = (int)p->N;
@@ -288,10 +294,10 @@ int weight_grad(const gemm_linear_params *p, const void *x, const void *dz, int6
     if (const int rc = need_device()) return rc;
     const bool t = p->transw == GEMM_OP_T;   // dw^T = dz^T . x
     LinearArgs a{};
-    a.A = t ? dz : x;
-    a.B = t ? x : dz;
-    a.lda = t ? lddz : p->ldx;
-    a.ldb = t ? p->ldx : lddz;
+    a.x = t ? dz : x;
+    a.w = t ? x : dz;
+    a.ldx = t ? lddz : p->ldx;
+    a.ldw = t ? p->ldx : lddz;
     a.offsets = p->groups > 0 ? offsets : nullptr;
     a.stride_c = p->groups > 0 ? p->stride_w : 0;
     a.rows = (int)q.rows;

@@ -49,20 +49,22 @@ __global__ void __launch_bounds__(256) linear_reduce_kernel(LinearArgs p)
 #pragma unroll
         for (int i = 0; i < V; ++i) v[i] = 0.0f;
         const float *w = p.ws + row * p.N + col;
-        if ((p.N & 3) == 0) {
-            for (int z = 0; z < p.splits; ++z, w += slice)
+        if (V > 1 && (p.N & 3) == 0) {
+#pragma unroll 4
+            for (int z = 0; z < p.splits; ++z)
 #pragma unroll
                 for (int h = 0; h < V; h += 4)
                     if (h < n) {
-                        const u32x4 q = load16(w + h);
+                        const u32x4 q = load16(w + z * slice + h);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) v[h + i] += __uint_as_float(q[i]);
+                        for (int i = 0; i < 4; ++i) v[(h + i) & (V - 1)] += __uint_as_float(q[i]);
                     }
         } else {
-            for (int z = 0; z < p.splits; ++z, w += slice)
+#pragma unroll 4
+            for (int z = 0; z < p.splits; ++z)
 #pragma unroll
                 for (int i = 0; i < V; ++i)
-                    if (i < n) v[i] += w[i];
+                    if (i < n) v[i] += w[z * slice + i];
         }
         float bias[V];
         load_bias<V>(p.e, group * p.stride_bias + col, n, bias);
@@ -86,7 +88,7 @@ __global__ void __launch_bounds__(256) act_grad_kernel(ActGradArgs p, int col_bl
     const int tile = (int)blockIdx.x / col_blocks, cb = (int)blockIdx.x - tile * col_blocks;
     if (tile >= list.total) return;
     int group, lo, m, tm;
-    list.find(p.offsets, p.groups, p.rows, kActGradRows, lane, tile, group, lo, m, tm);
+    list.find(p.offsets, p.groups, p.rows, kActGradRows, lane, 0, false, tile, group, lo, m, tm);
     const int col = (cb * 64 + lane) * V, n = p.N - col;
     const int first = tm * kActGradRows, count = min(kActGradRows, m - first);
     float s[V];
@@ -135,7 +137,8 @@ __global__ void __launch_bounds__(256) bias_reduce_kernel(ActGradArgs p, int col
     } else {
         for (int base = 0; base <= group; base += 64) {
             int lo, m;
-            const int t = GroupRows::lane_tiles(p.offsets, base + lane, p.groups, p.rows, kActGradRows, lo, m);
+            const int t = GroupRows::lane_tiles(p.offsets, base + lane, p.groups, p.rows, kActGradRows, 0, false,
+                                                 lo, m);
             const int upto = GroupRows::scan(t, lane);
             const int at = min(63, group - base);   // the group itself, or the last of these 64
             first += __builtin_amdgcn_readlane(upto, at);
@@ -166,15 +169,19 @@ unsigned grid_of(int64_t work)
 
 hipError_t launch_linear_reduce(const LinearArgs &a, bool weight_grad, hipStream_t stream)
 {
-    const int V = a.e.out_bf16 ? 8 : 4;
     const int64_t rows = weight_grad ? (int64_t)a.groups * a.M : a.rows;
+    // 16 bytes of output per thread; fewer where that leaves most of the chip
+    // without a thread (48 x 4096, 8 slices: 6.0 us with 8 values, see below)
+    const int64_t all = rows * a.N;
+    const int V = all <= 65536 ? 1 : a.e.out_bf16 && all > (1 << 21) ? 8 : 4;
     const dim3 grid(grid_of(rows * ((a.N + V - 1) / V)));
-    if (weight_grad)
-        hipLaunchKernelGGL((V == 8 ? linear_reduce_kernel<8, true> : linear_reduce_kernel<4, true>),
-                           grid, dim3(256), 0, stream, a);
-    else
-        hipLaunchKernelGGL((V == 8 ? linear_reduce_kernel<8, false> : linear_reduce_kernel<4, false>),
-                           grid, dim3(256), 0, stream, a);
+    auto kernel = weight_grad ? (V == 8   ? linear_reduce_kernel<8, true>
+                                 : V == 4 ? linear_reduce_kernel<4, true>
+                                          : linear_reduce_kernel<1, true>)
+                              : (V == 8   ? linear_reduce_kernel<8, false>
+                                 : V == 4 ? linear_reduce_kernel<4, false>
+                                          : linear_reduce_kernel<1, false>);
+    hipLaunchKernelGGL(kernel, grid, dim3(256), 0, stream, a);
     return hipGetLastError();
 }
 

@@ -26,15 +26,16 @@ struct LinearConfig {
     linear_fn fn[3][2];   // by form; [0] aligned, [1] not; nullptr where there is none
 };
 
-template <bool BF16, int BM, int BN, int BK, int WM, int WN, int STAGES, int LA, int LB, bool ALIGNED>
+template <bool BF16, int BM, int BN, int BK, int WM, int WN, int STAGES, int LX, int LW, bool ALIGNED>
 hipError_t launch_linear(const LinearArgs &args, int blocks, hipStream_t stream);
 
-#define DG_LIN_LA_N ::dg::KMAJOR
-#define DG_LIN_LB_N ::dg::MNMAJOR
-#define DG_LIN_LA_T ::dg::KMAJOR
-#define DG_LIN_LB_T ::dg::KMAJOR
-#define DG_LIN_LA_W ::dg::MNMAJOR
-#define DG_LIN_LB_W ::dg::MNMAJOR
+// how x and w (dz) lie in memory
+#define DG_LIN_LX_N ::dg::KMAJOR
+#define DG_LIN_LW_N ::dg::MNMAJOR
+#define DG_LIN_LX_T ::dg::KMAJOR
+#define DG_LIN_LW_T ::dg::KMAJOR
+#define DG_LIN_LX_W ::dg::MNMAJOR
+#define DG_LIN_LW_W ::dg::MNMAJOR
 
 #define DG_LIN_F32_TABLE(X)                                                  \
     X("f32_256x256x32_w4x2_s2", false, 256, 256, 32, 4, 2, 2, 8, ALL)        \
@@ -48,18 +49,11 @@ hipError_t launch_linear(const LinearArgs &args, int blocks, hipStream_t stream)
 
 #define DG_LIN_BF16_TABLE(X)                                                 \
     X("bf16_256x256x64_w2x2_s2", true, 256, 256, 64, 2, 2, 2, 8, ALL)        \
-    X("bf16_256x256x64_w2x4_s2", true, 256, 256, 64, 2, 4, 2, 8, ALL)        \
-    X("bf16_192x256x64_w2x2_s2", true, 192, 256, 64, 2, 2, 2, 8, FWD)        \
-    X("bf16_128x256x64_w2x2_s2", true, 128, 256, 64, 2, 2, 2, 8, ALL)        \
-    X("bf16_128x256x64_w1x4_s2", true, 128, 256, 64, 1, 4, 2, 8, ALL)        \
-    X("bf16_256x128x64_w2x2_s2", true, 256, 128, 64, 2, 2, 2, 8, ALL)        \
     X("bf16_128x128x64_w2x2_s2", true, 128, 128, 64, 2, 2, 2, 8, ALL)        \
     X("bf16_64x128x64_w1x4_s2", true, 64, 128, 64, 1, 4, 2, 8, ALL)        \
-    X("bf16_64x128x64_w2x2_s2", true, 64, 128, 64, 2, 2, 2, 8, ALL)        \
     X("bf16_64x64x64_w2x2_s2", true, 64, 64, 64, 2, 2, 2, 8, ALL)            \
-    X("bf16_64x64x64_w2x2_s4", true, 64, 64, 64, 2, 2, 4, 8, ALL)            \
     X("bf16_32x256x64_w1x4_s2", true, 32, 256, 64, 1, 4, 2, 1, FWD)          \
-    X("bf16_32x256x64_w1x4_s3", true, 32, 256, 64, 1, 4, 3, 1, FWD)
+    X("bf16_32x128x64_w1x4_s2", true, 32, 128, 64, 1, 4, 2, 1, FWD)
 
 // Entries for few rows: X(NAME, BF16, FORM (N or T), W, waves); 16 rows, 16 W columns.
 #define DG_LIN_F32_ROWS(X)                       \
@@ -89,8 +83,8 @@ hipError_t launch_linear(const LinearArgs &args, int blocks, hipStream_t stream)
     LinearConfig{NAME, 16, 16 * (W), 1, 64 * (WV), 0, 1, DG_LIN_ROWS_FNS_##F(BF16, F, W, WV)},
 
 #define DG_LIN_FNS(BF16, BM, BN, BK, WM, WN, S, F)                                              \
-    {&launch_linear<BF16, BM, BN, BK, WM, WN, S, DG_LIN_LA_##F, DG_LIN_LB_##F, true>,           \
-     &launch_linear<BF16, BM, BN, BK, WM, WN, S, DG_LIN_LA_##F, DG_LIN_LB_##F, false>}
+    {&launch_linear<BF16, BM, BN, BK, WM, WN, S, DG_LIN_LX_##F, DG_LIN_LW_##F, true>,           \
+     &launch_linear<BF16, BM, BN, BK, WM, WN, S, DG_LIN_LX_##F, DG_LIN_LW_##F, false>}
 #define DG_LIN_NOFNS {nullptr, nullptr}
 #define DG_LIN_FNS_ALL(...) \
     {DG_LIN_FNS(__VA_ARGS__, N), DG_LIN_FNS(__VA_ARGS__, T), DG_LIN_FNS(__VA_ARGS__, W)}

@@ -9,10 +9,10 @@
 
 namespace dg {
 
-template <bool BF16, int BM, int BN, int BK, int WM, int WN, int STAGES, int LA, int LB, bool ALIGNED>
+template <bool BF16, int BM, int BN, int BK, int WM, int WN, int STAGES, int LX, int LW, bool ALIGNED>
 hipError_t launch_linear(const LinearArgs &args, int blocks, hipStream_t stream)
 {
-    hipLaunchKernelGGL((linear_kernel<BF16, BM, BN, BK, WM, WN, STAGES, LA, LB, ALIGNED>),
+    hipLaunchKernelGGL((linear_kernel<BF16, BM, BN, BK, WM, WN, STAGES, LX, LW, ALIGNED>),
                        dim3(blocks), dim3(64 * WM * WN), 0, stream, args);
     return hipGetLastError();
 }
@@ -20,11 +20,11 @@ hipError_t launch_linear(const LinearArgs &args, int blocks, hipStream_t stream)
 }  // namespace dg
 
 #define DG_LIN_INST(BF16, BM, BN, BK, WM, WN, S, F)                                              \
-    template hipError_t dg::launch_linear<BF16, BM, BN, BK, WM, WN, S, DG_LIN_LA_##F,            \
-                                          DG_LIN_LB_##F, true>(const dg::LinearArgs &, int,      \
+    template hipError_t dg::launch_linear<BF16, BM, BN, BK, WM, WN, S, DG_LIN_LX_##F,            \
+                                          DG_LIN_LW_##F, true>(const dg::LinearArgs &, int,      \
                                                                hipStream_t);                     \
-    template hipError_t dg::launch_linear<BF16, BM, BN, BK, WM, WN, S, DG_LIN_LA_##F,            \
-                                          DG_LIN_LB_##F, false>(const dg::LinearArgs &, int,     \
+    template hipError_t dg::launch_linear<BF16, BM, BN, BK, WM, WN, S, DG_LIN_LX_##F,            \
+                                          DG_LIN_LW_##F, false>(const dg::LinearArgs &, int,     \
                                                                 hipStream_t);
 #define DG_LIN_INST_ALL_N(...) DG_LIN_INST(__VA_ARGS__, N)
 #define DG_LIN_INST_ALL_T(...) DG_LIN_INST(__VA_ARGS__, T)

@@ -1,8 +1,8 @@
 // Device code of the linear layers: the tiled product of gemm_kernel.hpp with
 // row groups and an epilogue of its own.
 //
-//     y = act(alpha x . w + bias) + beta_c residual        (LA == KMAJOR)
-//     dw = alpha x^T . dz + beta dw                        (LA == MNMAJOR)
+//     y = act(alpha x . w + bias) + residual               (x k-contiguous)
+//     dw = alpha x^T . dz + beta dw                        (x outer-contiguous)
 //
 // In the first form the groups cut the rows of the output: a group's rows are
 // covered by tiles of BM rows of their own, so a tile never mixes two weight
@@ -31,23 +31,24 @@ struct EpilogueArgs {
 };
 
 struct LinearArgs {
-    const void *A, *B;      // x and w, or x^T and dz (or dz^T and x)
+    const void *x, *w;      // x and w; of the second form, x and dz (or, for dw^T, dz and x)
     const int32_t *offsets; // nullptr: one group of all rows
     float *ws;              // partial sums of `splits` > 1 slices
     EpilogueArgs e;
-    int64_t lda, ldb;
-    int64_t stride_b;       // elements between the groups' w (first form)
+    int64_t ldx, ldw;
+    int64_t stride_w;       // elements between the groups' w (first form)
     int64_t stride_c;       // elements between the groups' dw (second form)
     int64_t stride_bias;
     int rows;               // rows of x: M of the first form, K of the second
     int M, N, K;            // extents of one group's product; the first form's M and the
                             // second's K are replaced by the group's row count
-    int m_load, n_load;     // as KernelArgs
+    int m_load, n_load;     // outer extents that the loads may read, as KernelArgs
     int groups;             // at least 1
     int tiles_m, tiles_n;   // tiles_m: second form only
     int splits, k_per_split;
     int group_m;
     int direct_ok;
+    int slots;              // compute units per XCD (for entries of one block per unit)
 };
 
 // ------------------------------------------------------------- activations --
@@ -65,28 +66,42 @@ __device__ __forceinline__ float sigmoid(float x)
 constexpr float kGeluA = 1.5957691216057308f;
 constexpr float kGeluB = 1.5957691216057308f * 0.044715f;
 
-// act(z) of V values, the activation chosen once for all of them.
+// Phi(z), the normal distribution function, and e = exp(-z^2 / 2) with it:
+// Phi(-|z|) = erfc(|x|) / 2, x = z / sqrt(2), by Hastings' rational form
+// (Abramowitz and Stegun 7.1.26): erfc(x) = (a1 t + .. + a5 t^5) exp(-x^2), t =
+// 1 / (1 + p x), off by at most 1.5e-7; a third of the instructions of erff.
+__device__ __forceinline__ float normal_cdf(float z, float &e)
+{
+    const float x = fabsf(z) * 0.70710678f;
+    const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.3275911f, x, 1.0f));
+    e = __builtin_amdgcn_exp2f(-1.44269504f * x * x);
+    float s = __builtin_fmaf(t, 1.061405429f, -1.453152027f);
+    s = __builtin_fmaf(t, s, 1.421413741f);
+    s = __builtin_fmaf(t, s, -0.284496736f);
+    s = __builtin_fmaf(t, s, 0.254829592f);
+    const float tail = 0.5f * s * t * e;
+    return z > 0.0f ? 1.0f - tail : tail;
+}
+
+// act(z) of V values, the activation chosen once for all of them.  Both forms
+// with a sigmoid are z sigmoid(z (a + b z^2)); a NaN stays a NaN.
 template <int V>
 __device__ __forceinline__ void act_apply(int act, float (&v)[V])
 {
-    switch (act) {
-    case ACT_RELU:
+    if (act == ACT_NONE) return;
+    if (act == ACT_RELU) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = v[i] <= 0.0f ? 0.0f : v[i];   // a NaN stays
-        break;
-    case ACT_GELU:
+        for (int i = 0; i < V; ++i) v[i] = v[i] <= 0.0f ? 0.0f : v[i];
+    } else if (act == ACT_GELU) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = 0.5f * v[i] * (1.0f + erff(0.70710678118654752f * v[i]));
-        break;
-    case ACT_GELU_TANH:
+        for (int i = 0; i < V; ++i) {
+            float e;
+            v[i] *= normal_cdf(v[i], e);
+        }
+    } else {
+        const float a = act == ACT_SILU ? 1.0f : kGeluA, b = act == ACT_SILU ? 0.0f : kGeluB;
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[i] *= sigmoid(v[i] * (kGeluA + kGeluB * v[i] * v[i]));
-        break;
-    case ACT_SILU:
-#pragma unroll
-        for (int i = 0; i < V; ++i) v[i] *= sigmoid(v[i]);
-        break;
-    default: break;
+        for (int i = 0; i < V; ++i) v[i] *= sigmoid(v[i] * __builtin_fmaf(b * v[i], v[i], a));
     }
 }
 
@@ -97,39 +112,25 @@ template <int V>
 __device__ __forceinline__ void act_slope(int act, float (&v)[V])
 {
     auto bounded = [](float z) { return z > 100.0f ? 100.0f : z < -100.0f ? -100.0f : z; };
-    switch (act) {
-    case ACT_RELU:
+    if (act == ACT_RELU) {
 #pragma unroll
         for (int i = 0; i < V; ++i) v[i] = v[i] > 0.0f ? 1.0f : v[i] <= 0.0f ? 0.0f : v[i];
-        break;
-    case ACT_GELU:   // Phi(z) + z phi(z)
+    } else if (act == ACT_GELU) {   // Phi(z) + z phi(z)
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const float z = bounded(v[i]);
-            v[i] = 0.5f * (1.0f + erff(0.70710678118654752f * z)) +
-                   z * 0.39894228040143268f * __builtin_amdgcn_exp2f(-0.72134752f * z * z);
+            float e;
+            const float cdf = normal_cdf(z, e);
+            v[i] = cdf + z * 0.39894228f * e;
         }
-        break;
-    case ACT_GELU_TANH:   // q + z q (1 - q) u',  q = sigmoid(u)
+    } else {                        // q + z q (1 - q) u',  q = sigmoid(u), u = z (a + b z^2)
+        const float a = act == ACT_SILU ? 1.0f : kGeluA, b = act == ACT_SILU ? 0.0f : kGeluB;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const float z = bounded(v[i]);
-            const float q = sigmoid(z * (kGeluA + kGeluB * z * z));
-            v[i] = q + z * q * (1.0f - q) * (kGeluA + 3.0f * kGeluB * z * z);
+            const float z = bounded(v[i]), bz = b * z;
+            const float q = sigmoid(z * __builtin_fmaf(bz, z, a));
+            v[i] = __builtin_fmaf(z * q * (1.0f - q), __builtin_fmaf(3.0f * bz, z, a), q);
         }
-        break;
-    case ACT_SILU:   // q (1 + z (1 - q)),  q = sigmoid(z)
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const float z = bounded(v[i]);
-            const float q = sigmoid(z);
-            v[i] = q * (1.0f + z * (1.0f - q));
-        }
-        break;
-    default:
-#pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = 1.0f;
-        break;
     }
 }
 
@@ -152,17 +153,22 @@ __device__ __forceinline__ void group_span(const int32_t *offsets, int g, int ro
 
 // The list of row tiles of `bm` rows over all groups, from the offsets: each
 // wave forms it for itself, 64 groups at a time (one per lane, a scan across
-// the lanes), so no launch before this one and no memory is needed.
+// the lanes), so no launch before this one and no memory is needed.  With
+// `half` > 0 a group's last tile of at most that many rows is small, and the
+// small tiles form a list of their own behind the others.
 struct GroupRows {
-    int total;   // tiles of all groups
+    int total, small;   // tiles of all groups: all but the small ones, the small ones
 
     __device__ __forceinline__ static int lane_tiles(const int32_t *offsets, int g, int groups,
-                                                     int rows, int bm, int &lo, int &m)
+                                                     int rows, int bm, int half, bool want_small,
+                                                     int &lo, int &m)
     {
         lo = 0;
         m = 0;
         if (g < groups) group_span(offsets, g, rows, lo, m);
-        return (m + bm - 1) / bm;
+        const int rest = m % bm;
+        const bool is_small = rest > 0 && rest <= half;
+        return want_small ? (is_small ? 1 : 0) : m / bm + (rest > half ? 1 : 0);
     }
     __device__ __forceinline__ static int scan(int v, int lane)
     {
@@ -173,32 +179,39 @@ struct GroupRows {
         }
         return v;
     }
-    __device__ __forceinline__ GroupRows(const int32_t *offsets, int groups, int rows, int bm, int lane)
+    __device__ __forceinline__ GroupRows(const int32_t *offsets, int groups, int rows, int bm, int lane,
+                                         int half = 0)
     {
-        total = 0;
+        total = small = 0;
         if (offsets == nullptr) {
-            total = (rows + bm - 1) / bm;
+            const int rest = rows % bm;
+            small = rest > 0 && rest <= half ? 1 : 0;
+            total = rows / bm + (rest > half ? 1 : 0);
             return;
         }
         for (int base = 0; base < groups; base += 64) {
             int lo, m;
-            const int t = scan(lane_tiles(offsets, base + lane, groups, rows, bm, lo, m), lane);
-            total += __builtin_amdgcn_readlane(t, 63);
+            const int t = lane_tiles(offsets, base + lane, groups, rows, bm, half, false, lo, m);
+            total += __builtin_amdgcn_readlane(scan(t, lane), 63);
+            if (half > 0)
+                small += __builtin_popcountll(__ballot(m % bm > 0 && m % bm <= half));
         }
     }
-    // Group, its first row, its rows and the tile inside it of tile `t` < total.
+    // Group, its first row, its rows and the tile inside it of tile `t` of
+    // either list.
     __device__ __forceinline__ void find(const int32_t *offsets, int groups, int rows, int bm,
-                                         int lane, int t, int &group, int &lo, int &m, int &tm) const
+                                         int lane, int half, bool want_small, int t, int &group, int &lo,
+                                         int &m, int &tm) const
     {
         group = 0;
         lo = 0;
         m = rows;
-        tm = t;
+        tm = want_small ? rows / bm : t;
         if (offsets == nullptr) return;
         int before = 0;
         for (int base = 0; base < groups; base += 64) {
             int l, n;
-            const int mine = lane_tiles(offsets, base + lane, groups, rows, bm, l, n);
+            const int mine = lane_tiles(offsets, base + lane, groups, rows, bm, half, want_small, l, n);
             const int upto = before + scan(mine, lane);
             const uint64_t past = __ballot(upto > t);
             if (past != 0) {
@@ -206,7 +219,8 @@ struct GroupRows {
                 group = base + at;
                 lo = __builtin_amdgcn_readlane(l, at);
                 m = __builtin_amdgcn_readlane(n, at);
-                tm = t - (__builtin_amdgcn_readlane(upto, at) - __builtin_amdgcn_readlane(mine, at));
+                tm = want_small ? m / bm
+                                : t - (__builtin_amdgcn_readlane(upto, at) - __builtin_amdgcn_readlane(mine, at));
                 return;
             }
             before = __builtin_amdgcn_readlane(upto, 63);
@@ -226,68 +240,140 @@ __device__ __forceinline__ int xcd_place(int active)
     return (bid >> 3) < per && at < active ? at : -1;
 }
 
+// The list position and the piece of this block, the j-th of its XCD, in a list
+// of n tiles and `small` small ones behind them.
+//
+// One block of a large tile fills a compute unit, so n tiles take n / slots
+// rounds of the XCD's `slots` units, and a last round that is not full leaves
+// units idle for a whole tile's time.  Its r = n % slots tiles are cut into two
+// or four pieces where that ends sooner, by the times of the pieces in tenths
+// of a tile's: half (and a small tile) 6, a quarter 4 (measured: 0.55 to 0.65
+// and 0.35 to 0.45 of a tile's time at K of 2048 to 8192).  slots == 0: no
+// pieces.  At most 3/2 slots pieces more than tiles come out of it: four pieces
+// are chosen for r <= slots / 2 only (beyond, 4 * 3 exceeds what whole tiles
+// take), two for r < slots.
+struct Piece {
+    int at;        // position in the list, or -1
+    int of, which; // 1, 2 or 4 pieces; which of them
+};
+__device__ __forceinline__ Piece xcd_piece(int j, int n, int small, int slots)
+{
+    const int r = slots > 0 ? n % slots : 0;
+    int of = 1;
+    if (r > 0) {
+        auto rounds = [&](int blocks) { return (max(blocks, 0) + slots - 1) / slots; };
+        const int t1 = 10 + 6 * rounds(small - (slots - r)), t2 = 6 * rounds(2 * r + small);
+        const int t4 = 4 * rounds(4 * r) + 6 * rounds(small);
+        of = t1 <= t2 && t1 <= t4 ? 1 : t2 <= t4 ? 2 : 4;
+    }
+    const int whole = of == 1 ? n : n - r;
+    if (j < whole) return {j, 1, 0};
+    const int h = j - whole, pieces = (n - whole) * of;
+    if (h < pieces) return {whole + h / of, of, h % of};
+    const int at = n + h - pieces;
+    return {at < n + small ? at : -1, 1, 0};
+}
+
+// Group of rank o in the order of falling row counts (ties: the lower group
+// first), for up to 64 groups, one per lane; the groups as they are for more.
+// Blocks of the largest groups start first, so that none of them runs alone at
+// the end.
+__device__ __forceinline__ int group_of_rank(const int32_t *offsets, int groups, int rows, int lane, int o)
+{
+    if (offsets == nullptr || groups == 1 || groups > 64) return o;
+    int lo, m = -1;
+    if (lane < groups) group_span(offsets, lane, rows, lo, m);
+    int rank = 0;
+    for (int g = 0; g < groups; ++g) {
+        const int other = __builtin_amdgcn_readlane(m, g);
+        rank += other > m || (other == m && g < lane) ? 1 : 0;
+    }
+    return __builtin_ctzll(__ballot(lane < groups && rank == o));
+}
+
 // --------------------------------------------------------------- epilogue --
 
-template <int V>
+// V values of an output row from element idx on, n of them inside the matrix.
+// WHOLE: all of them, 16 bytes at a 16-byte boundary; else decided here.
+template <int V, bool WHOLE = false>
 __device__ __forceinline__ void load_out(const void *C, int64_t idx, int n, bool bf16, bool vec,
                                          float (&v)[V])
 {
-    if (bf16) {
+    if (V == 8 && bf16) {
         const uint16_t *c = static_cast<const uint16_t *>(C) + idx;
-        if (V == 8 && vec && n >= V) {
+        if (WHOLE || (vec && n >= V)) {
             const u32x4 w = load16(c);
 #pragma unroll
             for (int i = 0; i < V / 2; ++i) {
                 v[2 * i] = __uint_as_float(w[i & 3] << 16);
                 v[2 * i + 1] = __uint_as_float(w[i & 3] & 0xFFFF0000u);
             }
-        } else {
-#pragma unroll
-            for (int i = 0; i < V; ++i) v[i] = i < n ? __uint_as_float((uint32_t)c[i] << 16) : 0.0f;
+            return;
         }
-    } else {
+    }
+    if (V == 4 && bf16 && !WHOLE && vec && n >= V) {
+        const u32x2 w = *reinterpret_cast<const u32x2 *>(static_cast<const uint16_t *>(C) + idx);
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+            v[2 * i] = __uint_as_float(w[i & 1] << 16);
+            v[2 * i + 1] = __uint_as_float(w[i & 1] & 0xFFFF0000u);
+        }
+        return;
+    }
+    if (V == 4 && !bf16) {
         const float *c = static_cast<const float *>(C) + idx;
-        if (V == 4 && vec && n >= V) {
+        if (WHOLE || (vec && n >= V)) {
             const u32x4 w = load16(c);
 #pragma unroll
             for (int i = 0; i < V; ++i) v[i] = __uint_as_float(w[i & 3]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < V; ++i) v[i] = i < n ? c[i] : 0.0f;
+            return;
         }
+    }
+    if constexpr (!WHOLE) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            v[i] = i >= n ? 0.0f
+                   : bf16 ? __uint_as_float((uint32_t) static_cast<const uint16_t *>(C)[idx + i] << 16)
+                          : static_cast<const float *>(C)[idx + i];
     }
 }
 
 // Rounded once, to nearest even (bf16), or as they are.  Non-temporal: the
 // layer's outputs are written once and must not evict the operand tiles that
 // other blocks still stream.
-template <int V>
+template <int V, bool WHOLE = false>
 __device__ __forceinline__ void store_outs(void *C, int64_t idx, int n, bool bf16, bool vec,
                                            const float (&v)[V])
 {
-    if (bf16) {
-        uint16_t *c = static_cast<uint16_t *>(C) + idx;
-        if (V == 8 && vec && n >= V) {
-            u32x4 w;
+    if (V == 8 && bf16 && (WHOLE || (vec && n >= V))) {
+        u32x4 w;
 #pragma unroll
-            for (int i = 0; i < V / 2; ++i) w[i & 3] = f32x2_to_bf16x2_rne(v[2 * i], v[2 * i + 1]);
-            __builtin_nontemporal_store(w, reinterpret_cast<u32x4 *>(c));
-        } else {
+        for (int i = 0; i < V / 2; ++i) w[i & 3] = f32x2_to_bf16x2_rne(v[2 * i], v[2 * i + 1]);
+        __builtin_nontemporal_store(w, reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(C) + idx));
+        return;
+    }
+    if (V == 4 && bf16 && !WHOLE && vec && n >= V) {
+        u32x2 w;
 #pragma unroll
-            for (int i = 0; i < V; ++i)
-                if (i < n) c[i] = f32_to_bf16_rne(v[i]);
-        }
-    } else {
-        float *c = static_cast<float *>(C) + idx;
-        if (V == 4 && vec && n >= V) {
-            u32x4 w;
+        for (int i = 0; i < V / 2; ++i) w[i & 1] = f32x2_to_bf16x2_rne(v[2 * i], v[2 * i + 1]);
+        *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(C) + idx) = w;
+        return;
+    }
+    if (V == 4 && !bf16 && (WHOLE || (vec && n >= V))) {
+        u32x4 w;
 #pragma unroll
-            for (int i = 0; i < V; ++i) w[i & 3] = __float_as_uint(v[i]);
-            __builtin_nontemporal_store(w, reinterpret_cast<u32x4 *>(c));
-        } else {
+        for (int i = 0; i < V; ++i) w[i & 3] = __float_as_uint(v[i]);
+        __builtin_nontemporal_store(w, reinterpret_cast<u32x4 *>(static_cast<float *>(C) + idx));
+        return;
+    }
+    if constexpr (!WHOLE) {
 #pragma unroll
-            for (int i = 0; i < V; ++i)
-                if (i < n) c[i] = v[i];
+        for (int i = 0; i < V; ++i) {
+            if (i >= n) break;
+            if (bf16)
+                static_cast<uint16_t *>(C)[idx + i] = f32_to_bf16_rne(v[i]);
+            else
+                static_cast<float *>(C)[idx + i] = v[i];
         }
     }
 }
@@ -310,89 +396,95 @@ __device__ __forceinline__ void load_bias(const EpilogueArgs &e, int64_t at, int
 // V sums of one output row from column col on, n of them inside the matrix,
 // finished and stored.  `row` counts rows of C, pre and residual; c_off is an
 // element offset of C (the group's dw).
-template <int V>
+template <int V, bool WHOLE = false>
 __device__ __forceinline__ void finish_piece(const EpilogueArgs &e, int64_t c_off, int64_t row,
                                              int col, int n, const float (&bias)[V], float (&v)[V])
 {
-    const bool bf16 = e.out_bf16 != 0, vec = e.vec != 0;
+    const bool bf16 = WHOLE ? V == 8 : e.out_bf16 != 0, vec = e.vec != 0;
     float old[V];
-    if (e.residual != nullptr) load_out<V>(e.residual, c_off + row * e.ldr + col, n, bf16, vec, old);
+    if (e.residual != nullptr) load_out<V, WHOLE>(e.residual, c_off + row * e.ldr + col, n, bf16, vec, old);
 #pragma unroll
     for (int i = 0; i < V; ++i) v[i] = e.alpha * v[i] + bias[i];
-    if (e.pre != nullptr) store_outs<V>(e.pre, row * e.ldp + col, n, bf16, vec, v);
+    if (e.pre != nullptr) store_outs<V, WHOLE>(e.pre, row * e.ldp + col, n, bf16, vec, v);
     act_apply<V>(e.act, v);
     if (e.residual != nullptr) {
 #pragma unroll
         for (int i = 0; i < V; ++i) v[i] += e.beta * old[i];
     }
-    store_outs<V>(e.C, c_off + row * e.ldc + col, n, bf16, vec, v);
+    store_outs<V, WHOLE>(e.C, c_off + row * e.ldc + col, n, bf16, vec, v);
 }
 
-// The block's accumulators, finished and stored (or stored raw, as partial
-// sums).  A fragment gives each lane single elements of 32 columns, so each
-// wave passes one 32-row fragment row at a time through LDS (its own scratch
-// in the stages, free after the main loop) and takes it back as pieces of V
-// consecutive columns -- 16 bytes of output -- per lane.  64 lanes cover whole
-// rows of the wave's sub-block, so a lane's column is the same in every piece
-// and its bias is loaded once.  Blocks at an edge and rows without 16-byte
-// alignment go the same way with masked element accesses.
+// The block's accumulators as pieces of V consecutive columns of an output row
+// per lane: out(row, col, piece) for each, row and col inside the block.
+//
+// The products run with w (or dz) as the first operand, so a lane's four
+// consecutive accumulators are four consecutive columns of one output row.
+// Each wave passes them through LDS, its share of the stages (free after the
+// main loop), as many rows at a time as fit: 16-byte writes, then a loop in
+// which the wave reads whole rows, 16 bytes of output per lane.  The loop holds
+// the epilogue's code once; written out for every accumulator instead, without
+// LDS, it filled the instruction cache and spilled registers.  The 16-byte
+// chunks of a row are permuted by its number, so that the lanes of a write (16
+// or 32 rows at the same columns) spread over the banks.
 template <class G, int V>
-struct FinishTile {
-    static constexpr int CPR = G::WTN / V;        // pieces per row
-    static constexpr int RPI = 64 / CPR;          // rows per pass of the wave
-    static constexpr int SCRATCH = 32 * G::WTN * 4;
-    static constexpr int PER_STAGE = G::STAGE_BYTES / SCRATCH;
-    static_assert(PER_STAGE * G::STAGES >= G::NW, "one scratch per wave");
-    static_assert(64 % CPR == 0 && 32 % RPI == 0, "whole rows per pass");
-    // Columns move in groups so that the lanes of a fragment write use other
-    // banks: 32 x 32 fragments (fp32) write rows 4 apart in two lane halves,
-    // 16 x 16 ones (bf16) in four quarters.
+struct StagedTile {
+    static constexpr int COLS = G::WTM;
+    static constexpr int FR = G::BF16 ? 16 : 32;    // rows of a fragment
+    // rows that fit a wave's share, whole fragments, a divisor of its rows
+    static constexpr int SHARE = G::STAGE_BYTES * 2 / G::NW;   // of two stages
+    static constexpr int FIT = SHARE / (COLS * 4);
+    static constexpr int ROWS = FIT >= G::WTN ? G::WTN : FIT >= G::WTN / 2 ? G::WTN / 2 : 32;
+    static_assert(ROWS * COLS * 4 <= SHARE && G::WTN % ROWS == 0 && ROWS % FR == 0, "whole fragments fit");
+    static constexpr int CPR = COLS / V, PASSES = ROWS * CPR / 64;
+    static_assert(ROWS * CPR % 64 == 0, "whole passes");
     static __device__ __forceinline__ int place(int row, int col)
     {
-        if (G::BF16) return col ^ (((row >> 2) & (G::WTN >= 64 ? 3 : 1)) << 4);
-        return G::WTN >= 64 ? col ^ (((row >> 2) & 1) << 5) : col;
+        return row * COLS + (col ^ ((row << 2) & (COLS - 4)));
     }
-    static __device__ __forceinline__ void put(unsigned char *scr, int row, int col, float v)
+    // The share of wave `wv`: half the waves in either of the first two stages.
+    static __device__ __forceinline__ unsigned char *share(unsigned char *s0, unsigned char *s1, int wv)
     {
-        *reinterpret_cast<float *>(scr + 4 * (row * G::WTN + place(row, col))) = v;
+        constexpr int HALF = G::NW > 1 ? G::NW / 2 : 1;
+        return (wv < HALF ? s0 : s1) + (wv % HALF) * (ROWS * COLS * 4);
     }
-
     template <class Acc, class Out>
     static __device__ __forceinline__ void run(unsigned char *scr, const BlockCtx<G> &c, const Acc &acc,
                                                Out &&out)
     {
-        const int cc = V * (c.lane % CPR), r0 = c.lane / CPR;
-        static_for<0, G::WTM / 32>([&](auto fm) {
-            if constexpr (G::BF16) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int fn = 0; fn < G::FN; ++fn)
-#pragma unroll
-                        for (int r = 0; r < 4; ++r)
-                            put(scr, 16 * h + 4 * (c.lane >> 4) + r, fn * 16 + (c.lane & 15),
-                                acc[2 * fm + h][fn][r]);
-            } else {
-#pragma unroll
-                for (int fn = 0; fn < G::FN; ++fn)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r)
-                        put(scr, 8 * (r >> 2) + 4 * (c.lane >> 5) + (r & 3), fn * 32 + (c.lane & 31),
-                            acc[fm][fn][r]);
-            }
+        static_for<0, G::WTN / ROWS>([&](auto s_c) {
+            constexpr int slab = decltype(s_c)::value;
+            static_for<0, ROWS / FR>([&](auto j_c) {
+                constexpr int j = decltype(j_c)::value;
+                static_for<0, G::FM>([&](auto i_c) {
+                    constexpr int i = decltype(i_c)::value;
+                    if constexpr (G::BF16) {
+                        *reinterpret_cast<floatx4 *>(
+                            scr + 4 * place(16 * j + (c.lane & 15), 16 * i + 4 * (c.lane >> 4))) =
+                            acc[i][slab * (ROWS / FR) + j];
+                    } else {
+                        const floatx16 &a = acc[i][slab * (ROWS / FR) + j];
+                        static_for<0, 4>([&](auto g_c) {
+                            constexpr int g = 4 * decltype(g_c)::value;
+                            *reinterpret_cast<floatx4 *>(
+                                scr + 4 * place(32 * j + (c.lane & 31), 32 * i + 2 * g + 4 * (c.lane >> 5))) =
+                                floatx4{a[g], a[g + 1], a[g + 2], a[g + 3]};
+                        });
+                    }
+                });
+            });
             // a wave's LDS accesses complete in order: the reads see the
-            // writes above, and the next rows' writes follow these reads
+            // writes above, and the next slab's writes follow these reads
 #pragma unroll 2
-            for (int u = 0; u < 32 / RPI; ++u) {
-                const int rr = r0 + u * RPI;
+            for (int u = 0; u < PASSES; ++u) {
+                const int ch = c.lane + 64 * u, row = ch / CPR, col = ch % CPR * V;
                 float v[V];
 #pragma unroll
                 for (int h = 0; h < V; h += 4) {
-                    const u32x4 w = lds_load16(scr, 4 * (rr * G::WTN + place(rr, cc + h)));
+                    const u32x4 w = lds_load16(scr, 4 * place(row, col + h));
 #pragma unroll
                     for (int i = 0; i < 4; ++i) v[h + i] = __uint_as_float(w[i]);
                 }
-                out(c.wrow * G::WTM + fm * 32 + rr, v);
+                out(c.wcol * G::WTN + ROWS * slab + row, c.wrow * G::WTM + col, v);
             }
         });
     }
@@ -400,83 +492,87 @@ struct FinishTile {
 
 // ------------------------------------------------------------------ kernel --
 
-template <bool BF16, int BM, int BN, int BK, int WM, int WN, int STAGES, int LA, int LB, bool ALIGNED>
-__global__ void __launch_bounds__(64 * WM * WN) linear_kernel(LinearArgs p)
+// Global -> registers of one operand's k-tile at k0 with masks, rows 16-byte
+// aligned: a chunk that holds an element of the matrix is read whole (it lies
+// inside the row's pitch or on the page of the row's last element), the
+// elements from kend on are zeros.  n_outer is a whole number of chunks where
+// it runs along the rows.
+template <class T>
+__device__ __forceinline__ void load_tile_chunks(const typename T::In *X, int64_t ld, int outer0, int n_outer,
+                                                 int k0, int kend, int tid, u32x4 (&r)[T::PER_THREAD])
 {
-    using G = typename std::conditional<BF16, Geo16<BM, BN, BK, WM, WN, STAGES, LA, LB>,
-                                        Geo<BF16, BM, BN, BK, WM, WN, STAGES, LA, LB>>::type;
+#pragma unroll
+    for (int u = 0; u < T::PER_THREAD; ++u) {
+        const int ch = tid + u * T::NT;
+        const int row = ch / T::CPR, e = (ch % T::CPR) * T::VEC;
+        if constexpr (T::LAYOUT == KMAJOR) {
+            const int left = kend - k0 - e;   // elements of the chunk before kend
+            u32x4 v = {0, 0, 0, 0};
+            if (outer0 + row < n_outer && left > 0) v = load16(X + (int64_t)(outer0 + row) * ld + k0 + e);
+#pragma unroll
+            for (int d = 0; d < 4; ++d) {
+                if constexpr (T::ES == 4)
+                    v[d] = d < left ? v[d] : 0u;
+                else
+                    v[d] &= 2 * d + 1 < left ? 0xFFFFFFFFu : 2 * d < left ? 0xFFFFu : 0u;
+            }
+            r[u] = v;
+        } else {
+            r[u] = u32x4{0, 0, 0, 0};
+            if (k0 + row < kend && outer0 + e < n_outer) r[u] = load16(X + (int64_t)(k0 + row) * ld + outer0 + e);
+        }
+    }
+}
+
+// The output tile of a block: rows row0 .. of the group's output (its m rows,
+// or the M rows of dw), columns col0 .. .
+struct TileSpec {
+    int slice, group;
+    int lo, m;          // the group's first row and rows
+    int row0, col0;
+};
+
+// One block's tile, all of it: main loop and epilogue.  The main loops' first
+// operand is w (or dz), whose rows are output columns, the second x, whose rows
+// are output rows: G is the geometry of the transposed tile.  The stages are
+// the kernel's arrays, at least as large as G's.
+template <class G, bool ALIGNED>
+__device__ __forceinline__ void linear_tile(const LinearArgs &p, const TileSpec &t, unsigned char *lds0,
+                                            unsigned char *lds1, unsigned char *lds2, unsigned char *lds3)
+{
     using In = typename G::In;
+    constexpr bool BF16 = G::BF16, WGRAD = G::LB == MNMAJOR;   // groups cut the summed axis
+    constexpr int BM = G::BN, BN = G::BM, BK = G::BK;
     using Sum = typename std::conditional<BF16, floatx4, floatx16>::type;
     constexpr int SUMS = BF16 ? 4 : 16;
-    constexpr bool PINNED = BF16 && WM * WN == 4 && BK == 64 && STAGES == 2 && ALIGNED;
-    constexpr bool TWO = BF16 && WM * WN == 8 && STAGES == two_groups_stages(BM / WM / 16);
-    constexpr bool WGRAD = LA == MNMAJOR;   // groups cut the summed axis
-
-    __shared__ __attribute__((aligned(1024))) unsigned char lds0[G::STAGE_BYTES];
-    __shared__ __attribute__((aligned(1024))) unsigned char lds1[G::STAGE_BYTES];
-    __shared__ __attribute__((aligned(1024))) unsigned char lds2[STAGES > 2 ? G::STAGE_BYTES : 1];
-    __shared__ __attribute__((aligned(1024))) unsigned char lds3[STAGES > 3 ? G::STAGE_BYTES : 1];
+    constexpr bool PINNED = BF16 && G::NW == 4 && BK == 64 && G::STAGES == 2 && ALIGNED;
 
     BlockCtx<G> c;
     c.tid = (int)threadIdx.x;
     c.lane = c.tid & 63;
     const int wave = c.tid >> 6;
-    c.wrow = wave / WN;
-    c.wcol = wave % WN;
-
-    // This block's slice, group and tile.
-    int slice, group, lo, m, tm, tn;
-    if constexpr (WGRAD) {
-        const int tiles = p.tiles_m * p.tiles_n;
-        const int at = xcd_place(p.splits * p.groups * tiles);
-        if (at < 0) return;
-        slice = at / (p.groups * tiles);
-        const int rest = at - slice * p.groups * tiles;
-        group = rest / tiles;
-        const int t = rest - group * tiles;
-        const int per_raster = p.group_m * p.tiles_n;
-        const int first = t / per_raster * p.group_m;
-        const int rows = min(p.tiles_m - first, p.group_m);
-        const int in = t - first * p.tiles_n;
-        tm = first + in % rows;
-        tn = in / rows;
-        group_span(p.offsets, group, p.rows, lo, m);
-        lo = __builtin_amdgcn_readfirstlane(lo);
-        m = __builtin_amdgcn_readfirstlane(m);
-    } else {
-        const GroupRows list(p.offsets, p.groups, p.rows, BM, c.lane);
-        const int tiles = list.total * p.tiles_n;
-        const int at = xcd_place(p.splits * tiles);
-        if (at < 0) return;
-        slice = at / tiles;
-        const int t = at - slice * tiles;
-        const int per_raster = p.group_m * p.tiles_n;
-        const int first = t / per_raster * p.group_m;
-        const int rows = min(list.total - first, p.group_m);
-        const int in = t - first * p.tiles_n;
-        tn = in / rows;
-        list.find(p.offsets, p.groups, p.rows, BM, c.lane, first + in % rows, group, lo, m, tm);
-    }
-    c.bm = tm * BM;
-    c.bn = tn * BN;
-    c.lda = p.lda;
-    c.ldb = p.ldb;
-    c.A = static_cast<const In *>(p.A) + (int64_t)lo * p.lda;
-    c.N = p.n_load;
+    c.wrow = wave / G::WN;
+    c.wcol = wave % G::WN;
+    c.bm = t.col0;
+    c.bn = t.row0;
+    c.lda = p.ldw;
+    c.ldb = p.ldx;
+    c.B = static_cast<const In *>(p.x) + (int64_t)t.lo * p.ldx;
+    c.M = p.n_load;
     int K, kps;
     if constexpr (WGRAD) {
-        c.B = static_cast<const In *>(p.B) + (int64_t)lo * p.ldb;
-        c.M = p.m_load;
-        K = m;
+        c.A = static_cast<const In *>(p.w) + (int64_t)t.lo * p.ldw;
+        c.N = p.m_load;
+        K = t.m;
         // whole k-tiles per slice; a slice past the group's rows sums nothing
-        kps = ((m + BK - 1) / BK + p.splits - 1) / p.splits * BK;
+        kps = ((K + BK - 1) / BK + p.splits - 1) / p.splits * BK;
     } else {
-        c.B = static_cast<const In *>(p.B) + group * p.stride_b;
-        c.M = m;
+        c.A = static_cast<const In *>(p.w) + t.group * p.stride_w;
+        c.N = t.m;
         K = p.K;
         kps = p.k_per_split;
     }
-    const int kbeg = min(K, slice * kps);
+    const int kbeg = min(K, t.slice * kps);
     c.kend = min(K, kbeg + kps);
     const int ntiles = (c.kend - kbeg + BK - 1) / BK;
 
@@ -487,45 +583,55 @@ __global__ void __launch_bounds__(64 * WM * WN) linear_kernel(LinearArgs p)
         for (int fn = 0; fn < G::FN; ++fn)
 #pragma unroll
             for (int r = 0; r < SUMS; ++r) acc[fm][fn][r] = 0.0f;
-    auto direct = [&](auto dw, int nfast, int kbeg) {
-        constexpr int DW = decltype(dw)::value;
-        if constexpr (BF16 && PINNED) {
-            static_assert(DW == 16, "aligned rows");
-            main_loop_pinned<G>(lds0, lds1, c, kbeg, nfast, acc);
-        } else if constexpr (BF16 && TWO) {
-            const bool busy = c.bm + c.wrow * G::WTM < c.M && c.bn + c.wcol * G::WTN < c.N;
-            main_loop_two_groups<G, DW>(lds0, lds1, lds2, c, kbeg, nfast,
-                                        __builtin_amdgcn_readfirstlane(busy), acc);
-        } else if constexpr (BF16)
-            main_loop16_direct<G, DW>(lds0, lds1, lds2, lds3, c, kbeg, nfast, acc);
-        else
-            main_loop_direct<G, decltype(dw)::value>(lds0, lds1, lds2, lds3, c, kbeg, nfast, acc);
-    };
 
-    // The main loops and the choice between them are those of the dense
-    // product, on the group's rows: whole k-tiles through direct loads of 16
-    // bytes per lane (aligned rows) or 4 range-checked ones, the rest masked.
+    // The choice between the loops is that of the dense product, on the
+    // group's rows: whole k-tiles through direct loads of 16 bytes per lane
+    // (aligned rows) or 4 range-checked ones, the rest masked.
     {
-        const bool edge_mn = c.bm + BM > c.M || c.bn + BN > c.N;
+        const bool edge_mn = c.bm + BN > c.M || c.bn + BM > c.N;
         const bool edge16 = (G::LA == KMAJOR || c.M % G::VEC == 0) &&
                             (G::LB == KMAJOR || c.N % G::VEC == 0);
         const bool x4 = ALIGNED && p.direct_ok && (!edge_mn || edge16);
         const bool pairs_ok =
-            !G::BF16 || (((p.lda | p.ldb) & 1) == 0 && (((uintptr_t)c.A | (uintptr_t)c.B) & 3) == 0 &&
-                         (G::LA == KMAJOR || (c.M & 1) == 0) && (G::LB == KMAJOR || (c.N & 1) == 0));
+            !BF16 || (((p.ldw | p.ldx) & 1) == 0 && (((uintptr_t)c.A | (uintptr_t)c.B) & 3) == 0 &&
+                      (G::LA == KMAJOR || (c.M & 1) == 0) && (G::LB == KMAJOR || (c.N & 1) == 0));
         const bool dw = G::DMA4 && !PINNED && p.direct_ok && pairs_ok && !x4;
         const int nfast = x4 || dw ? (c.kend - kbeg) / BK : 0;
-        c.rot = (tm + tn) % 8;
+        // Blocks of different groups start at different k-tiles.  Weights whose
+        // rows lie a power of two apart keep their k-tile on a few memory
+        // channels, and blocks in step would all read from those (16 groups of
+        // 512 rows, N x K weights of 4096 x 4096: 264 -> 232 us); blocks that
+        // share weights or rows are of one group and stay in step.
+        c.rot = WGRAD ? 0 : 8 * t.group;
         if constexpr (G::DMA4 && !PINNED) {
-            c.a_end = operand_end_bytes<typename G::TA>(p.lda, c.M, K);
-            c.b_end = operand_end_bytes<typename G::TB>(p.ldb, c.N, K);
-            if (dw && nfast > 0) direct(std::integral_constant<int, 4>(), nfast, kbeg);
+            c.a_end = operand_end_bytes<typename G::TA>(p.ldw, c.M, K);
+            c.b_end = operand_end_bytes<typename G::TB>(p.ldx, c.N, K);
+            if (dw && nfast > 0) {
+                if constexpr (BF16)
+                    main_loop16_direct<G, 4>(lds0, lds1, lds2, lds3, c, kbeg, nfast, acc);
+                else
+                    main_loop_direct<G, 4>(lds0, lds1, lds2, lds3, c, kbeg, nfast, acc);
+            }
         }
         if constexpr (ALIGNED) {
-            if (x4 && nfast > 0) direct(std::integral_constant<int, 16>(), nfast, kbeg);
+            if (x4 && nfast > 0) {
+                if constexpr (PINNED)
+                    main_loop_pinned<G>(lds0, lds1, c, kbeg, nfast, acc);
+                else if constexpr (BF16)
+                    main_loop16_direct<G, 16>(lds0, lds1, lds2, lds3, c, kbeg, nfast, acc);
+                else
+                    main_loop_direct<G, 16>(lds0, lds1, lds2, lds3, c, kbeg, nfast, acc);
+            }
         }
         if (ntiles > nfast) {
-            auto load = [&](int k0, StageRegs<G> &r) { global_load_masked<ALIGNED>(c, k0, r); };
+            auto load = [&](int k0, StageRegs<G> &r) {
+                if constexpr (ALIGNED) {
+                    load_tile_chunks<typename G::TA>(c.A, c.lda, c.bm, c.M, k0, c.kend, c.tid, r.a);
+                    load_tile_chunks<typename G::TB>(c.B, c.ldb, c.bn, c.N, k0, c.kend, c.tid, r.b);
+                } else {
+                    global_load_masked<false>(c, k0, r);
+                }
+            };
             if constexpr (BF16)
                 main_loop16_masked(lds0, lds1, c, kbeg + nfast * BK, ntiles - nfast, acc, load);
             else
@@ -533,53 +639,140 @@ __global__ void __launch_bounds__(64 * WM * WN) linear_kernel(LinearArgs p)
         }
     }
 
-    // Epilogue.  The waves' scratches share the stages: wait until the last
-    // reader of them is done.
-    __syncthreads();
-    using F = FinishTile<G, 4>;
-    const int wv = __builtin_amdgcn_readfirstlane(wave);
-    const int arr = wv / F::PER_STAGE;
-    unsigned char *scr = (arr == 0 ? lds0 : arr == 1 ? lds1 : arr == 2 ? lds2 : lds3) +
-                         (wv % F::PER_STAGE) * F::SCRATCH;
-    const int out_rows = WGRAD ? p.M : m;   // rows of this group's output
+    const int out_rows = WGRAD ? p.M : t.m;   // rows of this group's output
+    // the last readers of the stages have passed a barrier
+    unsigned char *scr = StagedTile<G, 4>::share(lds0, lds1, __builtin_amdgcn_readfirstlane(wave));
     if (p.splits > 1) {
         // raw sums, summed by the reduce kernel: slice-major, first form rows x
         // N by global row, second form groups x M x N
-        const int64_t row0 = WGRAD ? ((int64_t)slice * p.groups + group) * p.M
-                                   : (int64_t)slice * p.rows + lo;
-        const int col = c.bn + c.wcol * G::WTN + 4 * (c.lane % F::CPR);
-        F::run(scr, c, acc, [&](int r, float (&v)[4]) {
-            const int row = c.bm + r;
-            if (row >= out_rows) return;
-            float *out = p.ws + (row0 + row) * p.N + col;
-            if ((p.N & 3) == 0) {
-                if (col < p.N) *reinterpret_cast<u32x4 *>(out) = __builtin_bit_cast(u32x4, v);
+        const int64_t first = WGRAD ? ((int64_t)t.slice * p.groups + t.group) * p.M
+                                    : (int64_t)t.slice * p.rows + t.lo;
+        float *out = p.ws + (first + t.row0) * p.N + t.col0;
+        const bool quads = (p.N & 3) == 0;
+        StagedTile<G, 4>::run(scr, c, acc, [&](int r, int cc, float (&v)[4]) {
+            const int n = p.N - t.col0 - cc;
+            if (t.row0 + r >= out_rows || n <= 0) return;
+            float *o = out + (int64_t)r * p.N + cc;
+            if (quads) {
+                *reinterpret_cast<u32x4 *>(o) = __builtin_bit_cast(u32x4, v);
             } else {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    if (col + i < p.N) out[i] = v[i];
+                    if (i < n) o[i] = v[i];
             }
         });
         return;
     }
-    const int64_t crow0 = WGRAD ? 0 : lo;
-    const int64_t c_off = WGRAD ? group * p.stride_c : 0;
+    const int64_t crow0 = (WGRAD ? 0 : t.lo) + t.row0;
+    const int64_t c_off = WGRAD ? t.group * p.stride_c : 0;
+    const int64_t bias0 = t.group * p.stride_bias + t.col0;
     auto finish = [&](auto v_c) {
         constexpr int V = decltype(v_c)::value;
-        using FV = FinishTile<G, V>;
-        const int col = c.bn + c.wcol * G::WTN + V * (c.lane % FV::CPR);
-        const int n = p.N - col;
+        using S = StagedTile<G, V>;
+        // a lane's columns are the same in every piece: 64 lanes take whole rows
+        static_assert(64 % S::CPR == 0, "whole rows per pass");
+        const int cc = c.wrow * G::WTM + c.lane % S::CPR * V, n = p.N - t.col0 - cc;
+        const int rows = out_rows - t.row0;
         float bias[V];
-        load_bias<V>(p.e, group * p.stride_bias + col, n, bias);
-        FV::run(scr, c, acc, [&](int r, float (&v)[V]) {
-            const int row = c.bm + r;
-            if (row < out_rows && n > 0) finish_piece<V>(p.e, c_off, crow0 + row, col, n, bias, v);
-        });
+        load_bias<V>(p.e, bias0 + cc, n, bias);
+        if (t.col0 + BN <= p.N && p.e.vec) {
+            S::run(scr, c, acc, [&](int r, int, float (&v)[V]) {
+                if (r < rows) finish_piece<V, true>(p.e, c_off, crow0 + r, t.col0 + cc, V, bias, v);
+            });
+        } else {
+            S::run(scr, c, acc, [&](int r, int, float (&v)[V]) {
+                if (r < rows && n > 0) finish_piece<V, false>(p.e, c_off, crow0 + r, t.col0 + cc, n, bias, v);
+            });
+        }
     };
     if (p.e.out_bf16)
         finish(std::integral_constant<int, 8>());
     else
         finish(std::integral_constant<int, 4>());
+}
+
+// BM x BN output tile, WM x WN waves; LX and LW: how x and w (dz) lie in memory.
+template <bool BF16, int BM, int BN, int BK, int WM, int WN, int STAGES, int LX, int LW, bool ALIGNED>
+__global__ void __launch_bounds__(64 * WM * WN) linear_kernel(LinearArgs p)
+{
+    using G = typename std::conditional<BF16, Geo16<BN, BM, BK, WN, WM, STAGES, LW, LX>,
+                                        Geo<BF16, BN, BM, BK, WN, WM, STAGES, LW, LX>>::type;
+    constexpr bool WGRAD = LX == MNMAJOR;
+    // one block per compute unit, and pieces of a tile to choose from
+    constexpr bool PIECES = BF16 && BM == 256 && BN == 256 && WM * WN == 4;
+
+    __shared__ __attribute__((aligned(1024))) unsigned char lds0[G::STAGE_BYTES];
+    __shared__ __attribute__((aligned(1024))) unsigned char lds1[G::STAGE_BYTES];
+    __shared__ __attribute__((aligned(1024))) unsigned char lds2[STAGES > 2 ? G::STAGE_BYTES : 1];
+    __shared__ __attribute__((aligned(1024))) unsigned char lds3[STAGES > 3 ? G::STAGE_BYTES : 1];
+
+    // This block's slice, group and tile.  The tiles of a product (of one
+    // group, of all groups' rows) are walked in rasters of group_m tile rows,
+    // so that blocks that run together on an XCD share operands in its L2.
+    const int lane = (int)threadIdx.x & 63, xcd = (int)blockIdx.x & 7, j = (int)blockIdx.x >> 3;
+    const int slots = PIECES ? p.slots : 0;
+    TileSpec t;
+    Piece piece;
+    int tm, tn;
+    auto raster = [&](int i, int rows, int &r, int &col) {
+        const int per = p.group_m * p.tiles_n, first = i / per * p.group_m;
+        const int high = min(rows - first, p.group_m), in = i - first * p.tiles_n;
+        r = first + in % high;
+        col = in / high;
+    };
+    if constexpr (WGRAD) {
+        // every XCD takes an eighth of each group's tiles (another one from
+        // group to group, for groups of few tiles): groups of many rows do not
+        // pile up on one XCD
+        const int tiles = p.tiles_m * p.tiles_n, per = (tiles + 7) >> 3;
+        piece = xcd_piece(j, p.groups * p.splits * per, 0, slots);
+        if (piece.at < 0) return;
+        const int o = piece.at / per, rank = o / p.splits;
+        const int i = ((xcd + o) & 7) * per + piece.at - o * per;
+        if (i >= tiles) return;
+        t.slice = o - rank * p.splits;
+        t.group = __builtin_amdgcn_readfirstlane(group_of_rank(p.offsets, p.groups, p.rows, lane, rank));
+        raster(i, p.tiles_m, tm, tn);
+        group_span(p.offsets, t.group, p.rows, t.lo, t.m);
+        t.lo = __builtin_amdgcn_readfirstlane(t.lo);
+        t.m = __builtin_amdgcn_readfirstlane(t.m);
+    } else {
+        constexpr int HALF = PIECES ? BM / 2 : 0;
+        const GroupRows list(p.offsets, p.groups, p.rows, BM, lane, HALF);
+        // every XCD takes an eighth of either list
+        auto eighth = [&](int n) { return (n + 7) >> 3; };
+        auto mine = [&](int n) { return max(0, min(eighth(n), n - xcd * eighth(n))); };
+        const int n = p.splits * list.total * p.tiles_n, ns = p.splits * list.small * p.tiles_n;
+        piece = xcd_piece(j, mine(n), mine(ns), slots);
+        if (piece.at < 0) return;
+        const bool small = piece.at >= mine(n);
+        const int at = small ? xcd * eighth(ns) + piece.at - mine(n) : xcd * eighth(n) + piece.at;
+        const int high = small ? list.small : list.total, tiles = high * p.tiles_n;
+        t.slice = at / tiles;
+        raster(at - t.slice * tiles, high, tm, tn);
+        list.find(p.offsets, p.groups, p.rows, BM, lane, HALF, small, tm, t.group, t.lo, t.m, tm);
+    }
+    t.row0 = tm * BM;
+    t.col0 = tn * BN;
+    if constexpr (PIECES) {
+        const int out_rows = WGRAD ? p.M : t.m;
+        if (piece.of > 1) {
+            t.row0 += (piece.which & 1) * (BM / 2);
+            if (t.row0 >= out_rows) return;
+        }
+        if (piece.of == 4) {
+            t.col0 += (piece.which >> 1) * (BN / 2);
+            if (t.col0 >= p.N) return;
+            linear_tile<Geo16<BN / 2, BM / 2, BK, 2, 2, 2, LW, LX>, ALIGNED>(p, t, lds0, lds1, lds2, lds3);
+            return;
+        }
+        // halves, and a group's last tile where half the rows suffice
+        if (piece.of == 2 || out_rows - t.row0 <= BM / 2) {
+            linear_tile<Geo16<BN, BM / 2, BK, 4, 1, 2, LW, LX>, ALIGNED>(p, t, lds0, lds1, lds2, lds3);
+            return;
+        }
+    }
+    linear_tile<G, ALIGNED>(p, t, lds0, lds1, lds2, lds3);
 }
 
 // ---------------------------------------------------------------- few rows --
@@ -757,7 +950,7 @@ __global__ void __launch_bounds__(64 * WV) few_rows_kernel(LinearArgs p)
     if (at < 0) return;
     const int tn = at / list.total;
     int group, lo, m, tm;
-    list.find(p.offsets, p.groups, p.rows, BM, lane, at - tn * list.total, group, lo, m, tm);
+    list.find(p.offsets, p.groups, p.rows, BM, lane, 0, false, at - tn * list.total, group, lo, m, tm);
     const int row0 = lo + tm * BM, count = min(BM, m - tm * BM);
 
     F f;
@@ -766,9 +959,9 @@ __global__ void __launch_bounds__(64 * WV) few_rows_kernel(LinearArgs p)
     f.n0 = tn * BN;
     f.N = p.N;
     f.K = p.K;
-    f.ldw = p.ldb;
-    f.w = static_cast<const In *>(p.B) + group * p.stride_b;
-    f.xr = static_cast<const In *>(p.A) + (int64_t)(row0 + min(f.c, count - 1)) * p.lda;
+    f.ldw = p.ldw;
+    f.w = static_cast<const In *>(p.w) + group * p.stride_w;
+    f.xr = static_cast<const In *>(p.x) + (int64_t)(row0 + min(f.c, count - 1)) * p.ldx;
 
     floatx4 acc[W];
 #pragma unroll

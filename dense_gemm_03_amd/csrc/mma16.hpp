@@ -235,75 +235,9 @@ __device__ __forceinline__ void main_loop16_masked(unsigned char *smem0, unsigne
     }
 }
 
-// ------------------------------------------------------- two groups of waves --
+// ------------------------------------------------------------ pinned order ---
 
-// The loop for large blocks: eight waves, two to a SIMD, in two groups that
-// take turns.  A tile is cut into phases of MF x NF fragments over the whole
-// k-tile; a wave alternates between reading the fragments that the next phase
-// lacks (LDS, lgkmcnt(0), barrier) and its products (barrier).  The groups run
-// one slot apart, so on every SIMD one wave multiplies while the other reads:
-// the matrix cores are fed without a second set of fragment registers, and the
-// wait for LDS never stands before a product.
-//
-// Phases of a wave's FM x FN fragments, in an order that reads each fragment
-// once per tile: (0,0) (0,1) (1,1) (1,0) with two halves of either, or (0,0)
-// (0,1) with halves of the columns only.  The last phase's reading slot has the
-// fewest reads (none, for four phases) and issues the direct loads of the tile
-// two ahead, then waits for those of the next tile (issued one tile ago: a
-// whole tile's products cover their latency).
-//
-// Stages.  Tile t sits in stage t % S.  With four phases a tile's last LDS read
-// lies two slots before its last phase's reading slot in the same group, one
-// slot in the other, with barriers between, so tile t + 2 may go into the stage
-// of tile t there: S = 2.  With two phases the last phase still reads, and tile
-// t + 2 goes into the stage of tile t - 1: S = 3.
-constexpr int two_groups_stages(int fm) { return fm >= 8 ? 2 : 3; }
-
-template <class G>
-struct TwoGroups {
-    static constexpr int PM = G::FM >= 8 ? 2 : 1, PN = 2;    // halves of the fragments
-    static constexpr int P = PM * PN;                        // phases
-    static constexpr int MF = G::FM / PM, NF = G::FN / PN;   // fragments of a phase
-    static constexpr int KF = G::STEPS;
-    static constexpr bool OK = G::NW == 8 && G::FN % 2 == 0 && G::FM % PM == 0 &&
-                               G::STAGES == two_groups_stages(G::FM);
-
-    u32x4 a[MF][KF];
-    u32x4 b[PN][NF][KF];
-
-    __device__ __forceinline__ void read_a(const unsigned char *stage, const BlockCtx<G> &c, int pm, int k)
-    {
-#pragma unroll
-        for (int i = 0; i < MF; ++i)
-            a[i][k] = read_frag16<typename G::TA>(stage, c.lane, c.wrow * G::WTM + (pm * MF + i) * 16,
-                                                  k * 32 + 8 * (c.lane >> 4));
-    }
-    __device__ __forceinline__ void read_b(const unsigned char *stage, const BlockCtx<G> &c, int pn, int k)
-    {
-#pragma unroll
-        for (int j = 0; j < NF; ++j)
-            b[pn][j][k] = read_frag16<typename G::TB>(stage + G::A_BYTES, c.lane,
-                                                      c.wcol * G::WTN + (pn * NF + j) * 16,
-                                                      k * 32 + 8 * (c.lane >> 4));
-    }
-    template <int PMI, int PNI>
-    __device__ __forceinline__ void multiply(floatx4 (&acc)[G::FM][G::FN])
-    {
-#pragma unroll
-        for (int k = 0; k < KF; ++k)
-#pragma unroll
-            for (int i = 0; i < MF; ++i)
-#pragma unroll
-                for (int j = 0; j < NF; ++j) {
-                    floatx4 &s = acc[PMI * MF + i][PNI * NF + j];
-                    s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a[i][k]),
-                                                                __builtin_bit_cast(bf16x8, b[PNI][j][k]), s,
-                                                                0, 0, 0);
-                }
-    }
-};
-
-// Nothing moves across: the slots are what the barriers count.
+// Nothing moves across.
 __device__ __forceinline__ void slot_fence()
 {
     asm volatile("" ::: "memory");
@@ -315,100 +249,6 @@ __device__ __forceinline__ void slot_end()
     __builtin_amdgcn_s_barrier();
     slot_fence();
 }
-
-// Whole k-tiles [0, ntiles), ntiles > 0, from k_first.  `busy`: this wave's
-// sub-block holds outputs; a wave without (past the group's last row, past N)
-// only loads and waits.  On entry no wave may read or load any stage; on exit
-// no load is in flight and all waves have passed a barrier after their last
-// read.
-template <class G, int DW>
-__device__ __forceinline__ void main_loop_two_groups(unsigned char *s0, unsigned char *s1, unsigned char *s2,
-                                                     const BlockCtx<G> &c, int k_first, int ntiles, bool busy,
-                                                     floatx4 (&acc)[G::FM][G::FN])
-{
-    using W = TwoGroups<G>;
-    constexpr int S = G::STAGES, LOADS = DirectOffsets<G, DW>::LOADS_PER_TILE;
-    static_assert(W::OK && LOADS <= 63, "two stages (three with two phases), vmcnt within its range");
-    unsigned char *const st[3] = {s0, s1, s2};
-    const bool second = __builtin_amdgcn_readfirstlane(c.tid >> 8) != 0;
-    W w;
-    DirectOffsets<G, DW> o;
-    tile_offsets(c.tid >> 6, c.lane, c.lda, c.bm, c.M, o.a);
-    tile_offsets(c.tid >> 6, c.lane, c.ldb, c.bn, c.N, o.b);
-    // past the last tile the loads repeat it: in bounds, and never read
-    auto k_of = [&](int t) { return k_first + min(t, ntiles - 1) * G::BK; };
-
-    direct_tile_load(st[0], c, o, k_of(0));
-    direct_tile_load(st[1], c, o, k_of(1));
-    __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(LOADS));
-    slot_end();
-    if (second) slot_end();   // one slot behind
-
-    auto products = [&](auto pm, auto pn) {
-        if (busy) {
-            __builtin_amdgcn_s_setprio(1);   // before the reading wave of this SIMD
-            w.template multiply<decltype(pm)::value, decltype(pn)::value>(acc);
-            __builtin_amdgcn_s_setprio(0);
-        }
-        slot_end();
-    };
-    auto read_done = [&]() {
-        __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
-        slot_end();
-    };
-    std::integral_constant<int, 0> _0;
-    std::integral_constant<int, 1> _1;
-    for (int t0 = 0; t0 < ntiles; t0 += S) {
-        static_for<0, S>([&](auto s_c) {
-            constexpr int s = decltype(s_c)::value;
-            const int t = t0 + s;
-            if (s > 0 && t >= ntiles) return;
-            const unsigned char *stage = st[s];
-            unsigned char *load = st[(s + 2) % S];
-            if (busy) {
-#pragma unroll
-                for (int k = 0; k < W::KF; ++k) {
-                    w.read_b(stage, c, 0, k);
-                    w.read_a(stage, c, 0, k);
-                }
-            }
-            slot_end();
-            products(_0, _0);
-            if constexpr (W::PM == 2) {
-                if (busy) {
-#pragma unroll
-                    for (int k = 0; k < W::KF; ++k) w.read_b(stage, c, 1, k);
-                }
-                slot_end();
-                products(_0, _1);
-                if (busy) {
-#pragma unroll
-                    for (int k = 0; k < W::KF; ++k) w.read_a(stage, c, 1, k);
-                }
-                read_done();
-                products(_1, _1);
-                direct_tile_load(load, c, o, k_of(t + 2));
-                __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(LOADS));
-                slot_end();
-                products(_1, _0);
-            } else {
-                if (busy) {
-#pragma unroll
-                    for (int k = 0; k < W::KF; ++k) w.read_b(stage, c, 1, k);
-                }
-                direct_tile_load(load, c, o, k_of(t + 2));
-                __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(LOADS));
-                slot_end();
-                products(_0, _1);
-            }
-        });
-    }
-    if (!second) slot_end();   // the other group's last products
-    __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));
-    slot_end();
-}
-
-// ------------------------------------------------------------ pinned order ---
 
 // The loop for blocks with one wave per SIMD and large wave tiles: the order of
 // products, LDS reads and direct loads is written out and pinned, since no
@@ -424,11 +264,15 @@ __device__ __forceinline__ void main_loop_two_groups(unsigned char *s0, unsigned
 // here: every wave has waited for its reads of tile t and for its direct loads
 // of tile t + 1, so afterwards the loads of tile t + 2 may overwrite the stage
 // and the first fragments of tile t + 1 may be read, both during step 1.  The
-// loads are issued in the first half of step 1 and waited for at the end of the
-// next step 0: three quarters of a tile and more cover their latency.
+// loads are spread over all of step 1 (in its first half they came faster than
+// the LDS takes them, and stood before the products: bf16 zeros, 4096 x 4096 x
+// 8192, 157 against 136 us) and waited for at the end of the next step 0.
+//
+// The products go in 2 x 2 blocks of fragments, each product sharing an operand
+// with the one before: 1.7% over rows of fragments at the board's power limit.
 template <class G>
 struct PinnedLoop {
-    static constexpr bool OK = G::STEPS == 2 && G::STAGES == 2 && G::N_MMA % 4 == 0;
+    static constexpr bool OK = G::STEPS == 2 && G::STAGES == 2 && G::FM % 2 == 0 && G::FN % 2 == 0;
     static constexpr int GROUPS = G::N_MMA / 4;        // of four products
     static constexpr int FRAGS = G::FM + G::FN;
 
@@ -450,37 +294,38 @@ struct PinnedLoop {
     }
 
     // One step: the products of `f`, with the fragments of `step` of `from`
-    // read into `next` and `loads(i)`, i < NL, issued between them.  The reads
-    // take the first three quarters of the groups, the loads the first half.
+    // read into `next` and `loads(i)`, i < NL, issued between them: the reads in
+    // the first three quarters of the groups, the loads in all.
     template <int NL, class Load>
     static __device__ __forceinline__ void step(const Frags16<G> &f, const unsigned char *from,
                                                 const BlockCtx<G> &c, int s, Frags16<G> &next,
                                                 floatx4 (&acc)[G::FM][G::FN], Load &&loads)
     {
-        constexpr int GR = GROUPS * 3 / 4 > 0 ? GROUPS * 3 / 4 : 1, GL = GROUPS;
+        constexpr int GR = GROUPS * 3 / 4 > 0 ? GROUPS * 3 / 4 : 1;
         static_for<0, GROUPS>([&](auto g_c) {
             constexpr int g = decltype(g_c)::value;
-            if constexpr (g < GL)
-                static_for<NL * g / GL, NL *(g + 1) / GL>([&](auto i) { loads(i); });
+            static_for<NL * g / GROUPS, NL *(g + 1) / GROUPS>([&](auto i) { loads(i); });
             if constexpr (g < GR)
                 static_for<FRAGS * g / GR, FRAGS *(g + 1) / GR>(
                     [&](auto n) { read<decltype(n)::value>(from, c, s, next); });
-#pragma unroll
-            for (int m = 4 * g; m < 4 * g + 4; ++m) {
-                const int Q = m / 4, I = Q / (G::FN / 2) * 2 + (m & 3) / 2, J = Q % (G::FN / 2) * 2 + (((m & 3) == 1 || (m & 3) == 2) ? 1 : 0);
-                floatx4 &sum = acc[I][J];
-                sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, f.a[I]),
-                                                              __builtin_bit_cast(bf16x8, f.b[J]), sum,
-                                                              0, 0, 0);
-            }
+            // block g: (0, 0) (0, 1) (1, 1) (1, 0) of fragments 2 x 2
+            static_for<0, 4>([&](auto m_c) {
+                constexpr int m = decltype(m_c)::value;
+                constexpr int i = g / (G::FN / 2) * 2 + m / 2;
+                constexpr int j = g % (G::FN / 2) * 2 + (m == 1 || m == 2 ? 1 : 0);
+                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, f.a[i]),
+                                                                    __builtin_bit_cast(bf16x8, f.b[j]),
+                                                                    acc[i][j], 0, 0, 0);
+            });
             __builtin_amdgcn_sched_barrier(0);
         });
     }
 };
 
 // Whole k-tiles [0, ntiles), ntiles > 0, from k_first, through 16-byte direct
-// loads.  On entry no wave may read or load any stage; on exit no load is in
-// flight and all waves have passed a barrier after their last read.
+// loads, in the order c.rot, c.rot + 1, .. of the tiles taken round.  On entry
+// no wave may read or load any stage; on exit no load is in flight and all
+// waves have passed a barrier after their last read.
 template <class G>
 __device__ __forceinline__ void main_loop_pinned(unsigned char *s0, unsigned char *s1, const BlockCtx<G> &c,
                                                  int k_first, int ntiles, floatx4 (&acc)[G::FM][G::FN])
@@ -495,8 +340,13 @@ __device__ __forceinline__ void main_loop_pinned(unsigned char *s0, unsigned cha
     tile_offsets(c.tid >> 6, c.lane, c.lda, c.bm, c.M, o.a);
     tile_offsets(c.tid >> 6, c.lane, c.ldb, c.bn, c.N, o.b);
     const uint32_t wave = __builtin_amdgcn_readfirstlane(c.tid >> 6);
-    // past the last tile the loads repeat it: in bounds, and never read
-    auto k_of = [&](int t) { return k_first + min(t, ntiles - 1) * G::BK; };
+    // the t-th tile visited, from tile c.rot on; past the last one the loads
+    // repeat it: in bounds, and never read
+    const int rot = c.rot % ntiles;
+    auto k_of = [&](int t) {
+        const int u = min(t, ntiles - 1) + rot;
+        return k_first + (u >= ntiles ? u - ntiles : u) * G::BK;
+    };
     Frags16<G> f0, f1;
 
     direct_tile_load(st[0], c, o, k_of(0));
