@@ -3,6 +3,8 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cmath>
+#include <cstring>
 
 #include "gemm_internal.hpp"
 #include "gemm_linear.h"
@@ -43,90 +45,180 @@ bool valid_operands(const gemm_linear_params *p)
            p->stride_w >= (wrows - 1) * p->ldw + wrow;
 }
 
-// The entry and the slices of the summed axis of one product.
+// The entry and the slices of the summed axis of one product, and what it
+// needs of the workspace.
 struct Plan {
     int cfg = -1;
     int form = 0;
     int splits = 1;
     int64_t tiles_m = 0;   // row tiles: exact, or (grouped) the most there can be
     int64_t tiles_n = 0;
+    // copies of x and w (of the second form: x and dz) with 16-byte rows: pitch
+    // in elements (0: none) and place in the workspace
+    int64_t copy_x = 0, copy_w = 0, at_x = 0, at_w = 0;
     int64_t ws_bytes = 0;
 };
 
-int index_of(int dtype, int bm, int bn, int form)
+// Estimated time in us of entry c on a product of `tiles` output tiles over K,
+// cut into s slices: rounds of blocks over the compute units, k-tiles at the
+// rate of a full unit or of a block alone, whichever is longer, and the reduce.
+// The entries' constants, the reduce's 3.5 us + bytes / 4.6 TB/s and the model's
+// form were fitted to 17000 measurements (every entry, 1 to 16 slices, M 40 to
+// 4096, N 256 to 8192, K 512 to 8192, all forms): the choice by the model is
+// 2.4% (bf16) and 1.6% (fp32) slower in the mean than the best of all.
+double estimate(const LinearConfig &c, double tiles, int64_t out, int64_t K, int64_t s, int64_t cus, int es)
 {
-    int count = 0;
-    const LinearConfig *tab = linear_configs(dtype, &count);
-    for (int i = 0; i < count; ++i)
-        if (tab[i].bm == bm && (bn == 0 || tab[i].bn == bn) && tab[i].fn[form][0] != nullptr) return i;
-    return -1;
+    const double blocks = tiles * (double)s;
+    const int64_t per_cu = std::min<int64_t>(8, int64_t(160 * 1024) / ((int64_t)c.stages * (c.bm + c.bn) * c.bk * es));
+    const double ktiles = (double)ceil_div(K, c.bk * s);
+    double busy = std::max(1.0, std::ceil(blocks / (double)cus));   // blocks of the fullest unit
+    double rounds = std::ceil(busy / (double)per_cu);
+    if (es == 2 && c.bm == 256) {   // pieces in the last round (xcd_piece)
+        const double whole = std::floor(blocks / (double)cus), rest = blocks - whole * (double)cus;
+        busy = rounds = whole + (rest <= 0 ? 0.0 : 4 * rest <= cus ? 0.4 : 2 * rest <= cus ? 0.6 : 1.0);
+    }
+    double t = 3.0 + c.block * rounds + ktiles * std::max(c.step * busy, c.alone * rounds);
+    if (s > 1) t += 3.5 + 0.1 * (double)s + (double)s * (double)out * 8.0 / 4.6e6;
+    return t;
 }
 
-// M x N output tiles of a (the groups') product over a summed extent K.
-Plan make_plan(const gemm_linear_params &p, bool wgrad)
+// The same for the kernel for few rows: a compute unit streams 38 KB per us of
+// weights and x (measured: 33 to 49), whatever the strip's width.
+double estimate_rows(const LinearConfig &c, double tiles, int64_t N, int64_t K, double rows, int64_t cus, int es)
+{
+    const double busy = std::ceil(std::max(1.0, tiles * (double)ceil_div(N, c.bn)) / (double)cus);
+    return 3.3 + busy * ((double)c.bn + std::min(rows, 16.0)) * (double)K * es / 38e3;
+}
+
+Plan find_plan(const gemm_linear_params &p, bool wgrad, int64_t cus)
 {
     Plan pl;
-    const int64_t cus = device_compute_units();
     pl.form = wgrad ? FORM_WGRAD : p.transw == GEMM_OP_T ? FORM_T : FORM_N;
     const int64_t groups = std::max<int64_t>(1, p.groups);
-    const bool grouped = p.groups > 0;
+    const bool grouped = p.groups > 0, turned = wgrad && p.transw == GEMM_OP_T;
     // extents of one group's product, its rows at the average
-    const int64_t M = wgrad ? (p.transw == GEMM_OP_T ? p.N : p.K) : p.rows;
-    const int64_t N = wgrad && p.transw == GEMM_OP_T ? p.K : p.N;
+    const int64_t M = wgrad ? (turned ? p.N : p.K) : p.rows;
+    const int64_t N = turned ? p.K : p.N;
     const int64_t K = wgrad ? ceil_div(p.rows, groups) : p.K;
+    const int es = size_of(p.dtype);
+    const double per = (double)p.rows / (double)groups;
+    // Row tiles to expect.  Of a group's rows the last tile is half full on
+    // average; groups of few rows (counts spread like Poisson's) have one
+    // unless they are empty.
+    auto row_tiles = [&](int64_t bm) -> double {
+        if (wgrad) return (double)(groups * ceil_div(M, bm));
+        if (!grouped) return (double)ceil_div(M, bm);
+        return std::max(std::max(1.0, (double)groups * (1.0 - std::exp(-per))),
+                        (double)M / (double)bm + 0.5 * (double)std::min(groups, M));
+    };
+    const int64_t out = (wgrad ? groups * M : p.rows) * N;   // outputs
     int count = 0;
     const LinearConfig *tab = linear_configs(p.dtype, &count);
-    // expected row tiles: a group's last tile is half full on average
-    auto row_tiles = [&](int bm) {
-        return wgrad ? groups * ceil_div(M, bm)
-                     : grouped ? std::max<int64_t>(1, M / bm + std::min(groups, M) / 2) : ceil_div(M, bm);
-    };
-    if (t_cfg >= 0) {
-        pl.cfg = t_cfg < count && tab[t_cfg].fn[pl.form][0] != nullptr ? t_cfg : -1;
-        if (pl.cfg < 0) return pl;
-    } else {
-        const int64_t per = wgrad ? M : grouped ? ceil_div(M, groups) : M;
-        if (!wgrad && per <= 16 && !(grouped && per > 8)) {
-            // strips as wide as still give every compute unit a block
-            pl.cfg = index_of(p.dtype, 16, 0, pl.form);
-            for (int i = pl.cfg + 1; i > 0 && i < count; ++i)
-                if (tab[i].bm == 16 && tab[i].fn[pl.form][0] != nullptr &&
-                    row_tiles(16) * ceil_div(N, tab[i].bn) >= (pl.form == FORM_T ? 2 * cus : cus))
-                    pl.cfg = i;
-        } else if (!wgrad && per <= 32)
-            pl.cfg = index_of(p.dtype, 32, p.dtype == GEMM_DTYPE_F32 ? 128 : 256, pl.form);
-        else if (row_tiles(256) * ceil_div(N, 256) >= cus * 3 / 4 && (wgrad || per >= 192))
-            pl.cfg = index_of(p.dtype, 256, 256, pl.form);
-        else if (row_tiles(128) * ceil_div(N, 128) >= cus * 3 / 4 && (wgrad || per >= 96))
-            pl.cfg = index_of(p.dtype, 128, 128, pl.form);
-        else
-            pl.cfg = index_of(p.dtype, 64, 64, pl.form);
-        if (pl.cfg < 0) return pl;
+    double best = 0.0;
+    for (int i = 0; i < count; ++i) {
+        const LinearConfig &c = tab[i];
+        if (c.fn[pl.form][0] == nullptr || (t_cfg >= 0 && i != t_cfg)) continue;
+        if (c.stages == 0) {
+            const double t = estimate_rows(c, row_tiles(16), N, K, per, cus, es);
+            if (pl.cfg < 0 || t < best) {
+                pl.cfg = i;
+                pl.splits = 1;
+                best = t;
+            }
+            continue;
+        }
+        const int64_t ktiles = std::max<int64_t>(1, ceil_div(K, c.bk));
+        static const int slices[] = {1, 2, 3, 4, 6, 8, 12, 16};
+        for (int want : slices) {
+            if (t_split > 0) want = t_split;
+            int64_t s = std::min<int64_t>(want, std::min<int64_t>(ktiles, 64));
+            if (!wgrad) s = ceil_div(ktiles, ceil_div(ktiles, s));   // every slice has a k-tile
+            const double t = estimate(c, row_tiles(c.bm) * (double)ceil_div(N, c.bn), out, K, s, cus, es);
+            if (pl.cfg < 0 || t < best) {
+                pl.cfg = i;
+                pl.splits = (int)s;
+                best = t;
+            }
+            if (t_split > 0 || want >= ktiles) break;
+        }
     }
+    if (pl.cfg < 0) return pl;
     const LinearConfig &c = tab[pl.cfg];
     pl.tiles_n = ceil_div(N, c.bn);
     pl.tiles_m = wgrad ? ceil_div(M, c.bm)
                        : grouped ? M / c.bm + std::min(groups, M) : ceil_div(M, c.bm);
-    if (c.stages == 0) return pl;
-    const int64_t tiles = row_tiles(c.bm) * pl.tiles_n;
-    const int64_t ktiles = ceil_div(K, c.bk);
-    int64_t s = 1;
-    if (t_split > 0)
-        s = t_split;
-    else if (tiles > 0 && tiles < cus)
-        s = std::min(ceil_div(2 * cus, tiles), ktiles / 4);
-    s = std::max<int64_t>(1, std::min<int64_t>(s, std::max<int64_t>(ktiles, 1)));
-    s = std::min<int64_t>(s, 64);
-    if (!wgrad) s = std::max<int64_t>(1, ceil_div(ktiles, ceil_div(std::max<int64_t>(ktiles, 1), s)));
-    pl.splits = (int)s;
-    if (s > 1) pl.ws_bytes = s * (wgrad ? groups * M : p.rows) * N * 4;
+    if (pl.splits > 1) pl.ws_bytes = (pl.splits * out * 4 + 255) / 256 * 256;
+
+    // bf16 operands without 16-byte rows lose the wide direct loads: in place,
+    // rows at 4-byte boundaries take 1.45 times as long, others 3.5 times
+    // (2048^3: 23 us against 32 and 81 to 108).  Where that costs more than
+    // copying them into rows of 16-byte pitch first (a launch, and a pass at 3
+    // TB/s over each), they are copied.  fp32 operands lose 10% at most.
+    if (p.dtype == GEMM_DTYPE_BF16 && c.stages > 0 && t_cfg < 0 && K > 0 && out > 0) {
+        const int64_t x_ld = p.ldx, w_ld = wgrad ? p.N : p.ldw;   // dz: see weight_grad
+        const int64_t w_rows = wgrad ? p.rows : groups * (p.transw == GEMM_OP_T ? p.N : p.K);
+        const int64_t w_cols = wgrad ? p.N : p.transw == GEMM_OP_T ? p.K : p.N;
+        // the groups' weights as one matrix
+        const bool w_one = wgrad || groups == 1 || p.stride_w == w_rows / groups * p.ldw;
+        const bool x_odd = x_ld % 8 != 0, w_odd = w_ld % 8 != 0 || (!wgrad && groups > 1 && p.stride_w % 8 != 0);
+        const bool halves = ((x_ld | w_ld) & 1) != 0;
+        const int64_t px = ceil_div(p.K, 8) * 8, pw = ceil_div(w_cols, 8) * 8;
+        const double copy = (x_odd ? 3.0 + (double)p.rows * (double)px * 4.0 / 3e6 : 0.0) +
+                            (w_odd ? 3.0 + (double)w_rows * (double)pw * 4.0 / 3e6 : 0.0);
+        if ((x_odd || w_odd) && (!w_odd || w_one) && copy < best * (halves ? 2.5 : 0.45)) {
+            if (x_odd) {
+                pl.copy_x = px;
+                pl.at_x = pl.ws_bytes;
+                pl.ws_bytes += (p.rows * px * 2 + 255) / 256 * 256;
+            }
+            if (w_odd) {
+                pl.copy_w = pw;
+                pl.at_w = pl.ws_bytes;
+                pl.ws_bytes += w_rows * pw * 2;
+            }
+        }
+    }
     return pl;
+}
+
+// Plans by their parameters, a few per thread: a call asks for the workspace
+// size first, and the next call is often the same.
+Plan make_plan(const gemm_linear_params &p, bool wgrad)
+{
+    struct Known {
+        bool set = false, wgrad = false;
+        int cfg = 0, split = 0;
+        int64_t cus = 0;
+        gemm_linear_params p{};
+        Plan plan;
+    };
+    thread_local Known known[16];
+    thread_local unsigned next = 0;
+    const int64_t cus = device_compute_units();
+    for (Known &k : known)
+        if (k.set && k.wgrad == wgrad && k.cfg == t_cfg && k.split == t_split && k.cus == cus &&
+            std::memcmp(&k.p, &p, sizeof p) == 0)
+            return k.plan;
+    Known &k = known[next++ % 16];
+    k = Known{true, wgrad, t_cfg, t_split, cus, p, find_plan(p, wgrad, cus)};
+    return k.plan;
 }
 
 bool aligned16(const void *p, int64_t ld, int64_t stride, int dtype)
 {
     const int64_t vec = 16 / size_of(dtype);
     return (uintptr_t)p % 16 == 0 && ld % vec == 0 && stride % vec == 0;
+}
+
+// Copies `rows` rows of `cols` bf16 values to rows of `pitch` in the workspace.
+int copy_rows(const void **m, int64_t *ld, int64_t rows, int64_t cols, int64_t pitch, void *workspace,
+              int64_t at, hipStream_t stream)
+{
+    void *to = static_cast<char *>(workspace) + at;
+    if (launch_stage_rows(*m, *ld, rows, cols, 2, to, pitch, stream) != hipSuccess) return GEMM_ERR_HIP;
+    *m = to;
+    *ld = pitch;
+    return GEMM_OK;
 }
 
 int launch_plan(const Plan &pl, int dtype, LinearArgs &a, bool wgrad, void *workspace, hipStream_t stream)
@@ -170,15 +262,24 @@ bool valid_workspace(const void *ws, int64_t bytes, int64_t need)
 
 // Scratch of the bias gradient: one row of N sums per chunk of rows, when
 // there is more than one chunk.
+//
+// A chunk has 64 rows, or 16 where 64 would leave fewer than two blocks per
+// compute unit (777 x 1025 fp32: 19 us with 65 blocks of 64 rows).
+int act_grad_rows(const gemm_linear_params &p)
+{
+    const int64_t blocks = ceil_div(p.rows, 64) * ceil_div(p.N, p.dtype == GEMM_DTYPE_F32 ? 256 : 512);
+    return p.rows > 64 && blocks < 512 ? 16 : 64;
+}
+
 int64_t act_grad_chunks(const gemm_linear_params &p)
 {
-    return p.groups > 0 ? p.rows / kActGradRows + std::min(p.groups, p.rows)
-                        : ceil_div(p.rows, kActGradRows);
+    const int64_t rows = act_grad_rows(p);
+    return p.groups > 0 ? p.rows / rows + std::min(p.groups, p.rows) : ceil_div(p.rows, rows);
 }
 
 int64_t act_grad_bytes(const gemm_linear_params &p)
 {
-    if (p.groups == 0 && p.rows <= kActGradRows && p.rows > 0) return 0;
+    if (p.groups == 0 && act_grad_chunks(p) == 1) return 0;
     return std::max<int64_t>(16, act_grad_chunks(p) * p.N * 4);
 }
 
@@ -215,10 +316,21 @@ int linear(const gemm_linear_params *p, const void *x, const void *w, const int3
     LinearArgs a{};
     a.x = x;
     a.w = w;
-    a.offsets = p->groups > 0 ? offsets : nullptr;
     a.ldx = p->ldx;
     a.ldw = p->ldw;
     a.stride_w = p->groups > 0 ? p->stride_w : 0;
+    if (pl.copy_x) {
+        const int rc = copy_rows(&a.x, &a.ldx, p->rows, p->K, pl.copy_x, workspace, pl.at_x, stream);
+        if (rc != GEMM_OK) return rc;
+    }
+    if (pl.copy_w) {
+        const int64_t rows = p->transw == GEMM_OP_T ? p->N : p->K;
+        const int rc = copy_rows(&a.w, &a.ldw, rows * std::max<int64_t>(1, p->groups),
+                                 p->transw == GEMM_OP_T ? p->K : p->N, pl.copy_w, workspace, pl.at_w, stream);
+        if (rc != GEMM_OK) return rc;
+        if (p->groups > 0) a.stride_w = rows * pl.copy_w;
+    }
+    a.offsets = p->groups > 0 ? offsets : nullptr;
     a.stride_bias = p->groups > 0 ? p->stride_bias : 0;
     a.rows = a.M = (int)p->rows;
     a.N = (int)p->N;
@@ -268,8 +380,8 @@ int act_grad(const gemm_linear_params *p, const void *dy, int64_t lddy, const vo
             (!act || p->dtype_y != p->dtype || aligned16(pre, p->ldp, 0, p->dtype_y));
     const int64_t chunks = act_grad_chunks(*p);
     a.chunks = (int)chunks;
-    if (chunks * ceil_div(p->N, a.bf16 ? 512 : 256) > INT32_MAX ||
-        a.groups * ceil_div(p->N, 256) > INT32_MAX)
+    a.chunk_rows = act_grad_rows(*p);
+    if (chunks * ceil_div(p->N, 64) > INT32_MAX || a.groups * ceil_div(p->N, 64) > INT32_MAX)
         return GEMM_ERR_INVALID_ARG;
     return launch_act_grad(a, stream) == hipSuccess ? GEMM_OK : GEMM_ERR_HIP;
 }
@@ -293,11 +405,21 @@ int weight_grad(const gemm_linear_params *p, const void *x, const void *dz, int6
     if (empty) return GEMM_OK;
     if (const int rc = need_device()) return rc;
     const bool t = p->transw == GEMM_OP_T;   // dw^T = dz^T . x
+    int64_t ldx = p->ldx;
+    if (pl.copy_x) {
+        const int rc = copy_rows(&x, &ldx, p->rows, p->K, pl.copy_x, workspace, pl.at_x, stream);
+        if (rc != GEMM_OK) return rc;
+    }
+    // planned for dz at a pitch of N: a wider one may have 16-byte rows as it is
+    if (pl.copy_w && lddz % 8 != 0) {
+        const int rc = copy_rows(&dz, &lddz, p->rows, p->N, pl.copy_w, workspace, pl.at_w, stream);
+        if (rc != GEMM_OK) return rc;
+    }
     LinearArgs a{};
     a.x = t ? dz : x;
     a.w = t ? x : dz;
-    a.ldx = t ? lddz : p->ldx;
-    a.ldw = t ? p->ldx : lddz;
+    a.ldx = t ? lddz : ldx;
+    a.ldw = t ? ldx : lddz;
     a.offsets = p->groups > 0 ? offsets : nullptr;
     a.stride_c = p->groups > 0 ? p->stride_w : 0;
     a.rows = (int)q.rows;

@@ -74,71 +74,96 @@ __global__ void __launch_bounds__(256) linear_reduce_kernel(LinearArgs p)
 }
 
 // dz = dy act'(pre), and each column's sum over the chunk's rows.  A block
-// takes one chunk of kActGradRows rows of one group and 64 V columns: its four
-// waves walk the rows in turn, a lane holding V columns (16 bytes of a row),
-// so a wave reads 1 KiB of a row at a time and every byte once; the sums meet
-// in LDS.  Bound by HBM: 2 reads and 1 write of rows x N.
-template <bool BF16>
+// takes one chunk of rows of one group and 64 V columns: its four waves walk
+// the rows in turn, V columns per lane; the sums meet in LDS.  Bound by HBM: 2
+// reads and 1 write of rows x N.  16-byte rows are taken 16 bytes per lane (1
+// KiB of a row per wave), others with the lanes side by side, element by
+// element.  V == 1 spreads few columns over more blocks.
+template <bool BF16, int V>
 __global__ void __launch_bounds__(256) act_grad_kernel(ActGradArgs p, int col_blocks)
 {
-    constexpr int V = BF16 ? 8 : 4;
+    constexpr bool WIDE = V > 1;
     __shared__ float sums[4][64 * V];
     const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
-    const GroupRows list(p.offsets, p.groups, p.rows, kActGradRows, lane);
+    const GroupRows list(p.offsets, p.groups, p.rows, p.chunk_rows, lane);
     const int tile = (int)blockIdx.x / col_blocks, cb = (int)blockIdx.x - tile * col_blocks;
     if (tile >= list.total) return;
     int group, lo, m, tm;
-    list.find(p.offsets, p.groups, p.rows, kActGradRows, lane, 0, false, tile, group, lo, m, tm);
-    const int col = (cb * 64 + lane) * V, n = p.N - col;
-    const int first = tm * kActGradRows, count = min(kActGradRows, m - first);
+    list.find(p.offsets, p.groups, p.rows, p.chunk_rows, lane, 0, false, tile, group, lo, m, tm);
+    const int col0 = cb * 64 * V, first = tm * p.chunk_rows, count = min(p.chunk_rows, m - first);
+    // lane's columns: V in a row, or every 64th
+    const bool vec = WIDE && p.vec != 0;
+    auto column = [&](int i) { return vec ? lane * V + i : lane + 64 * i; };
+    auto load = [&](const void *X, int64_t at, bool bf16, float (&v)[V]) {
+        const int n = p.N - col0 - lane * V;
+        if (vec && bf16 == BF16 && n >= V) {
+            load_out<V, WIDE>(X, at + lane * V, V, BF16, true, v);
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const int64_t j = at + column(i);
+                v[i] = col0 + column(i) >= p.N ? 0.0f
+                       : bf16 ? __uint_as_float((uint32_t) static_cast<const uint16_t *>(X)[j] << 16)
+                              : static_cast<const float *>(X)[j];
+            }
+        }
+    };
     float s[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) s[i] = 0.0f;
-    if (n > 0) {
 #pragma unroll 4
-        for (int r = wave; r < count; r += 4) {
-            const int64_t row = lo + first + r;
-            float g[V], z[V];
-            load_out<V>(p.dy, row * p.lddy + col, n, BF16, p.vec != 0, g);
-            if (p.act != ACT_NONE) {
-                if (BF16 == (p.pre_bf16 != 0))
-                    load_out<V>(p.pre, row * p.ldp + col, n, BF16, p.vec != 0, z);
-                else   // another type than dy's: element by element
-                    load_out<V>(p.pre, row * p.ldp + col, n, !BF16, false, z);
-                act_slope<V>(p.act, z);
+    for (int r = wave; r < count; r += 4) {
+        const int64_t row = lo + first + r;
+        float g[V], z[V];
+        load(p.dy, row * p.lddy + col0, BF16, g);
+        if (p.act != ACT_NONE) {
+            load(p.pre, row * p.ldp + col0, p.pre_bf16 != 0, z);
+            act_slope<V>(p.act, z);
 #pragma unroll
-                for (int i = 0; i < V; ++i) g[i] *= z[i];
+            for (int i = 0; i < V; ++i) g[i] *= z[i];
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) s[i] += col0 + column(i) < p.N ? g[i] : 0.0f;
+        if (p.dz == nullptr) continue;
+        const int64_t at = row * p.lddz + col0;
+        if (vec && p.N - col0 - lane * V >= V) {
+            store_outs<V, WIDE>(p.dz, at + lane * V, V, BF16, true, g);
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                if (col0 + column(i) >= p.N) continue;
+                if (BF16)
+                    static_cast<uint16_t *>(p.dz)[at + column(i)] = f32_to_bf16_rne(g[i]);
+                else
+                    static_cast<float *>(p.dz)[at + column(i)] = g[i];
             }
-#pragma unroll
-            for (int i = 0; i < V; ++i) s[i] += i < n ? g[i] : 0.0f;
-            if (p.dz != nullptr) store_outs<V>(p.dz, row * p.lddz + col, n, BF16, p.vec != 0, g);
         }
     }
     if (p.dbias == nullptr) return;
 #pragma unroll
-    for (int i = 0; i < V; ++i) sums[wave][lane * V + i] = s[i];
+    for (int i = 0; i < V; ++i) sums[wave][column(i)] = s[i];
     __syncthreads();
     // one chunk in all (dense, few rows): the sums are the result
     float *out = p.ws != nullptr ? p.ws + (int64_t)tile * p.N : p.dbias;
-    for (int i = (int)threadIdx.x; i < 64 * V; i += 256) {
-        const int j = cb * 64 * V + i;
-        if (j < p.N) out[j] = sums[0][i] + sums[1][i] + sums[2][i] + sums[3][i];
-    }
+    for (int i = (int)threadIdx.x; i < 64 * V; i += 256)
+        if (col0 + i < p.N) out[col0 + i] = sums[0][i] + sums[1][i] + sums[2][i] + sums[3][i];
 }
 
-// dbias of one group: its chunks' sums in order (none: zero).
+// dbias of one group: its chunks' sums (none: zero).  Four threads per column
+// take every fourth chunk each, in order.
 __global__ void __launch_bounds__(256) bias_reduce_kernel(ActGradArgs p, int col_blocks)
 {
-    const int lane = (int)threadIdx.x & 63;
+    __shared__ float sums[4][64];
+    const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
     const int group = (int)blockIdx.x / col_blocks, cb = (int)blockIdx.x - group * col_blocks;
     int first = 0, mine = 0;   // the group's first chunk, and its chunks
     if (p.offsets == nullptr) {
-        mine = (p.rows + kActGradRows - 1) / kActGradRows;
+        mine = (p.rows + p.chunk_rows - 1) / p.chunk_rows;
     } else {
         for (int base = 0; base <= group; base += 64) {
             int lo, m;
-            const int t = GroupRows::lane_tiles(p.offsets, base + lane, p.groups, p.rows, kActGradRows, 0, false,
-                                                 lo, m);
+            const int t = GroupRows::lane_tiles(p.offsets, base + lane, p.groups, p.rows, p.chunk_rows, 0,
+                                                false, lo, m);
             const int upto = GroupRows::scan(t, lane);
             const int at = min(63, group - base);   // the group itself, or the last of these 64
             first += __builtin_amdgcn_readlane(upto, at);
@@ -150,13 +175,17 @@ __global__ void __launch_bounds__(256) bias_reduce_kernel(ActGradArgs p, int col
         first = min(first, p.chunks);
         mine = min(mine, p.chunks - first);
     }
-    const int j = cb * 256 + (int)threadIdx.x;
-    if (j >= p.N) return;
+    const int j = cb * 64 + lane;
     const float *w = p.ws + (int64_t)first * p.N + j;
     float s = 0.0f;
+    if (j < p.N) {
 #pragma unroll 8
-    for (int t = 0; t < mine; ++t) s += w[(int64_t)t * p.N];
-    p.dbias[(int64_t)group * p.N + j] = s;
+        for (int t = wave; t < mine; t += 4) s += w[(int64_t)t * p.N];
+    }
+    sums[wave][lane] = s;
+    __syncthreads();
+    if (wave == 0 && j < p.N)
+        p.dbias[(int64_t)group * p.N + j] = sums[0][lane] + sums[1][lane] + sums[2][lane] + sums[3][lane];
 }
 
 unsigned grid_of(int64_t work)
@@ -187,17 +216,20 @@ hipError_t launch_linear_reduce(const LinearArgs &a, bool weight_grad, hipStream
 
 hipError_t launch_act_grad(const ActGradArgs &a, hipStream_t stream)
 {
-    const int V = a.bf16 ? 8 : 4;
-    const int64_t tiles = a.chunks;
+    const int W = a.bf16 ? 8 : 4;
+    // 16 bytes per lane, unless that leaves most of the chip idle
+    const bool wide = (int64_t)a.chunks * ((a.N + 64 * W - 1) / (64 * W)) >= 64;
+    const int V = wide ? W : 1;
     const int col_blocks = (a.N + 64 * V - 1) / (64 * V);
-    if (tiles > 0) {
-        hipLaunchKernelGGL((a.bf16 ? act_grad_kernel<true> : act_grad_kernel<false>),
-                           dim3((unsigned)(tiles * col_blocks)), dim3(256), 0, stream, a, col_blocks);
+    if (a.chunks > 0) {
+        auto kernel = a.bf16 ? (wide ? act_grad_kernel<true, 8> : act_grad_kernel<true, 1>)
+                             : (wide ? act_grad_kernel<false, 4> : act_grad_kernel<false, 1>);
+        hipLaunchKernelGGL(kernel, dim3((unsigned)(a.chunks * col_blocks)), dim3(256), 0, stream, a, col_blocks);
         const hipError_t err = hipGetLastError();
         if (err != hipSuccess) return err;
     }
     if (a.dbias != nullptr && a.ws != nullptr) {
-        const int cb = (a.N + 255) / 256;
+        const int cb = (a.N + 63) / 64;
         hipLaunchKernelGGL(bias_reduce_kernel, dim3((unsigned)(cb * a.groups)), dim3(256), 0, stream, a, cb);
         return hipGetLastError();
     }

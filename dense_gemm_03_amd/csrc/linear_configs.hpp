@@ -2,9 +2,11 @@
 // for y = x . w (w as K x N, or as N x K) and for dw = x^T . dz, each for
 // 16-byte aligned rows and for any alignment of the element type.
 //
-//   X(NAME, BF16, BM, BN, BK, WM, WN, STAGES, GROUP_M, FORMS)
+//   X(NAME, BF16, BM, BN, BK, WM, WN, STAGES, GROUP_M, STEP, ALONE, BLOCK)
 //
-// FORMS = FWD (both forms of x . w), WG (x^T . dz) or ALL.
+// The last three are times in us that the dispatcher ranks the entries by
+// (linear_api.hip): of a k-tile per block on a full compute unit, of a k-tile
+// of a block that has the unit to itself, and of a block's start and end.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -22,6 +24,7 @@ enum { FORM_N = 0, FORM_T = 1, FORM_WGRAD = 2 };
 
 struct LinearConfig {
     const char *name;
+    float step, alone, block;
     int bm, bn, bk, threads, stages, group_m;   // stages == 0: the kernel for few rows
     linear_fn fn[3][2];   // by form; [0] aligned, [1] not; nullptr where there is none
 };
@@ -37,38 +40,27 @@ hipError_t launch_linear(const LinearArgs &args, int blocks, hipStream_t stream)
 #define DG_LIN_LX_W ::dg::MNMAJOR
 #define DG_LIN_LW_W ::dg::MNMAJOR
 
-#define DG_LIN_F32_TABLE(X)                                                  \
-    X("f32_256x256x32_w4x2_s2", false, 256, 256, 32, 4, 2, 2, 8, ALL)        \
-    X("f32_128x128x32_w2x2_s2", false, 128, 128, 32, 2, 2, 2, 8, ALL)        \
-    X("f32_256x128x32_w4x2_s2", false, 256, 128, 32, 4, 2, 2, 8, ALL)        \
-    X("f32_128x64x32_w2x2_s2", false, 128, 64, 32, 2, 2, 2, 8, ALL)        \
-    X("f32_64x64x32_w2x2_s2", false, 64, 64, 32, 2, 2, 2, 8, ALL)        \
-    X("f32_64x128x32_w2x2_s2", false, 64, 128, 32, 2, 2, 2, 8, ALL)        \
-    X("f32_64x64x32_w2x2_s3", false, 64, 64, 32, 2, 2, 3, 8, ALL)            \
-    X("f32_32x128x32_w1x4_s3", false, 32, 128, 32, 1, 4, 3, 1, FWD)
+#define DG_LIN_F32_TABLE(X)                                                                  \
+    X("f32_256x256x32_w4x2_s2", false, 256, 256, 32, 4, 2, 2, 8, 7.03f, 0.8f, 6.0f)          \
+    X("f32_128x128x32_w2x2_s2", false, 128, 128, 32, 2, 2, 2, 8, 1.87f, 1.2f, 4.0f)          \
+    X("f32_64x64x32_w2x2_s3", false, 64, 64, 32, 2, 2, 3, 8, 0.48f, 0.51f, 0.83f)
 
-#define DG_LIN_BF16_TABLE(X)                                                 \
-    X("bf16_256x256x64_w2x2_s2", true, 256, 256, 64, 2, 2, 2, 8, ALL)        \
-    X("bf16_128x128x64_w2x2_s2", true, 128, 128, 64, 2, 2, 2, 8, ALL)        \
-    X("bf16_64x128x64_w1x4_s2", true, 64, 128, 64, 1, 4, 2, 8, ALL)        \
-    X("bf16_64x64x64_w2x2_s2", true, 64, 64, 64, 2, 2, 2, 8, ALL)            \
-    X("bf16_32x256x64_w1x4_s2", true, 32, 256, 64, 1, 4, 2, 1, FWD)          \
-    X("bf16_32x128x64_w1x4_s2", true, 32, 128, 64, 1, 4, 2, 1, FWD)
+#define DG_LIN_BF16_TABLE(X)                                                                 \
+    X("bf16_256x256x64_w2x2_s2", true, 256, 256, 64, 2, 2, 2, 8, 1.44f, 0.9f, 6.1f)          \
+    X("bf16_128x128x64_w2x2_s2", true, 128, 128, 64, 2, 2, 2, 8, 0.41f, 0.585f, 1.4f)        \
+    X("bf16_64x128x64_w1x4_s2", true, 64, 128, 64, 1, 4, 2, 8, 0.303f, 0.5f, 0.51f)          \
+    X("bf16_64x64x64_w2x2_s2", true, 64, 64, 64, 2, 2, 2, 8, 0.188f, 0.444f, 0.13f)
 
 // Entries for few rows: X(NAME, BF16, FORM (N or T), W, waves); 16 rows, 16 W columns.
 #define DG_LIN_F32_ROWS(X)                       \
     X("f32_rows_n_w2x8", false, N, 2, 8)         \
     X("f32_rows_n_w4x8", false, N, 4, 8)         \
-    X("f32_rows_n_w2x16", false, N, 2, 16)       \
-    X("f32_rows_t_w1x16", false, T, 1, 16)       \
     X("f32_rows_t_w1x8", false, T, 1, 8)         \
     X("f32_rows_t_w2x8", false, T, 2, 8)
 
 #define DG_LIN_BF16_ROWS(X)                      \
     X("bf16_rows_n_w2x8", true, N, 2, 8)         \
     X("bf16_rows_n_w4x8", true, N, 4, 8)         \
-    X("bf16_rows_n_w2x16", true, N, 2, 16)       \
-    X("bf16_rows_t_w1x16", true, T, 1, 16)       \
     X("bf16_rows_t_w1x8", true, T, 1, 8)         \
     X("bf16_rows_t_w2x8", true, T, 2, 8)
 
@@ -80,19 +72,16 @@ hipError_t launch_linear(const LinearArgs &args, int blocks, hipStream_t stream)
 #define DG_LIN_ROWS_FNS_N(...) {DG_LIN_ROWS_FN(__VA_ARGS__), DG_LIN_NOFNS, DG_LIN_NOFNS}
 #define DG_LIN_ROWS_FNS_T(...) {DG_LIN_NOFNS, DG_LIN_ROWS_FN(__VA_ARGS__), DG_LIN_NOFNS}
 #define DG_LIN_ROWS_ENTRY(NAME, BF16, F, W, WV) \
-    LinearConfig{NAME, 16, 16 * (W), 1, 64 * (WV), 0, 1, DG_LIN_ROWS_FNS_##F(BF16, F, W, WV)},
+    LinearConfig{NAME, 0, 0, 0, 16, 16 * (W), 1, 64 * (WV), 0, 1, DG_LIN_ROWS_FNS_##F(BF16, F, W, WV)},
 
 #define DG_LIN_FNS(BF16, BM, BN, BK, WM, WN, S, F)                                              \
     {&launch_linear<BF16, BM, BN, BK, WM, WN, S, DG_LIN_LX_##F, DG_LIN_LW_##F, true>,           \
      &launch_linear<BF16, BM, BN, BK, WM, WN, S, DG_LIN_LX_##F, DG_LIN_LW_##F, false>}
 #define DG_LIN_NOFNS {nullptr, nullptr}
-#define DG_LIN_FNS_ALL(...) \
-    {DG_LIN_FNS(__VA_ARGS__, N), DG_LIN_FNS(__VA_ARGS__, T), DG_LIN_FNS(__VA_ARGS__, W)}
-#define DG_LIN_FNS_FWD(...) {DG_LIN_FNS(__VA_ARGS__, N), DG_LIN_FNS(__VA_ARGS__, T), DG_LIN_NOFNS}
-#define DG_LIN_FNS_WG(...) {DG_LIN_NOFNS, DG_LIN_NOFNS, DG_LIN_FNS(__VA_ARGS__, W)}
-#define DG_LIN_ENTRY(NAME, BF16, BM, BN, BK, WM, WN, S, GM, FORMS)                              \
-    LinearConfig{NAME, BM, BN, BK, 64 * (WM) * (WN), S, GM,                                     \
-                 DG_LIN_FNS_##FORMS(BF16, BM, BN, BK, WM, WN, S)},
+#define DG_LIN_ENTRY(NAME, BF16, BM, BN, BK, WM, WN, S, GM, STEP, ALONE, BLOCK)                 \
+    LinearConfig{NAME, STEP, ALONE, BLOCK, BM, BN, BK, 64 * (WM) * (WN), S, GM,                 \
+                 {DG_LIN_FNS(BF16, BM, BN, BK, WM, WN, S, N), DG_LIN_FNS(BF16, BM, BN, BK, WM, WN, S, T), \
+                  DG_LIN_FNS(BF16, BM, BN, BK, WM, WN, S, W)}},
 
 const LinearConfig *linear_configs(int dtype, int *count);
 
@@ -100,6 +89,10 @@ const LinearConfig *linear_configs(int dtype, int *count);
 // epilogue: y (rows x N; rows outside the groups are left alone) or dw
 // (groups x M x N).
 hipError_t launch_linear_reduce(const LinearArgs &args, bool weight_grad, hipStream_t stream);
+
+// Copies a stored matrix into rows of a 16-byte pitch (gemm_aux.hip).
+hipError_t launch_stage_rows(const void *src, int64_t ld, int64_t rows, int64_t cols, int esize,
+                             void *dst, int64_t ldd, hipStream_t stream);
 
 // dz and dbias.
 struct ActGradArgs {
@@ -112,10 +105,9 @@ struct ActGradArgs {
     int rows, N, groups;
     int act, bf16, pre_bf16;
     int vec;                // rows of dy, pre and dz are 16-byte aligned
+    int chunk_rows;         // rows of one chunk of the sums
     int chunks;             // chunks that ws has room for: all that there can be
 };
-// Rows of one chunk of the bias gradient's sum.
-constexpr int kActGradRows = 64;
 hipError_t launch_act_grad(const ActGradArgs &args, hipStream_t stream);
 
 }  // namespace dg

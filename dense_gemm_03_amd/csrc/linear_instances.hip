@@ -26,18 +26,8 @@ hipError_t launch_linear(const LinearArgs &args, int blocks, hipStream_t stream)
     template hipError_t dg::launch_linear<BF16, BM, BN, BK, WM, WN, S, DG_LIN_LX_##F,            \
                                           DG_LIN_LW_##F, false>(const dg::LinearArgs &, int,     \
                                                                 hipStream_t);
-#define DG_LIN_INST_ALL_N(...) DG_LIN_INST(__VA_ARGS__, N)
-#define DG_LIN_INST_ALL_T(...) DG_LIN_INST(__VA_ARGS__, T)
-#define DG_LIN_INST_ALL_W(...) DG_LIN_INST(__VA_ARGS__, W)
-#define DG_LIN_INST_FWD_N(...) DG_LIN_INST(__VA_ARGS__, N)
-#define DG_LIN_INST_FWD_T(...) DG_LIN_INST(__VA_ARGS__, T)
-#define DG_LIN_INST_FWD_W(...)
-#define DG_LIN_INST_WG_N(...)
-#define DG_LIN_INST_WG_T(...)
-#define DG_LIN_INST_WG_W(...) DG_LIN_INST(__VA_ARGS__, W)
-#define DG_LIN_INST_SEL2(FORMS, F) DG_LIN_INST_##FORMS##_##F
-#define DG_LIN_INST_SEL(FORMS, F) DG_LIN_INST_SEL2(FORMS, F)
-#define DG_LIN_INST_ENTRY(NAME, BF16, BM, BN, BK, WM, WN, S, GM, FORMS) \
-    DG_LIN_INST_SEL(FORMS, DG_LIN_FORM)(BF16, BM, BN, BK, WM, WN, S)
+#define DG_LIN_INST_FORM2(BF16, BM, BN, BK, WM, WN, S, F) DG_LIN_INST(BF16, BM, BN, BK, WM, WN, S, F)
+#define DG_LIN_INST_ENTRY(NAME, BF16, BM, BN, BK, WM, WN, S, GM, STEP, ALONE, BLOCK) \
+    DG_LIN_INST_FORM2(BF16, BM, BN, BK, WM, WN, S, DG_LIN_FORM)
 
 DG_LIN_TABLE(DG_LIN_INST_ENTRY)

@@ -349,7 +349,9 @@ def _backward(dy, x, w, offsets, groups, act, pre, alpha, transb, out_dtype, nee
         dbias = at.empty((groups, N) if groups else (N,), torch.float32) if need_dbias else None
         dz, lddz = dy, lddy
         if act and (need_dx or need_dw):
-            dz, lddz = at.empty((rows, N), x.dtype), max(N, 1)
+            # rows of a 16-byte pitch, which the two products read best
+            lddz = max((N + 7) // 8 * 8, 1)
+            dz = at.empty((rows, lddz), x.dtype)
         if act or need_dbias:
             params = _block(dtype, dtype_pre, 0, 0, act, 1.0, rows, N, K, groups, 0, 0, 0, 0, ldp, 0, 0)
             need = lib.gemm_linear_act_grad_workspace_size(params) if need_dbias else 0

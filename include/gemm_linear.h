@@ -21,7 +21,7 @@
  * rows; it is read by the kernels alone (no host synchronisation), so the
  * counts may come from a router that still runs on the stream.  A group may be
  * empty.  Rows before offsets[0] and from offsets[groups] on belong to nobody:
- * they are neither read nor written.  Values outside 0 .. rows are clamped into
+ * their values are not used, and they are not written.  Values outside 0 .. rows are clamped into
  * it and a group that ends before it begins is taken as empty, so no access
  * leaves the arrays whatever offsets holds; with offsets that fall, the results
  * of the rows between the smallest and the largest of them are undefined.  With groups == 0 there is one product over all rows,

@@ -261,6 +261,33 @@ def test_empty(cuda, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_alpha_zero_does_not_read_the_operands(cuda, dtype):
+    """alpha == 0: act(bias) + residual and zero gradients, whatever x and w
+    hold, at pitches that would be copied to aligned rows otherwise."""
+    dt = DTYPES[dtype]
+    nan = lambda *s: torch.full(s, float("nan"), dtype=dt, device="cuda")  # noqa: E731
+    bias = rand(301, dtype=dt, seed=1)
+    y = dg.linear(nan(401, 501), nan(501, 301), bias=bias, act="relu", alpha=0.0, out_dtype=dt)
+    assert torch.equal(y, torch.relu(bias).expand(401, 301))
+    dx, dw, db = dg.linear_grad(rand(401, 301, dtype=dt, seed=2), nan(401, 501), nan(501, 301), alpha=0.0)
+    assert not dx.any() and not dw.any() and bool(torch.isfinite(db).all())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("size", [(900, 1025, 1001), (520, 2047, 770), (2049, 515, 1030), (300, 4097, 2051)], ids=str)
+def test_large_odd_sizes(cuda, dtype, size):
+    """Rows below 16-byte alignment in products large enough to be copied to
+    aligned rows first, dense and grouped, all three products."""
+    m, n, k = size
+    cuts = [0, m // 3, m // 3, m // 2, m - 7]
+    for transb in (False, True):
+        check_forward(dtype, m, n, k, transb=transb, act="silu", offsets=cuts)
+        check_backward(dtype, m, n, k, transb=transb, act="gelu_tanh")
+    check_forward(dtype, m, n, k, residual=True)
+    check_backward(dtype, m, n, k, offsets=cuts)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_nan_and_infinity_stay_in_their_rows(cuda, dtype):
     """A NaN or an infinity in one row's input reaches that row's output only
     (and, in the gradients, its own group's), wherever a tile ends."""
