@@ -110,8 +110,9 @@ SIGNATURES.update({
 
 from .layers import (  # noqa: E402,F401
     ACTIVATIONS, GEMM_ACT_GELU, GEMM_ACT_GELU_TANH, GEMM_ACT_NONE, GEMM_ACT_RELU, GEMM_ACT_SILU,
-    LinearParams, gemm_linear, gemm_linear_act_grad, gemm_linear_act_grad_workspace_size,
-    gemm_linear_config_forms, gemm_linear_config_name, gemm_linear_force_config,
+    LinearGradOutputs, LinearParams, gemm_linear, gemm_linear_act_grad,
+    gemm_linear_act_grad_workspace_size, gemm_linear_config_forms, gemm_linear_config_name,
+    gemm_linear_force_config, gemm_linear_grad, gemm_linear_grad_workspace_size,
     gemm_linear_num_configs, gemm_linear_select_config, gemm_linear_weight_grad,
     gemm_linear_weight_grad_workspace_size, gemm_linear_workspace_size, grouped_linear,
     grouped_linear_grad, linear, linear_grad)

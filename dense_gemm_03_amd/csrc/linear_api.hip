@@ -64,16 +64,23 @@ struct Plan {
 // rate of a full unit or of a block alone, whichever is longer, and the reduce.
 // The entries' constants, the reduce's 3.5 us + bytes / 4.6 TB/s and the model's
 // form were fitted to 17000 measurements (every entry, 1 to 16 slices, M 40 to
-// 4096, N 256 to 8192, K 512 to 8192, all forms): the choice by the model is
-// 2.4% (bf16) and 1.6% (fp32) slower in the mean than the best of all.
-double estimate(const LinearConfig &c, double tiles, int64_t out, int64_t K, int64_t s, int64_t cus, int es)
+// 4096, N 256 to 8192, K 512 to 8192, all forms): the choice by the model was
+// 2.4% (bf16) and 1.6% (fp32) slower in the mean than the best of all.  The bf16
+// rates of a full unit are those of long runs at the board's power limit, up to
+// a fifth below the fitted ones (4096 x 16384 x 4096: 392 us with 256 x 256
+// tiles, 537 with 128 x 128).
+double estimate(const LinearConfig &c, double tiles, bool exact, int64_t out, int64_t K, int64_t s,
+                int64_t cus, int es)
 {
     const double blocks = tiles * (double)s;
     const int64_t per_cu = std::min<int64_t>(8, int64_t(160 * 1024) / ((int64_t)c.stages * (c.bm + c.bn) * c.bk * es));
     const double ktiles = (double)ceil_div(K, c.bk * s);
     double busy = std::max(1.0, std::ceil(blocks / (double)cus));   // blocks of the fullest unit
     double rounds = std::ceil(busy / (double)per_cu);
-    if (es == 2 && c.bm == 256) {   // pieces in the last round (xcd_piece)
+    if (!exact) {                   // a count of tiles that is not known: no steps
+        busy = std::max(1.0, blocks / (double)cus + 0.3);
+        rounds = std::max(1.0, busy / (double)per_cu);
+    } else if (es == 2 && c.bm == 256) {   // pieces in the last round (xcd_piece)
         const double whole = std::floor(blocks / (double)cus), rest = blocks - whole * (double)cus;
         busy = rounds = whole + (rest <= 0 ? 0.0 : 4 * rest <= cus ? 0.4 : 2 * rest <= cus ? 0.6 : 1.0);
     }
@@ -112,9 +119,30 @@ Plan find_plan(const gemm_linear_params &p, bool wgrad, int64_t cus)
                         (double)M / (double)bm + 0.5 * (double)std::min(groups, M));
     };
     const int64_t out = (wgrad ? groups * M : p.rows) * N;   // outputs
+    // bf16 operands without 16-byte rows lose the wide direct loads of the
+    // tiles: in place, rows at 4-byte boundaries take 1.45 times as long, others
+    // 3.5 times (2048^3: 23 us against 32 and 81 to 108).  Where that costs more
+    // than copying them into rows of 16-byte pitch first (a launch, and a pass at
+    // 3 TB/s over each), they are copied.  fp32 operands lose 10% at most, and
+    // the kernel for few rows nothing.
+    const int64_t w_ld = wgrad ? p.ldy : p.ldw;
+    const int64_t w_rows = wgrad ? p.rows : groups * (p.transw == GEMM_OP_T ? p.N : p.K);
+    const int64_t w_cols = wgrad ? p.N : p.transw == GEMM_OP_T ? p.K : p.N;
+    const int64_t px = ceil_div(p.K, 8) * 8, pw = ceil_div(w_cols, 8) * 8;
+    const bool bf16 = p.dtype == GEMM_DTYPE_BF16 && K > 0 && out > 0;
+    const bool x_odd = bf16 && p.ldx % 8 != 0;
+    const bool w_odd = bf16 && (w_ld % 8 != 0 || (!wgrad && groups > 1 && p.stride_w % 8 != 0));
+    const double in_place = !(x_odd || w_odd) ? 1.0 : ((p.ldx | w_ld) & 1) != 0 ? 3.5 : 1.45;
+    // the groups' weights have to be one matrix for that; a forced entry runs in place
+    const bool may_copy = (x_odd || w_odd) && t_cfg < 0 &&
+                          (!w_odd || wgrad || groups == 1 || p.stride_w == w_rows / groups * p.ldw);
+    const double copying = (x_odd ? 3.0 + (double)p.rows * (double)px * 4.0 / 3e6 : 0.0) +
+                           (w_odd ? 3.0 + (double)w_rows * (double)pw * 4.0 / 3e6 : 0.0);
+
     int count = 0;
     const LinearConfig *tab = linear_configs(p.dtype, &count);
     double best = 0.0;
+    bool copies = false;
     for (int i = 0; i < count; ++i) {
         const LinearConfig &c = tab[i];
         if (c.fn[pl.form][0] == nullptr || (t_cfg >= 0 && i != t_cfg)) continue;
@@ -124,6 +152,7 @@ Plan find_plan(const gemm_linear_params &p, bool wgrad, int64_t cus)
                 pl.cfg = i;
                 pl.splits = 1;
                 best = t;
+                copies = false;
             }
             continue;
         }
@@ -133,11 +162,15 @@ Plan find_plan(const gemm_linear_params &p, bool wgrad, int64_t cus)
             if (t_split > 0) want = t_split;
             int64_t s = std::min<int64_t>(want, std::min<int64_t>(ktiles, 64));
             if (!wgrad) s = ceil_div(ktiles, ceil_div(ktiles, s));   // every slice has a k-tile
-            const double t = estimate(c, row_tiles(c.bm) * (double)ceil_div(N, c.bn), out, K, s, cus, es);
+            const double whole = estimate(c, row_tiles(c.bm) * (double)ceil_div(N, c.bn), wgrad || !grouped,
+                                          out, K, s, cus, es);
+            const bool copied = may_copy && whole + copying < whole * in_place;
+            const double t = copied ? whole + copying : whole * in_place;
             if (pl.cfg < 0 || t < best) {
                 pl.cfg = i;
                 pl.splits = (int)s;
                 best = t;
+                copies = copied;
             }
             if (t_split > 0 || want >= ktiles) break;
         }
@@ -149,34 +182,15 @@ Plan find_plan(const gemm_linear_params &p, bool wgrad, int64_t cus)
                        : grouped ? M / c.bm + std::min(groups, M) : ceil_div(M, c.bm);
     if (pl.splits > 1) pl.ws_bytes = (pl.splits * out * 4 + 255) / 256 * 256;
 
-    // bf16 operands without 16-byte rows lose the wide direct loads: in place,
-    // rows at 4-byte boundaries take 1.45 times as long, others 3.5 times
-    // (2048^3: 23 us against 32 and 81 to 108).  Where that costs more than
-    // copying them into rows of 16-byte pitch first (a launch, and a pass at 3
-    // TB/s over each), they are copied.  fp32 operands lose 10% at most.
-    if (p.dtype == GEMM_DTYPE_BF16 && c.stages > 0 && t_cfg < 0 && K > 0 && out > 0) {
-        const int64_t x_ld = p.ldx, w_ld = wgrad ? p.N : p.ldw;   // dz: see weight_grad
-        const int64_t w_rows = wgrad ? p.rows : groups * (p.transw == GEMM_OP_T ? p.N : p.K);
-        const int64_t w_cols = wgrad ? p.N : p.transw == GEMM_OP_T ? p.K : p.N;
-        // the groups' weights as one matrix
-        const bool w_one = wgrad || groups == 1 || p.stride_w == w_rows / groups * p.ldw;
-        const bool x_odd = x_ld % 8 != 0, w_odd = w_ld % 8 != 0 || (!wgrad && groups > 1 && p.stride_w % 8 != 0);
-        const bool halves = ((x_ld | w_ld) & 1) != 0;
-        const int64_t px = ceil_div(p.K, 8) * 8, pw = ceil_div(w_cols, 8) * 8;
-        const double copy = (x_odd ? 3.0 + (double)p.rows * (double)px * 4.0 / 3e6 : 0.0) +
-                            (w_odd ? 3.0 + (double)w_rows * (double)pw * 4.0 / 3e6 : 0.0);
-        if ((x_odd || w_odd) && (!w_odd || w_one) && copy < best * (halves ? 2.5 : 0.45)) {
-            if (x_odd) {
-                pl.copy_x = px;
-                pl.at_x = pl.ws_bytes;
-                pl.ws_bytes += (p.rows * px * 2 + 255) / 256 * 256;
-            }
-            if (w_odd) {
-                pl.copy_w = pw;
-                pl.at_w = pl.ws_bytes;
-                pl.ws_bytes += w_rows * pw * 2;
-            }
-        }
+    if (copies && x_odd) {
+        pl.copy_x = px;
+        pl.at_x = pl.ws_bytes;
+        pl.ws_bytes += (p.rows * px * 2 + 255) / 256 * 256;
+    }
+    if (copies && w_odd) {
+        pl.copy_w = pw;
+        pl.at_w = pl.ws_bytes;
+        pl.ws_bytes += w_rows * pw * 2;
     }
     return pl;
 }
@@ -260,28 +274,28 @@ bool valid_workspace(const void *ws, int64_t bytes, int64_t need)
     return need == 0 || (ws != nullptr && (uintptr_t)ws % 16 == 0 && bytes >= need);
 }
 
-// Scratch of the bias gradient: one row of N sums per chunk of rows, when
-// there is more than one chunk.
-//
-// A chunk has 64 rows, or 16 where 64 would leave fewer than two blocks per
+// Scratch of the bias gradient.  Up to 128 rows per group on average and 1024 in
+// all, a block walks all of a group's rows and its sums are the result, without
+// a second launch (28 groups of 26 rows, whole backward pass: 15.0 us against
+// 21.6; but 484 rows of one: 31 against 26.5).  Beyond, chunks of rows, a row of
+// N sums each: 64 rows, or 16 where 64 would leave fewer than two blocks per
 // compute unit (777 x 1025 fp32: 19 us with 65 blocks of 64 rows).
+
 int act_grad_rows(const gemm_linear_params &p)
 {
     const int64_t blocks = ceil_div(p.rows, 64) * ceil_div(p.N, p.dtype == GEMM_DTYPE_F32 ? 256 : 512);
-    return p.rows > 64 && blocks < 512 ? 16 : 64;
+    if (p.rows <= 1024 && p.rows <= 128 * std::max<int64_t>(1, p.groups)) return 0;
+    return blocks < 512 ? 16 : 64;
 }
 
 int64_t act_grad_chunks(const gemm_linear_params &p)
 {
     const int64_t rows = act_grad_rows(p);
+    if (rows == 0) return 0;
     return p.groups > 0 ? p.rows / rows + std::min(p.groups, p.rows) : ceil_div(p.rows, rows);
 }
 
-int64_t act_grad_bytes(const gemm_linear_params &p)
-{
-    if (p.groups == 0 && act_grad_chunks(p) == 1) return 0;
-    return std::max<int64_t>(16, act_grad_chunks(p) * p.N * 4);
-}
+int64_t act_grad_bytes(const gemm_linear_params &p) { return act_grad_chunks(p) * p.N * 4; }
 
 int need_device()
 {
@@ -386,13 +400,13 @@ int act_grad(const gemm_linear_params *p, const void *dy, int64_t lddy, const vo
     return launch_act_grad(a, stream) == hipSuccess ? GEMM_OK : GEMM_ERR_HIP;
 }
 
-int weight_grad(const gemm_linear_params *p, const void *x, const void *dz, int64_t lddz,
-                const int32_t *offsets, int dtype_dw, float beta, void *dw, void *workspace,
-                int64_t workspace_bytes, hipStream_t stream)
+int weight_grad(const gemm_linear_params *p, const void *x, const void *dz, const int32_t *offsets,
+                int dtype_dw, float beta, void *dw, void *workspace, int64_t workspace_bytes,
+                hipStream_t stream)
 {
     if (!valid_sizes(p) || !valid_operands(p) || !known(dtype_dw)) return GEMM_ERR_INVALID_ARG;
     const bool sums = p->rows > 0 && p->alpha != 0.0f, empty = p->K == 0 || p->N == 0;
-    if (lddz < std::max<int64_t>(p->N, 1)) return GEMM_ERR_INVALID_ARG;
+    if (p->ldy < std::max<int64_t>(p->N, 1)) return GEMM_ERR_INVALID_ARG;
     if (!empty && (!dw || (sums && (!x || !dz)) || (p->groups > 0 && !offsets))) return GEMM_ERR_INVALID_ARG;
     if (misaligned(x, p->dtype) || misaligned(dz, p->dtype) || misaligned(dw, dtype_dw) ||
         (uintptr_t)offsets % 4)
@@ -405,13 +419,12 @@ int weight_grad(const gemm_linear_params *p, const void *x, const void *dz, int6
     if (empty) return GEMM_OK;
     if (const int rc = need_device()) return rc;
     const bool t = p->transw == GEMM_OP_T;   // dw^T = dz^T . x
-    int64_t ldx = p->ldx;
+    int64_t ldx = p->ldx, lddz = p->ldy;
     if (pl.copy_x) {
         const int rc = copy_rows(&x, &ldx, p->rows, p->K, pl.copy_x, workspace, pl.at_x, stream);
         if (rc != GEMM_OK) return rc;
     }
-    // planned for dz at a pitch of N: a wider one may have 16-byte rows as it is
-    if (pl.copy_w && lddz % 8 != 0) {
+    if (pl.copy_w) {
         const int rc = copy_rows(&dz, &lddz, p->rows, p->N, pl.copy_w, workspace, pl.at_w, stream);
         if (rc != GEMM_OK) return rc;
     }
@@ -433,10 +446,122 @@ int weight_grad(const gemm_linear_params *p, const void *x, const void *dz, int6
     return launch_plan(pl, p->dtype, a, true, workspace, stream);
 }
 
+// The pieces of the backward pass and their places in the workspace: dz first,
+// then scratch that they take in turn (they run one after another).
+struct GradParts {
+    gemm_linear_params act, dx, dw;
+    int64_t lddz = 0, dz_bytes = 0, act_bytes = 0, dx_bytes = 0, dw_bytes = 0, total = 0;
+    bool need_act = false, need_dz = false;
+    bool forms = true;   // false: a forced entry lacks a form
+};
+
+int64_t round16(int64_t n) { return (n + 15) / 16 * 16; }
+
+GradParts grad_parts(const gemm_linear_params &p, const gemm_linear_grad_outputs &o, bool dx, bool dw, bool db)
+{
+    GradParts g;
+    const int64_t vec = 16 / size_of(p.dtype);
+    g.need_dz = p.act != GEMM_ACT_NONE && (dx || dw);
+    g.need_act = g.need_dz || db;
+    g.lddz = g.need_dz ? std::max<int64_t>(vec, ceil_div(p.N, vec) * vec) : p.ldy;
+    g.dz_bytes = g.need_dz ? round16(p.rows * g.lddz * size_of(p.dtype)) : 0;
+    g.act = p;
+    g.dx = p;
+    g.dx.dtype_y = o.dtype_dx;
+    g.dx.dtype_bias = GEMM_DTYPE_F32;
+    g.dx.transw = p.transw == GEMM_OP_T ? GEMM_OP_N : GEMM_OP_T;
+    g.dx.act = GEMM_ACT_NONE;
+    g.dx.N = p.K;
+    g.dx.K = p.N;
+    g.dx.ldx = g.lddz;
+    g.dx.ldy = o.lddx;
+    g.dx.ldr = g.dx.ldp = 0;
+    g.dx.stride_bias = 0;
+    g.dw = p;
+    g.dw.act = GEMM_ACT_NONE;
+    g.dw.ldy = g.lddz;
+    g.dw.ldw = o.lddw;
+    g.dw.stride_w = o.stride_dw;
+    const bool rows = p.rows > 0;
+    g.act_bytes = db && p.N > 0 ? round16(act_grad_bytes(g.act)) : 0;
+    gemm_linear_params q = g.dx;
+    if (p.alpha == 0.0f) q.K = 0;
+    if (dx) {
+        const Plan pl = make_plan(q, false);
+        g.forms = pl.cfg >= 0;
+        g.dx_bytes = rows && p.K > 0 ? round16(pl.ws_bytes) : 0;
+    }
+    q = g.dw;
+    if (p.alpha == 0.0f) q.rows = 0;
+    if (dw) {
+        const Plan pl = make_plan(q, true);
+        g.forms = g.forms && pl.cfg >= 0;
+        g.dw_bytes = p.K > 0 && p.N > 0 ? round16(pl.ws_bytes) : 0;
+    }
+    g.total = g.dz_bytes + std::max(std::max(g.act_bytes, g.dx_bytes), g.dw_bytes);
+    return g;
+}
+
+bool valid_outputs(const gemm_linear_grad_outputs *o)
+{
+    return o != nullptr && known(o->dtype_dx) && known(o->dtype_dw);
+}
+
+int grad(const gemm_linear_params *p, const gemm_linear_grad_outputs *o, const void *dy, const void *x,
+         const void *w, const int32_t *offsets, const void *pre, void *dx, void *dw, float *dbias,
+         void *workspace, int64_t workspace_bytes, hipStream_t stream)
+{
+    if (!valid_sizes(p) || !valid_outputs(o) || !valid_operands(p)) return GEMM_ERR_INVALID_ARG;
+    const GradParts g = grad_parts(*p, *o, dx != nullptr, dw != nullptr, dbias != nullptr);
+    if (!g.forms || !valid_workspace(workspace, workspace_bytes, g.total)) return GEMM_ERR_INVALID_ARG;
+    // what the parts check before they launch, checked for all of them before the first
+    const bool some = p->rows > 0 && p->N > 0, sums = p->alpha != 0.0f;
+    const int64_t wrow = p->transw == GEMM_OP_T ? p->K : p->N, wrows = p->transw == GEMM_OP_T ? p->N : p->K;
+    if (p->ldy < std::max<int64_t>(p->N, 1) ||
+        (g.need_act && p->act != GEMM_ACT_NONE && (p->ldp < std::max<int64_t>(p->N, 1) || (some && !pre))) ||
+        (some && !dy) || (p->groups > 0 && !offsets) || misaligned(dy, p->dtype) || misaligned(pre, p->dtype_y) ||
+        (uintptr_t)dbias % 4 || (uintptr_t)offsets % 4)
+        return GEMM_ERR_INVALID_ARG;
+    if (dx && (o->lddx < std::max<int64_t>(p->K, 1) || misaligned(dx, o->dtype_dx) || misaligned(w, p->dtype) ||
+               (some && p->K > 0 && sums && !w)))
+        return GEMM_ERR_INVALID_ARG;
+    if (dw && (o->lddw < std::max<int64_t>(wrow, 1) || o->lddw > (int64_t(1) << 40) ||
+               (p->groups > 1 && wrow > 0 && wrows > 0 && o->stride_dw < (wrows - 1) * o->lddw + wrow) ||
+               misaligned(dw, o->dtype_dw) || misaligned(x, p->dtype) || (some && p->K > 0 && sums && !x)))
+        return GEMM_ERR_INVALID_ARG;
+    void *dz = g.need_dz ? workspace : const_cast<void *>(dy);
+    void *scratch = workspace ? static_cast<char *>(workspace) + g.dz_bytes : nullptr;
+    if (g.need_act) {
+        const int rc = act_grad(&g.act, dy, p->ldy, pre, offsets, g.need_dz ? dz : nullptr, g.lddz, dbias,
+                                scratch, g.act_bytes, stream);
+        if (rc != GEMM_OK) return rc;
+    }
+    if (dx) {
+        const int rc = linear(&g.dx, dz, w, offsets, nullptr, nullptr, nullptr, dx, scratch, g.dx_bytes, stream);
+        if (rc != GEMM_OK) return rc;
+    }
+    if (dw) return weight_grad(&g.dw, x, dz, offsets, o->dtype_dw, o->beta, dw, scratch, g.dw_bytes, stream);
+    return GEMM_OK;
+}
+
 }  // namespace
 }  // namespace dg
 
 extern "C" {
+
+int64_t gemm_linear_grad_workspace_size(const gemm_linear_params *p, const gemm_linear_grad_outputs *o, int dx,
+                                        int dw, int dbias)
+{
+    if (!dg::valid_sizes(p) || !dg::valid_outputs(o)) return GEMM_ERR_INVALID_ARG;
+    return dg::grad_parts(*p, *o, dx != 0, dw != 0, dbias != 0).total;
+}
+
+int gemm_linear_grad(const gemm_linear_params *p, const gemm_linear_grad_outputs *o, const void *dy,
+                     const void *x, const void *w, const int32_t *offsets, const void *pre, void *dx,
+                     void *dw, float *dbias, void *workspace, int64_t workspace_bytes, hipStream_t stream)
+{
+    return dg::grad(p, o, dy, x, w, offsets, pre, dx, dw, dbias, workspace, workspace_bytes, stream);
+}
 
 int64_t gemm_linear_workspace_size(const gemm_linear_params *p)
 {
@@ -474,11 +599,11 @@ int64_t gemm_linear_weight_grad_workspace_size(const gemm_linear_params *p)
     return p->K == 0 || p->N == 0 ? 0 : dg::make_plan(q, true).ws_bytes;
 }
 
-int gemm_linear_weight_grad(const gemm_linear_params *p, const void *x, const void *dz, int64_t lddz,
+int gemm_linear_weight_grad(const gemm_linear_params *p, const void *x, const void *dz,
                             const int32_t *offsets, int dtype_dw, float beta, void *dw,
                             void *workspace, int64_t workspace_bytes, hipStream_t stream)
 {
-    return dg::weight_grad(p, x, dz, lddz, offsets, dtype_dw, beta, dw, workspace, workspace_bytes, stream);
+    return dg::weight_grad(p, x, dz, offsets, dtype_dw, beta, dw, workspace, workspace_bytes, stream);
 }
 
 int gemm_linear_num_configs(int dtype)

@@ -73,46 +73,55 @@ __global__ void __launch_bounds__(256) linear_reduce_kernel(LinearArgs p)
     }
 }
 
-// dz = dy act'(pre), and each column's sum over the chunk's rows.  A block
-// takes one chunk of rows of one group and 64 V columns: its four waves walk
-// the rows in turn, V columns per lane; the sums meet in LDS.  Bound by HBM: 2
-// reads and 1 write of rows x N.  16-byte rows are taken 16 bytes per lane (1
-// KiB of a row per wave), others with the lanes side by side, element by
-// element.  V == 1 spreads few columns over more blocks.
-template <bool BF16, int V>
-__global__ void __launch_bounds__(256) act_grad_kernel(ActGradArgs p, int col_blocks)
+// dz = dy act'(pre), and each column's sum over the block's rows.  A block
+// takes 64 V columns of one chunk of rows of one group, or (CHUNKS false) of a
+// whole group, whose sums are then the result; its WV waves walk the rows in
+// turn, V columns per lane, and the sums meet in LDS.  Bound by HBM: 2 reads
+// and 1 write of rows x N.  16-byte rows are taken 16 bytes per lane (1 KiB of
+// a row per wave), others with the lanes side by side, element by element.  V
+// == 1 spreads few columns over more blocks.
+template <bool BF16, int V, bool CHUNKS>
+__global__ void __launch_bounds__(CHUNKS ? 256 : 1024) act_grad_kernel(ActGradArgs p, int col_blocks)
 {
     constexpr bool WIDE = V > 1;
-    __shared__ float sums[4][64 * V];
+    constexpr int WV = CHUNKS ? 4 : 16;
+    __shared__ float sums[WV][64 * V];
     const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
-    const GroupRows list(p.offsets, p.groups, p.rows, p.chunk_rows, lane);
     const int tile = (int)blockIdx.x / col_blocks, cb = (int)blockIdx.x - tile * col_blocks;
-    if (tile >= list.total) return;
-    int group, lo, m, tm;
-    list.find(p.offsets, p.groups, p.rows, p.chunk_rows, lane, 0, false, tile, group, lo, m, tm);
-    const int col0 = cb * 64 * V, first = tm * p.chunk_rows, count = min(p.chunk_rows, m - first);
+    int lo, first = 0, count;
+    if constexpr (CHUNKS) {
+        const GroupRows list(p.offsets, p.groups, p.rows, p.chunk_rows, lane);
+        if (tile >= list.total) return;
+        int group, m, tm;
+        list.find(p.offsets, p.groups, p.rows, p.chunk_rows, lane, 0, false, tile, group, lo, m, tm);
+        first = tm * p.chunk_rows;
+        count = min(p.chunk_rows, m - first);
+    } else {
+        group_span(p.offsets, tile, p.rows, lo, count);
+    }
+    const int col0 = cb * 64 * V, last = p.N - 1 - col0;
     // lane's columns: V in a row, or every 64th
     const bool vec = WIDE && p.vec != 0;
     auto column = [&](int i) { return vec ? lane * V + i : lane + 64 * i; };
     auto load = [&](const void *X, int64_t at, bool bf16, float (&v)[V]) {
-        const int n = p.N - col0 - lane * V;
-        if (vec && bf16 == BF16 && n >= V) {
+        if (vec && bf16 == BF16 && p.N - col0 - lane * V >= V) {
             load_out<V, WIDE>(X, at + lane * V, V, BF16, true, v);
+        } else if (bf16) {
+            // past the edge the last column's value, which nothing takes up: no
+            // branch, so that the loads are under way together
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                v[i] = __uint_as_float((uint32_t) static_cast<const uint16_t *>(X)[at + min(column(i), last)] << 16);
         } else {
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const int64_t j = at + column(i);
-                v[i] = col0 + column(i) >= p.N ? 0.0f
-                       : bf16 ? __uint_as_float((uint32_t) static_cast<const uint16_t *>(X)[j] << 16)
-                              : static_cast<const float *>(X)[j];
-            }
+            for (int i = 0; i < V; ++i) v[i] = static_cast<const float *>(X)[at + min(column(i), last)];
         }
     };
     float s[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) s[i] = 0.0f;
 #pragma unroll 4
-    for (int r = wave; r < count; r += 4) {
+    for (int r = wave; r < count; r += WV) {
         const int64_t row = lo + first + r;
         float g[V], z[V];
         load(p.dy, row * p.lddy + col0, BF16, g);
@@ -143,10 +152,14 @@ __global__ void __launch_bounds__(256) act_grad_kernel(ActGradArgs p, int col_bl
 #pragma unroll
     for (int i = 0; i < V; ++i) sums[wave][column(i)] = s[i];
     __syncthreads();
-    // one chunk in all (dense, few rows): the sums are the result
-    float *out = p.ws != nullptr ? p.ws + (int64_t)tile * p.N : p.dbias;
-    for (int i = (int)threadIdx.x; i < 64 * V; i += 256)
-        if (col0 + i < p.N) out[col0 + i] = sums[0][i] + sums[1][i] + sums[2][i] + sums[3][i];
+    float *out = (CHUNKS ? p.ws : p.dbias) + (int64_t)tile * p.N;
+    for (int i = (int)threadIdx.x; i < 64 * V; i += 64 * WV)
+        if (col0 + i < p.N) {
+            float t = 0.0f;
+#pragma unroll
+            for (int w = 0; w < WV; ++w) t += sums[w][i];
+            out[col0 + i] = t;
+        }
 }
 
 // dbias of one group: its chunks' sums (none: zero).  Four threads per column
@@ -200,9 +213,9 @@ hipError_t launch_linear_reduce(const LinearArgs &a, bool weight_grad, hipStream
 {
     const int64_t rows = weight_grad ? (int64_t)a.groups * a.M : a.rows;
     // 16 bytes of output per thread; fewer where that leaves most of the chip
-    // without a thread (48 x 4096, 8 slices: 6.0 us with 8 values, see below)
+    // without a thread, one value where rows have no 16-byte alignment
     const int64_t all = rows * a.N;
-    const int V = all <= 65536 ? 1 : a.e.out_bf16 && all > (1 << 21) ? 8 : 4;
+    const int V = all <= 65536 || !a.e.vec || a.N % 4 != 0 ? 1 : a.e.out_bf16 && all > (1 << 21) ? 8 : 4;
     const dim3 grid(grid_of(rows * ((a.N + V - 1) / V)));
     auto kernel = weight_grad ? (V == 8   ? linear_reduce_kernel<8, true>
                                  : V == 4 ? linear_reduce_kernel<4, true>
@@ -217,18 +230,23 @@ hipError_t launch_linear_reduce(const LinearArgs &a, bool weight_grad, hipStream
 hipError_t launch_act_grad(const ActGradArgs &a, hipStream_t stream)
 {
     const int W = a.bf16 ? 8 : 4;
+    const bool whole = a.chunk_rows == 0;
+    const int parts = whole ? a.groups : a.chunks;
     // 16 bytes per lane, unless that leaves most of the chip idle
-    const bool wide = (int64_t)a.chunks * ((a.N + 64 * W - 1) / (64 * W)) >= 64;
+    const bool wide = (int64_t)parts * ((a.N + 64 * W - 1) / (64 * W)) >= 64;
     const int V = wide ? W : 1;
     const int col_blocks = (a.N + 64 * V - 1) / (64 * V);
-    if (a.chunks > 0) {
-        auto kernel = a.bf16 ? (wide ? act_grad_kernel<true, 8> : act_grad_kernel<true, 1>)
-                             : (wide ? act_grad_kernel<false, 4> : act_grad_kernel<false, 1>);
-        hipLaunchKernelGGL(kernel, dim3((unsigned)(a.chunks * col_blocks)), dim3(256), 0, stream, a, col_blocks);
+    if (parts > 0) {
+        auto kernel = a.bf16 ? (whole ? (wide ? act_grad_kernel<true, 8, false> : act_grad_kernel<true, 1, false>)
+                                      : (wide ? act_grad_kernel<true, 8, true> : act_grad_kernel<true, 1, true>))
+                             : (whole ? (wide ? act_grad_kernel<false, 4, false> : act_grad_kernel<false, 1, false>)
+                                      : (wide ? act_grad_kernel<false, 4, true> : act_grad_kernel<false, 1, true>));
+        hipLaunchKernelGGL(kernel, dim3((unsigned)(parts * col_blocks)), dim3(whole ? 1024 : 256), 0, stream, a,
+                           col_blocks);
         const hipError_t err = hipGetLastError();
         if (err != hipSuccess) return err;
     }
-    if (a.dbias != nullptr && a.ws != nullptr) {
+    if (a.dbias != nullptr && !whole) {
         const int cb = (a.N + 63) / 64;
         hipLaunchKernelGGL(bias_reduce_kernel, dim3((unsigned)(cb * a.groups)), dim3(256), 0, stream, a, cb);
         return hipGetLastError();

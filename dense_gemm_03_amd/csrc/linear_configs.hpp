@@ -46,10 +46,10 @@ hipError_t launch_linear(const LinearArgs &args, int blocks, hipStream_t stream)
     X("f32_64x64x32_w2x2_s3", false, 64, 64, 32, 2, 2, 3, 8, 0.48f, 0.51f, 0.83f)
 
 #define DG_LIN_BF16_TABLE(X)                                                                 \
-    X("bf16_256x256x64_w2x2_s2", true, 256, 256, 64, 2, 2, 2, 8, 1.44f, 0.9f, 6.1f)          \
-    X("bf16_128x128x64_w2x2_s2", true, 128, 128, 64, 2, 2, 2, 8, 0.41f, 0.585f, 1.4f)        \
-    X("bf16_64x128x64_w1x4_s2", true, 64, 128, 64, 1, 4, 2, 8, 0.303f, 0.5f, 0.51f)          \
-    X("bf16_64x64x64_w2x2_s2", true, 64, 64, 64, 2, 2, 2, 8, 0.188f, 0.444f, 0.13f)
+    X("bf16_256x256x64_w2x2_s2", true, 256, 256, 64, 2, 2, 2, 8, 1.50f, 0.9f, 6.1f)          \
+    X("bf16_128x128x64_w2x2_s2", true, 128, 128, 64, 2, 2, 2, 8, 0.50f, 0.585f, 1.4f)        \
+    X("bf16_64x128x64_w1x4_s2", true, 64, 128, 64, 1, 4, 2, 8, 0.335f, 0.5f, 0.51f)          \
+    X("bf16_64x64x64_w2x2_s2", true, 64, 64, 64, 2, 2, 2, 8, 0.20f, 0.444f, 0.13f)
 
 // Entries for few rows: X(NAME, BF16, FORM (N or T), W, waves); 16 rows, 16 W columns.
 #define DG_LIN_F32_ROWS(X)                       \
@@ -105,7 +105,7 @@ struct ActGradArgs {
     int rows, N, groups;
     int act, bf16, pre_bf16;
     int vec;                // rows of dy, pre and dz are 16-byte aligned
-    int chunk_rows;         // rows of one chunk of the sums
+    int chunk_rows;         // rows of one chunk of the sums; 0: blocks take whole groups
     int chunks;             // chunks that ws has room for: all that there can be
 };
 hipError_t launch_act_grad(const ActGradArgs &args, hipStream_t stream);

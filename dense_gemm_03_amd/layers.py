@@ -22,8 +22,16 @@ class LinearParams(ctypes.Structure):
             "stride_bias")]
 
 
+class LinearGradOutputs(ctypes.Structure):
+    """gemm_linear_grad_outputs of include/gemm_linear.h."""
+    _fields_ = [("dtype_dx", ctypes.c_int32), ("dtype_dw", ctypes.c_int32), ("beta", ctypes.c_float),
+                ("reserved", ctypes.c_int32), ("lddx", ctypes.c_int64), ("lddw", ctypes.c_int64),
+                ("stride_dw", ctypes.c_int64)]
+
+
 _i64, _p, _int, _f = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int, ctypes.c_float
 _pl = ctypes.POINTER(LinearParams)
+_pg = ctypes.POINTER(LinearGradOutputs)
 # Every symbol include/gemm_linear.h declares, with its ctypes signature.
 SIGNATURES = {
     "gemm_linear_workspace_size": (_i64, [_pl]),
@@ -31,7 +39,9 @@ SIGNATURES = {
     "gemm_linear_act_grad_workspace_size": (_i64, [_pl]),
     "gemm_linear_act_grad": (_int, [_pl, _p, _i64, _p, _p, _p, _i64, _p, _p, _i64, _p]),
     "gemm_linear_weight_grad_workspace_size": (_i64, [_pl]),
-    "gemm_linear_weight_grad": (_int, [_pl, _p, _p, _i64, _p, _int, _f, _p, _p, _i64, _p]),
+    "gemm_linear_weight_grad": (_int, [_pl, _p, _p, _p, _int, _f, _p, _p, _i64, _p]),
+    "gemm_linear_grad_workspace_size": (_i64, [_pl, _pg, _int, _int, _int]),
+    "gemm_linear_grad": (_int, [_pl, _pg] + [_p] * 9 + [_i64, _p]),
     "gemm_linear_num_configs": (_int, [_int]),
     "gemm_linear_config_name": (ctypes.c_char_p, [_int, _int]),
     "gemm_linear_config_forms": (_int, [_int, _int]),
@@ -40,9 +50,15 @@ SIGNATURES = {
 }
 
 
+_lib = None
+
+
 def _library():
-    from . import load_library
-    return load_library()
+    global _lib
+    if _lib is None:
+        from . import load_library
+        _lib = load_library()
+    return _lib
 
 
 def _status(rc):
@@ -77,10 +93,20 @@ def gemm_linear_weight_grad_workspace_size(params) -> int:
     return _library().gemm_linear_weight_grad_workspace_size(params)
 
 
-def gemm_linear_weight_grad(params, x, dz, lddz, offsets, dtype_dw, beta, dw, workspace,
+def gemm_linear_weight_grad(params, x, dz, offsets, dtype_dw, beta, dw, workspace,
                             workspace_bytes, stream=None) -> int:
-    return _library().gemm_linear_weight_grad(params, x, dz, lddz, offsets, dtype_dw, beta, dw,
+    return _library().gemm_linear_weight_grad(params, x, dz, offsets, dtype_dw, beta, dw,
                                               workspace, workspace_bytes, stream)
+
+
+def gemm_linear_grad_workspace_size(params, outputs, dx=1, dw=1, dbias=1) -> int:
+    return _library().gemm_linear_grad_workspace_size(params, outputs, dx, dw, dbias)
+
+
+def gemm_linear_grad(params, outputs, dy, x, w, offsets, pre, dx, dw, dbias, workspace,
+                     workspace_bytes, stream=None) -> int:
+    return _library().gemm_linear_grad(params, outputs, dy, x, w, offsets, pre, dx, dw, dbias,
+                                       workspace, workspace_bytes, stream)
 
 
 def gemm_linear_num_configs(dtype: int) -> int:
@@ -205,6 +231,16 @@ def _block(*values):
         if len(_blocks) >= 4096:
             _blocks.clear()
         found = _blocks[values] = LinearParams(*values)
+    return found
+
+
+def _outputs(dtype_dx, dtype_dw, beta, lddx, lddw, stride_dw):
+    values = (dtype_dx, dtype_dw, beta, 0, lddx, lddw, stride_dw)
+    found = _blocks.get(values)
+    if found is None:
+        if len(_blocks) >= 4096:
+            _blocks.clear()
+        found = _blocks[values] = LinearGradOutputs(*values)
     return found
 
 
@@ -341,47 +377,30 @@ def _backward(dy, x, w, offsets, groups, act, pre, alpha, transb, out_dtype, nee
         dtype_dw = dtype_out
         ld_dw = max(w.shape[-1], 1)
         stride_dw = w.shape[-2] * w.shape[-1] if groups else 0
-    t = 1 if transb else 0
-    off = offsets.data_ptr() if groups else None
-    lib = _library()
     at = _Launch(device, stream)
     try:
+        dx = at.empty((rows, K), out_dtype) if need_dx else None
         dbias = at.empty((groups, N) if groups else (N,), torch.float32) if need_dbias else None
-        dz, lddz = dy, lddy
-        if act and (need_dx or need_dw):
-            # rows of a 16-byte pitch, which the two products read best
-            lddz = max((N + 7) // 8 * 8, 1)
-            dz = at.empty((rows, lddz), x.dtype)
-        if act or need_dbias:
-            params = _block(dtype, dtype_pre, 0, 0, act, 1.0, rows, N, K, groups, 0, 0, 0, 0, ldp, 0, 0)
-            need = lib.gemm_linear_act_grad_workspace_size(params) if need_dbias else 0
-            ws, ws_ptr = at.scratch(need)
-            _status(lib.gemm_linear_act_grad(
-                params, dy.data_ptr(), lddy, pre.data_ptr() if act else None, off,
-                dz.data_ptr() if dz is not dy else None, lddz,
-                dbias.data_ptr() if need_dbias else None, ws_ptr, need, at.stream))
-        dx = None
-        if need_dx:
-            dx = at.empty((rows, K), out_dtype)
-            params = _block(dtype, dtype_out, 0, 1 - t, 0, float(alpha), rows, K, N, groups, lddz, ldw,
-                            max(K, 1), 0, 0, stride_w, 0)
-            need = lib.gemm_linear_workspace_size(params)
-            ws, ws_ptr = at.scratch(need)
-            _status(lib.gemm_linear(params, dz.data_ptr(), w.data_ptr(), off, None, None, None,
-                                    dx.data_ptr(), ws_ptr, need, at.stream))
-        if need_dw:
-            if dw is None:
-                dw = at.empty(tuple(w.shape), out_dtype)
-            params = _block(dtype, 0, 0, t, 0, float(alpha), rows, N, K, groups, ldx, ld_dw, 0, 0, 0,
-                            stride_dw, 0)
-            need = lib.gemm_linear_weight_grad_workspace_size(params)
-            ws, ws_ptr = at.scratch(need)
-            _status(lib.gemm_linear_weight_grad(
-                params, x.data_ptr(), dz.data_ptr(), lddz, off, dtype_dw,
-                1.0 if accumulate else 0.0, dw.data_ptr(), ws_ptr, need, at.stream))
+        if need_dw and dw is None:
+            dw = at.empty(tuple(w.shape), out_dtype)
+        elif not need_dw:
+            dw = None
+        params = _block(dtype, dtype_pre, 0, 1 if transb else 0, act, float(alpha), rows, N, K, groups,
+                        ldx, ldw, lddy, 0, ldp, stride_w, 0)
+        outputs = _outputs(dtype_out, dtype_dw, 1.0 if accumulate else 0.0, max(K, 1), ld_dw, stride_dw)
+        lib = _library()
+        need = lib.gemm_linear_grad_workspace_size(params, outputs, need_dx, need_dw, need_dbias)
+        ws, ws_ptr = at.scratch(need)
+        rc = lib.gemm_linear_grad(params, outputs, dy.data_ptr(), x.data_ptr(), w.data_ptr(),
+                                  offsets.data_ptr() if groups else None,
+                                  pre.data_ptr() if act else None,
+                                  dx.data_ptr() if need_dx else None,
+                                  dw.data_ptr() if need_dw else None,
+                                  dbias.data_ptr() if need_dbias else None, ws_ptr, need, at.stream)
     finally:
         at.done()
-    return dx, dw if need_dw else None, dbias
+    _status(rc)
+    return dx, dw, dbias
 
 
 def linear_grad(dy, x, w, act="none", pre=None, *, alpha=1.0, transb=False, out_dtype=None,

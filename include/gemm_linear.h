@@ -21,11 +21,12 @@
  * rows; it is read by the kernels alone (no host synchronisation), so the
  * counts may come from a router that still runs on the stream.  A group may be
  * empty.  Rows before offsets[0] and from offsets[groups] on belong to nobody:
- * their values are not used, and they are not written.  Values outside 0 .. rows are clamped into
- * it and a group that ends before it begins is taken as empty, so no access
- * leaves the arrays whatever offsets holds; with offsets that fall, the results
- * of the rows between the smallest and the largest of them are undefined.  With groups == 0 there is one product over all rows,
- * and offsets, stride_w and stride_bias are not used.
+ * their values are not used, and they are not written.  Values outside 0 .. rows
+ * are clamped into it and a group that ends before it begins is taken as empty,
+ * so no access leaves the arrays whatever offsets holds; with offsets that fall,
+ * the results of the rows between the smallest and the largest of them are
+ * undefined.  With groups == 0 there is one product over all rows, and offsets,
+ * stride_w and stride_bias are not used.
  *
  * Gradients, for dy = the gradient of y:
  *
@@ -120,12 +121,39 @@ int64_t gemm_linear_weight_grad_workspace_size(const gemm_linear_params *params)
 /*
  * dw := alpha * x^T . dz + beta * dw in the layout of w (K x N, or N x K with
  * transw; one per group, stride_w apart), of type dtype_dw.  dz is rows x N of
- * params->dtype with leading dimension lddz.  dw is not read when beta == 0.
+ * params->dtype with leading dimension ldy.  dw is not read when beta == 0.
  */
 int gemm_linear_weight_grad(const gemm_linear_params *params, const void *x, const void *dz,
-                            int64_t lddz, const int32_t *offsets, int dtype_dw, float beta,
-                            void *dw, void *workspace, int64_t workspace_bytes,
-                            hipStream_t stream);
+                            const int32_t *offsets, int dtype_dw, float beta, void *dw,
+                            void *workspace, int64_t workspace_bytes, hipStream_t stream);
+
+/* What gemm_linear_grad writes. */
+typedef struct {
+    int32_t dtype_dx, dtype_dw;
+    float beta;          /* dw := .. + beta * dw */
+    int32_t reserved;    /* 0 */
+    int64_t lddx;        /* of dx, rows x K */
+    int64_t lddw, stride_dw; /* of dw, in the layout of w */
+} gemm_linear_grad_outputs;
+
+/* Scratch of gemm_linear_grad for these outputs (dx, dw, dbias: 1 for those it
+ * will be asked for, else 0). */
+int64_t gemm_linear_grad_workspace_size(const gemm_linear_params *params,
+                                        const gemm_linear_grad_outputs *outputs,
+                                        int dx, int dw, int dbias);
+
+/*
+ * The whole backward pass: gemm_linear_act_grad, gemm_linear on dz and
+ * gemm_linear_weight_grad in one call.  params describes the layer: dtype,
+ * transw, act, alpha, sizes, ldx, ldw, stride_w; dtype_y and ldp are pre's, ldy
+ * is dy's leading dimension (dy is of params->dtype).  dx, dw and dbias may each
+ * be NULL and are then left out; pre is needed for an activation only.  dz lives
+ * in the workspace.
+ */
+int gemm_linear_grad(const gemm_linear_params *params, const gemm_linear_grad_outputs *outputs,
+                     const void *dy, const void *x, const void *w, const int32_t *offsets,
+                     const void *pre, void *dx, void *dw, float *dbias, void *workspace,
+                     int64_t workspace_bytes, hipStream_t stream);
 
 /*
  * Kernel-table hooks, for tests and tuning: as the tile-table hooks of gemm.h.

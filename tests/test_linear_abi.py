@@ -49,7 +49,7 @@ def test_bad_parameters(kw):
     p = params(**kw)
     assert forward(p) == BAD
     assert dg.gemm_linear_act_grad(p, P, 48, P, P, P, 48, P, P, 1 << 40) == BAD
-    assert dg.gemm_linear_weight_grad(p, P, P, 48, P, 0, 0.0, P, P, 1 << 40) == BAD
+    assert dg.gemm_linear_weight_grad(p, P, P, P, 0, 0.0, P, P, 1 << 40) == BAD
     for size in (dg.gemm_linear_workspace_size, dg.gemm_linear_act_grad_workspace_size,
                  dg.gemm_linear_weight_grad_workspace_size):
         assert size(p) == BAD
@@ -80,21 +80,82 @@ def test_bad_forward_arguments():
 
 
 def test_bad_gradient_arguments():
-    act = lambda p=params(), dy=P, ldd=48, pre=P, off=P, dz=P, lddz=48, db=P, ws=P, n=1 << 40: \
+    act = lambda p=params(rows=2000), dy=P, ldd=48, pre=P, off=P, dz=P, lddz=48, db=P, ws=P, n=1 << 40: \
         dg.gemm_linear_act_grad(p, dy, ldd, pre, off, dz, lddz, db, ws, n)  # noqa: E731
     grouped = params(groups=3, stride_w=64 * 48)
-    need = dg.gemm_linear_act_grad_workspace_size(params())
+    need = dg.gemm_linear_act_grad_workspace_size(params(rows=2000))
     assert need > 0
     for kw in (dict(dy=None), dict(ldd=47), dict(lddz=47), dict(pre=None), dict(dy=P + 1), dict(dz=P + 1),
                dict(pre=P + 1), dict(db=P + 2), dict(ws=None), dict(n=need - 1), dict(p=grouped, off=None),
                dict(p=params(ldp=47))):
         assert act(**kw) == BAD, kw
-    wg = lambda p=params(), x=P, dz=P, lddz=48, off=P, dt=0, dw=P, ws=P, n=1 << 40: \
-        dg.gemm_linear_weight_grad(p, x, dz, lddz, off, dt, 0.0, dw, ws, n)  # noqa: E731
-    for kw in (dict(x=None), dict(dz=None), dict(dw=None), dict(lddz=47), dict(dt=2), dict(dw=P + 2), dict(x=P + 1),
+    wg = lambda p=params(), x=P, dz=P, off=P, dt=0, dw=P, ws=P, n=1 << 40: \
+        dg.gemm_linear_weight_grad(p, x, dz, off, dt, 0.0, dw, ws, n)  # noqa: E731
+    for kw in (dict(x=None), dict(dz=None), dict(dw=None), dict(p=params(ldy=47)), dict(dt=2), dict(dw=P + 2), dict(x=P + 1),
                dict(dz=P + 1), dict(p=grouped, off=None), dict(p=params(ldw=47)), dict(p=params(ldx=63)),
                dict(p=params(groups=2, stride_w=10))):
         assert wg(**kw) == BAD, kw
+
+
+def grad(p=None, o=None, dy=P, x=P, w=P, off=P, pre=P, dx=P, dw=P, db=P, ws=P, n=1 << 40):
+    return dg.gemm_linear_grad(p or params(), o or outputs(), dy, x, w, off, pre, dx, dw, db, ws, n)
+
+
+def outputs(**kw):
+    o = dict(dtype_dx=0, dtype_dw=0, beta=0.0, lddx=64, lddw=48, stride_dw=64 * 48)
+    o.update(kw)
+    return dg.LinearGradOutputs(**o)
+
+
+def test_bad_backward_arguments():
+    groups = dict(groups=3, stride_w=64 * 48)
+    need = dg.gemm_linear_grad_workspace_size(params(), outputs())
+    assert need >= 100 * 48 * 2
+    for kw in BAD_PARAMS:
+        assert grad(params(**kw)) == BAD, kw
+        assert dg.gemm_linear_grad_workspace_size(params(**kw), outputs()) == BAD, kw
+    for kw in (dict(dy=None), dict(x=None), dict(w=None), dict(pre=None), dict(dy=P + 1), dict(x=P + 1), dict(w=P + 1),
+               dict(pre=P + 1), dict(dx=P + 2), dict(dw=P + 2), dict(db=P + 2), dict(ws=None), dict(ws=P + 8),
+               dict(n=need - 1), dict(o=outputs(dtype_dx=2)), dict(o=outputs(dtype_dw=-1)), dict(o=outputs(lddx=63)),
+               dict(o=outputs(lddw=47)), dict(p=params(ldx=63)), dict(p=params(ldw=47)), dict(p=params(ldy=47)),
+               dict(p=params(ldp=47)), dict(p=params(**groups), off=None), dict(p=params(**groups), off=P + 2),
+               dict(p=params(**groups), o=outputs(stride_dw=64 * 48 - 1)),
+               dict(p=params(transw=1, ldw=64), o=outputs(lddw=63))):
+        assert grad(**kw) == BAD, kw
+    assert dg.gemm_linear_grad(None, outputs(), P, P, P, P, P, P, P, P, P, 1 << 40) == BAD
+    assert dg.gemm_linear_grad(params(), None, P, P, P, P, P, P, P, P, P, 1 << 40) == BAD
+    assert dg.gemm_linear_grad_workspace_size(params(), None) == BAD
+    # nothing asked for, nothing done
+    assert grad(dx=None, dw=None, db=None, x=None, w=None, ws=None, n=0) == dg.GEMM_OK
+    # a forced entry that lacks one of the forms is refused before anything runs
+    rows = [c for c in range(dg.gemm_linear_num_configs(1)) if dg.gemm_linear_config_forms(1, c) != 7]
+    assert rows
+    dg.gemm_linear_force_config(rows[0])
+    try:
+        assert grad() == BAD
+    finally:
+        dg.gemm_linear_force_config()
+
+
+def test_backward_scratch_covers_the_parts():
+    for rows, N, K in ((1, 1, 1), (100, 48, 64), (2000, 333, 515), (40, 4096, 4096), (5000, 64, 8192)):
+        for dtype in (0, 1):
+            for t in (0, 1):
+                for act in (0, 4):
+                    lddz = N if act == 0 else -(-N // (4 << dtype)) * (4 << dtype)
+                    p = params(dtype=dtype, rows=rows, N=N, K=K, transw=t, act=act, ldx=K, ldw=K if t else N, ldy=N,
+                               ldp=N)
+                    o = outputs(lddx=K, lddw=K if t else N)
+                    dz = rows * lddz * (4 >> dtype) if act else 0
+                    turned = params(dtype=dtype, dtype_y=0, rows=rows, N=K, K=N, transw=1 - t, act=0, ldx=lddz,
+                                    ldw=K if t else N, ldy=K, ldr=0, ldp=0)
+                    weight = params(dtype=dtype, rows=rows, N=N, K=K, transw=t, act=0, ldx=K, ldw=K if t else N,
+                                    ldy=lddz)
+                    size = lambda *which: dg.gemm_linear_grad_workspace_size(p, o, *which)  # noqa: E731
+                    assert size(1, 0, 0) >= dz + dg.gemm_linear_workspace_size(turned)
+                    assert size(0, 1, 0) >= dz + dg.gemm_linear_weight_grad_workspace_size(weight)
+                    assert size(0, 0, 1) >= dg.gemm_linear_act_grad_workspace_size(p)
+                    assert size(1, 1, 1) >= max(size(1, 0, 0), size(0, 1, 0), size(0, 0, 1))
 
 
 def test_empty_calls_launch_nothing():
@@ -102,7 +163,7 @@ def test_empty_calls_launch_nothing():
     assert forward(params(N=0), w=None, y=None, ws=None, nbytes=0) == dg.GEMM_OK
     assert dg.gemm_linear_act_grad(params(rows=0), None, 48, None, None, None, 48, None, None, 0) == dg.GEMM_OK
     assert dg.gemm_linear_act_grad(params(N=0), None, 48, None, None, P, 48, P, None, 0) == dg.GEMM_OK
-    assert dg.gemm_linear_weight_grad(params(K=0), None, P, 48, None, 0, 0.0, None, None, 0) == dg.GEMM_OK
+    assert dg.gemm_linear_weight_grad(params(K=0), None, P, None, 0, 0.0, None, None, 0) == dg.GEMM_OK
 
 
 def test_the_dispatchers_entry_has_the_form():
