@@ -63,28 +63,30 @@ struct Plan {
 // cut into s slices: rounds of blocks over the compute units, k-tiles at the
 // rate of a full unit or of a block alone, whichever is longer, and the reduce.
 // The entries' constants, the reduce's 3.5 us + bytes / 4.6 TB/s and the model's
-// form were fitted to 17000 measurements (every entry, 1 to 16 slices, M 40 to
+// form were fitted to 30000 measurements (every entry, 1 to 16 slices, M 40 to
 // 4096, N 256 to 8192, K 512 to 8192, all forms): the choice by the model was
-// 2.4% (bf16) and 1.6% (fp32) slower in the mean than the best of all.  The bf16
-// rates of a full unit are those of long runs at the board's power limit, up to
-// a fifth below the fitted ones (4096 x 16384 x 4096: 392 us with 256 x 256
-// tiles, 537 with 128 x 128).
+// 1.5% (bf16) and 1.1% (fp32) slower in the mean than the best of all.  With
+// groups the smaller bf16 tiles run a quarter slower than that: the weights come
+// from HBM and each is read by a few row tiles only (12000 rows of 10 groups,
+// 2048 x 2048: 0.58 us per k-tile of 128 x 128, against 0.45).
 double estimate(const LinearConfig &c, double tiles, bool exact, int64_t out, int64_t K, int64_t s,
                 int64_t cus, int es)
 {
     const double blocks = tiles * (double)s;
     const int64_t per_cu = std::min<int64_t>(8, int64_t(160 * 1024) / ((int64_t)c.stages * (c.bm + c.bn) * c.bk * es));
     const double ktiles = (double)ceil_div(K, c.bk * s);
+    const double step = !exact && es == 2 && c.bm < 256 ? 1.25 * c.step : c.step;
     double busy = std::max(1.0, std::ceil(blocks / (double)cus));   // blocks of the fullest unit
     double rounds = std::ceil(busy / (double)per_cu);
     if (!exact) {                   // a count of tiles that is not known: no steps
-        busy = std::max(1.0, blocks / (double)cus + 0.3);
+        busy = std::max(1.0, blocks / (double)cus + (es == 2 && c.bm == 256 ? 0.2 : 0.3));
         rounds = std::max(1.0, busy / (double)per_cu);
     } else if (es == 2 && c.bm == 256) {   // pieces in the last round (xcd_piece)
         const double whole = std::floor(blocks / (double)cus), rest = blocks - whole * (double)cus;
-        busy = rounds = whole + (rest <= 0 ? 0.0 : 4 * rest <= cus ? 0.4 : 2 * rest <= cus ? 0.6 : 1.0);
+        busy = whole + (rest <= 0 ? 0.0 : 4 * rest <= cus ? 0.4 : std::max(0.72, rest / (double)cus));
+        rounds = whole + (rest > 0 ? 1.0 : 0.0);
     }
-    double t = 3.0 + c.block * rounds + ktiles * std::max(c.step * busy, c.alone * rounds);
+    double t = 3.0 + c.block * rounds + ktiles * std::max(step * busy, c.alone * rounds);
     if (s > 1) t += 3.5 + 0.1 * (double)s + (double)s * (double)out * 8.0 / 4.6e6;
     return t;
 }
@@ -139,6 +141,11 @@ Plan find_plan(const gemm_linear_params &p, bool wgrad, int64_t cus)
     const double copying = (x_odd ? 3.0 + (double)p.rows * (double)px * 4.0 / 3e6 : 0.0) +
                            (w_odd ? 3.0 + (double)w_rows * (double)pw * 4.0 / 3e6 : 0.0);
 
+    // An entry's time t, or that of the weights from HBM at 4.7 TB/s, whichever
+    // is longer, and a little of the other.
+    const double stream = wgrad ? 0.0 : row_tiles((int64_t(1) << 31)) * (double)K * (double)N * es / 4.7e6;
+    auto with_stream = [&](double t) { return std::max(stream, t) + 0.1 * std::min(stream, t); };
+
     int count = 0;
     const LinearConfig *tab = linear_configs(p.dtype, &count);
     double best = 0.0;
@@ -147,7 +154,7 @@ Plan find_plan(const gemm_linear_params &p, bool wgrad, int64_t cus)
         const LinearConfig &c = tab[i];
         if (c.fn[pl.form][0] == nullptr || (t_cfg >= 0 && i != t_cfg)) continue;
         if (c.stages == 0) {
-            const double t = estimate_rows(c, row_tiles(16), N, K, per, cus, es);
+            const double t = with_stream(estimate_rows(c, row_tiles(16), N, K, per, cus, es));
             if (pl.cfg < 0 || t < best) {
                 pl.cfg = i;
                 pl.splits = 1;
@@ -162,8 +169,8 @@ Plan find_plan(const gemm_linear_params &p, bool wgrad, int64_t cus)
             if (t_split > 0) want = t_split;
             int64_t s = std::min<int64_t>(want, std::min<int64_t>(ktiles, 64));
             if (!wgrad) s = ceil_div(ktiles, ceil_div(ktiles, s));   // every slice has a k-tile
-            const double whole = estimate(c, row_tiles(c.bm) * (double)ceil_div(N, c.bn), wgrad || !grouped,
-                                          out, K, s, cus, es);
+            const double whole = with_stream(estimate(c, row_tiles(c.bm) * (double)ceil_div(N, c.bn),
+                                                      wgrad || !grouped, out, K, s, cus, es));
             const bool copied = may_copy && whole + copying < whole * in_place;
             const double t = copied ? whole + copying : whole * in_place;
             if (pl.cfg < 0 || t < best) {
@@ -257,11 +264,13 @@ int launch_plan(const Plan &pl, int dtype, LinearArgs &a, bool wgrad, void *work
     a.ws = pl.splits > 1 ? static_cast<float *>(workspace) : nullptr;
     // Blocks per XCD, for all eight: the tiles (or, grouped, the most there can
     // be), rounded up for either list, and room for the pieces of a last round
-    // (xcd_piece): at most 3/2 of the slots more.
+    // (xcd_piece): at most 3/4 of the slots more, and one more per group's last
+    // row of tiles.
     const int64_t tiles = pl.tiles_m * pl.tiles_n;
     a.slots = c.bm == 256 && c.bn == 256 && dtype == GEMM_DTYPE_BF16 ? device_compute_units() / 8 : 0;
+    const int64_t lasts = wgrad ? 0 : std::min<int64_t>(a.groups, a.rows) * pl.tiles_n * pl.splits;
     const int64_t per = (wgrad ? ceil_div(tiles, 8) * a.groups * pl.splits : tiles * pl.splits / 8 + 2) +
-                        ceil_div(a.slots * 3, 2);
+                        (a.slots > 0 ? ceil_div(a.slots * 3, 4) + lasts / 8 + 2 : 0);
     if (per > INT32_MAX / 8) return GEMM_ERR_INVALID_ARG;
     const int64_t blocks = per * 8;
     if (c.fn[pl.form][x16 && w16 ? 0 : 1](a, (int)blocks, stream) != hipSuccess) return GEMM_ERR_HIP;

@@ -45,11 +45,18 @@ hipError_t launch_linear(const LinearArgs &args, int blocks, hipStream_t stream)
     X("f32_128x128x32_w2x2_s2", false, 128, 128, 32, 2, 2, 2, 8, 1.87f, 1.2f, 4.0f)          \
     X("f32_64x64x32_w2x2_s3", false, 64, 64, 32, 2, 2, 3, 8, 0.48f, 0.51f, 0.83f)
 
+// Small bf16 tiles have three or four stages: two leave less than a k-tile's
+// products to cover a load, and where a unit has one block every k-tile waits
+// (0.44 us per k-tile of 64 x 64 with two stages, 0.20 with four).  With two,
+// five blocks share a unit, which is better where a block has a k-tile or two
+// and its stores are what counts (dw of 12 groups of 1 row, 1088 x 4864: 64
+// against 76 us).
 #define DG_LIN_BF16_TABLE(X)                                                                 \
-    X("bf16_256x256x64_w2x2_s2", true, 256, 256, 64, 2, 2, 2, 8, 1.50f, 0.9f, 6.1f)          \
-    X("bf16_128x128x64_w2x2_s2", true, 128, 128, 64, 2, 2, 2, 8, 0.50f, 0.585f, 1.4f)        \
-    X("bf16_64x128x64_w1x4_s2", true, 64, 128, 64, 1, 4, 2, 8, 0.335f, 0.5f, 0.51f)          \
-    X("bf16_64x64x64_w2x2_s2", true, 64, 64, 64, 2, 2, 2, 8, 0.20f, 0.444f, 0.13f)
+    X("bf16_256x256x64_w2x2_s2", true, 256, 256, 64, 2, 2, 2, 8, 1.45f, 0.60f, 6.6f)         \
+    X("bf16_128x128x64_w2x2_s2", true, 128, 128, 64, 2, 2, 2, 8, 0.45f, 0.565f, 1.1f)        \
+    X("bf16_64x128x64_w1x4_s3", true, 64, 128, 64, 1, 4, 3, 8, 0.32f, 0.33f, 0.75f)          \
+    X("bf16_64x64x64_w2x2_s2", true, 64, 64, 64, 2, 2, 2, 8, 0.20f, 0.42f, 0.05f)            \
+    X("bf16_64x64x64_w2x2_s4", true, 64, 64, 64, 2, 2, 4, 8, 0.21f, 0.215f, 0.3f)
 
 // Entries for few rows: X(NAME, BF16, FORM (N or T), W, waves); 16 rows, 16 W columns.
 #define DG_LIN_F32_ROWS(X)                       \

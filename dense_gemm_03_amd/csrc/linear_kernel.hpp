@@ -245,33 +245,23 @@ __device__ __forceinline__ int xcd_place(int active)
 //
 // One block of a large tile fills a compute unit, so n tiles take n / slots
 // rounds of the XCD's `slots` units, and a last round that is not full leaves
-// units idle for a whole tile's time.  Its r = n % slots tiles are cut into two
-// or four pieces where that ends sooner, by the times of the pieces in tenths
-// of a tile's: half (and a small tile) 6, a quarter 4 (measured: 0.55 to 0.65
-// and 0.35 to 0.45 of a tile's time at K of 2048 to 8192).  slots == 0: no
-// pieces.  At most 3/2 slots pieces more than tiles come out of it: four pieces
-// are chosen for r <= slots / 2 only (beyond, 4 * 3 exceeds what whole tiles
-// take), two for r < slots.
+// units idle for a whole tile's time.  If its r = n % slots tiles make no more
+// than one round of quarters, they are cut into those (128 tiles on 256 units, K
+// = 4096: 67 us whole, 82 in two rounds of quarters; 64 tiles: 64 against 44 in
+// one).  A small tile is two quarters.  slots == 0: no pieces.  There are at
+// most 3/4 slots + small pieces more than tiles.
 struct Piece {
-    int at;        // position in the list, or -1
-    int of, which; // 1, 2 or 4 pieces; which of them
+    int at;       // position in the list, or -1
+    int which;    // -1: the whole tile; quarter 0 .. 3: row half + 2 * column half
 };
 __device__ __forceinline__ Piece xcd_piece(int j, int n, int small, int slots)
 {
-    const int r = slots > 0 ? n % slots : 0;
-    int of = 1;
-    if (r > 0) {
-        auto rounds = [&](int blocks) { return (max(blocks, 0) + slots - 1) / slots; };
-        const int t1 = 10 + 6 * rounds(small - (slots - r)), t2 = 6 * rounds(2 * r + small);
-        const int t4 = 4 * rounds(4 * r) + 6 * rounds(small);
-        of = t1 <= t2 && t1 <= t4 ? 1 : t2 <= t4 ? 2 : 4;
-    }
-    const int whole = of == 1 ? n : n - r;
-    if (j < whole) return {j, 1, 0};
-    const int h = j - whole, pieces = (n - whole) * of;
-    if (h < pieces) return {whole + h / of, of, h % of};
-    const int at = n + h - pieces;
-    return {at < n + small ? at : -1, 1, 0};
+    if (slots == 0) return {j < n ? j : -1, -1};
+    const int r = n % slots, cut = 4 * r <= slots ? r : 0, whole = n - cut;
+    if (j < whole) return {j, -1};
+    const int h = j - whole - 4 * cut;   // among the small tiles' quarters
+    if (h < 0) return {whole + (j - whole) / 4, (j - whole) % 4};
+    return {h < 2 * small ? n + h / 2 : -1, h % 2 * 2};
 }
 
 // Group of rank o in the order of falling row counts (ties: the lower group
@@ -755,20 +745,13 @@ __global__ void __launch_bounds__(64 * WM * WN) linear_kernel(LinearArgs p)
     t.row0 = tm * BM;
     t.col0 = tn * BN;
     if constexpr (PIECES) {
-        const int out_rows = WGRAD ? p.M : t.m;
-        if (piece.of > 1) {
+        if (piece.which >= 0) {
             t.row0 += (piece.which & 1) * (BM / 2);
-            if (t.row0 >= out_rows) return;
-        }
-        if (piece.of == 4) {
             t.col0 += (piece.which >> 1) * (BN / 2);
-            if (t.col0 >= p.N) return;
-            linear_tile<Geo16<BN / 2, BM / 2, BK, 2, 2, 2, LW, LX>, ALIGNED>(p, t, lds0, lds1, lds2, lds3);
-            return;
-        }
-        // halves, and a group's last tile where half the rows suffice
-        if (piece.of == 2 || out_rows - t.row0 <= BM / 2) {
-            linear_tile<Geo16<BN, BM / 2, BK, 4, 1, 2, LW, LX>, ALIGNED>(p, t, lds0, lds1, lds2, lds3);
+            if (t.row0 >= (WGRAD ? p.M : t.m) || t.col0 >= p.N) return;
+            // alone on its unit: four stages, or each k-tile waits for its loads
+            using Q = Geo16<BN / 2, BM / 2, BK, 2, 2, 4, LW, LX>;
+            linear_tile<Q, ALIGNED>(p, t, lds0, lds1, lds0 + Q::STAGE_BYTES, lds1 + Q::STAGE_BYTES);
             return;
         }
     }

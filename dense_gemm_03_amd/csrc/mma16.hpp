@@ -168,9 +168,10 @@ __device__ __forceinline__ void direct_tile16(const unsigned char *stage, const 
     cur = nxt;
 }
 
-// Whole k-tiles [0, ntiles) from k_first, as main_loop_direct: distinct
-// restrict stages, STAGES tiles per iteration, loads past the last tile wrap
-// round to tiles already done.  On entry no wave may read or load any stage;
+// Whole k-tiles [0, ntiles) from k_first, in the order c.rot, c.rot + 1, .. of
+// the tiles taken round, as main_loop_direct: distinct restrict stages, STAGES
+// tiles per iteration, loads past the last tile wrap round to tiles already
+// done.  On entry no wave may read or load any stage;
 // on exit no load is in flight.
 template <class G, int DW>
 __device__ __forceinline__ void main_loop16_direct(unsigned char *__restrict__ s0,
@@ -187,7 +188,7 @@ __device__ __forceinline__ void main_loop16_direct(unsigned char *__restrict__ s
     DirectOffsets<G, DW> o;
     tile_offsets(c.tid >> 6, c.lane, c.lda, c.bm, c.M, o.a);
     tile_offsets(c.tid >> 6, c.lane, c.ldb, c.bn, c.N, o.b);
-    int kt = 0;
+    int kt = c.rot % ntiles;
     auto next_k = [&]() {
         const int k = k_first + kt * BK;
         kt = kt + 1 == ntiles ? 0 : kt + 1;
