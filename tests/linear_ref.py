@@ -8,8 +8,9 @@ inside, so twice that is allowed: sum_bound(K) S.  The activations and their
 slopes are formed from the hardware's exp2 and reciprocal (1 ulp each) and a
 rounded exponent, which makes sigmoid(x) off by at most (|x| + 4) 2^-23
 (1 - sigmoid) relative; since z^2 q (1 - q) < 1 and |z| q (1 - q) < 0.3, the
-activations are off by less than 2^-21 (1 + |z|); erf's 2 ulp give less.  Twice
-that is allowed: act_bound.  |act'| < 1.13, so an error in z grows by less than
+activations are off by less than 2^-21 (1 + |z|).  The error function is a
+polynomial within 1.5e-7 of it and half of that, times z, is less than 2^-23 |z|.
+Twice the former is allowed: act_bound.  |act'| < 1.13, so an error in z grows by less than
 that.  An output in a narrower type adds half a step of it (eps / 2 relative).
 """
 from __future__ import annotations

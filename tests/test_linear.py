@@ -174,6 +174,110 @@ def check_weight_grad(dtype, rows, n, k, transb, offsets):
         check("dw %d" % g, dw[g] if groups else dw, want + o, bound + 2.0 ** -22 * (o.abs() + want.abs()))
 
 
+def offsets_of(counts, before=0):
+    out = [before]
+    for c in counts:
+        out.append(out[-1] + c)
+    return out
+
+
+# Tiles of 256 x 256 on 256 compute units, 32 per XCD: 81 tiles are whole ones,
+# 272 leave a last round that is cut into quarters, and so do 9.
+@pytest.mark.parametrize("transb", [False, True])
+@pytest.mark.parametrize("size", [(2100, 2060, 200), (4250, 4096, 136), (700, 600, 192)], ids=str)
+def test_whole_tiles_and_quarters(cuda, size, transb):
+    m, n, k = size
+    try:
+        for split in (1, 2):
+            assert dg.gemm_linear_force_config(0, split) == 0
+            check_forward("bf16", m, n, k, transb=transb, act="silu", residual=True, pre=True)
+            check_weight_grad("bf16", k, n, m, transb, None)
+    finally:
+        dg.gemm_linear_force_config()
+
+
+GROUPS = {
+    "last tiles of a few rows": [260, 512, 257, 1, 0, 300, 256, 770, 512, 3, 640, 129, 128, 127, 384],
+    "only small tiles": [100, 7, 0, 128, 64] * 8,
+    "one large": [3000, 1, 1, 1],
+}
+
+
+@pytest.mark.parametrize("transb", [False, True])
+@pytest.mark.parametrize("name", GROUPS)
+def test_quarters_of_groups(cuda, name, transb):
+    offsets = offsets_of(GROUPS[name], 5)
+    try:
+        for n in (520, 2304):
+            assert dg.gemm_linear_force_config(0) == 0
+            check_forward("bf16", offsets[-1] + 9, n, 136, transb=transb, act="relu", residual=True, offsets=offsets)
+    finally:
+        dg.gemm_linear_force_config()
+
+
+@pytest.mark.parametrize("groups", [5, 20, 70])
+def test_weight_gradients_of_many_tiles(cuda, groups):
+    """dw of groups with 9 tiles each: whole tiles, quarters in the last round
+    (20), and more groups than a wave has lanes."""
+    offsets = offsets_of([(37 * g) % 150 for g in range(groups)], 2)
+    try:
+        for split in (1, 2):
+            assert dg.gemm_linear_force_config(0, split) == 0
+            check_weight_grad("bf16", offsets[-1] + 3, 600, 520, False, offsets)
+            check_weight_grad("bf16", offsets[-1] + 3, 600, 520, True, offsets)
+    finally:
+        dg.gemm_linear_force_config()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,n", [(1030, 40), (1500, 264), (8300, 2050), (8192, 2048)])
+def test_bias_gradient_of_many_rows(cuda, dtype, rows, n):
+    """Chunks of 16 and of 64 rows, one group and uneven ones."""
+    for offsets in (None, offsets_of([rows // 3, 0, 1, rows // 2, 15], 4)):
+        check_backward(dtype, rows, n, 24, act="silu", offsets=offsets)
+
+
+@pytest.mark.parametrize("act", ["gelu", "gelu_tanh", "silu"])
+@pytest.mark.parametrize("transb", [False, True])
+def test_gradients_against_differences(cuda, act, transb):
+    """The directional derivative of L = <dy, y> along random signs v, from
+    (L(+h) - L(-h)) / 2h at points that fp32 holds exactly.  It is off by h^2 / 6
+    times the third derivative along v (those of the activations stay below 2),
+    by the outputs' errors, each inside its bound, over h, and the gradient by
+    its own bound."""
+    m, n, k, h = 30, 40, 48, 2.0 ** -7
+    exact = lambda *s, **kw: rand(*s, dtype=torch.bfloat16, **kw).float()  # noqa: E731
+    at = dict(x=exact(m, k, seed=1), w=exact(*((n, k) if transb else (k, n)), seed=2, scale=k ** -0.5),
+              b=exact(n, seed=3))
+    dy = rand(m, n, dtype=torch.float32, seed=4)
+    z = torch.empty(m, n, device="cuda")
+    dg.linear(at["x"], at["w"], bias=at["b"], act=act, transb=transb, pre=z)
+    got = dict(zip("xwb", dg.linear_grad(dy, at["x"], at["w"], act=act, pre=z, transb=transb)))
+    bounds = ref.backward(dy, at["x"], at["w"], act, z, 1.0, transb, torch.float32)
+    d, x64 = dy.cpu().double(), at["x"].cpu().double()
+    w64 = (at["w"].t() if transb else at["w"]).cpu().double()
+    for which, name in zip("xwb", ("dx", "dw", "dbias")):
+        v = torch.sign(exact(*at[which].shape, seed=9) + 1e-30)
+        ends, noise = [], 0.0
+        for step in (h, -h):
+            moved = dict(at)
+            moved[which] = at[which] + step * v
+            assert torch.equal(moved[which].double(), at[which].double() + step * v.double())
+            y = dg.linear(moved["x"], moved["w"], bias=moved["b"], act=act, transb=transb)
+            bound = ref.forward(moved["x"], moved["w"], moved["b"], act, None, 1.0, transb, torch.float32)[3]
+            noise += float((d.abs() * bound).sum())
+            ends.append(float((d * y.cpu().double()).sum()))
+        v = v.cpu().double()
+        along = {"x": lambda: v @ w64, "b": lambda: v.expand(m, n),
+                 "w": lambda: x64 @ (v.t() if transb else v)}[which]()
+        want = (ends[0] - ends[1]) / (2 * h)
+        grad = float((got[which].cpu().double() * v).sum())
+        limit = (float((d.abs() * along.abs() ** 3).sum()) * 2 * h * h / 6 + noise / (2 * h) +
+                 float((bounds[name][1] * v.abs()).sum()))
+        log("  %s: difference %.5f, gradient %.5f, limit %.3g" % (name, want, grad, limit))
+        assert abs(grad - want) <= limit, name
+
+
 OFFSETS = {
     "one group": [0, 90],
     "all in the middle": [0, 0, 90, 90],
