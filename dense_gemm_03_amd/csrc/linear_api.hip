@@ -69,13 +69,13 @@ struct Plan {
 // groups the smaller bf16 tiles run a quarter slower than that: the weights come
 // from HBM and each is read by a few row tiles only (12000 rows of 10 groups,
 // 2048 x 2048: 0.58 us per k-tile of 128 x 128, against 0.45).
-double estimate(const LinearConfig &c, double tiles, bool exact, int64_t out, int64_t K, int64_t s,
+double estimate(const LinearConfig &c, double tiles, bool grouped, bool exact, int64_t out, int64_t K, int64_t s,
                 int64_t cus, int es)
 {
     const double blocks = tiles * (double)s;
     const int64_t per_cu = std::min<int64_t>(8, int64_t(160 * 1024) / ((int64_t)c.stages * (c.bm + c.bn) * c.bk * es));
     const double ktiles = (double)ceil_div(K, c.bk * s);
-    const double step = !exact && es == 2 && c.bm < 256 ? 1.25 * c.step : c.step;
+    const double step = grouped && es == 2 && c.bm < 256 ? 1.25 * c.step : c.step;
     double busy = std::max(1.0, std::ceil(blocks / (double)cus));   // blocks of the fullest unit
     double rounds = std::ceil(busy / (double)per_cu);
     if (!exact) {                   // a count of tiles that is not known: no steps
@@ -169,7 +169,7 @@ Plan find_plan(const gemm_linear_params &p, bool wgrad, int64_t cus)
             if (t_split > 0) want = t_split;
             int64_t s = std::min<int64_t>(want, std::min<int64_t>(ktiles, 64));
             if (!wgrad) s = ceil_div(ktiles, ceil_div(ktiles, s));   // every slice has a k-tile
-            const double whole = with_stream(estimate(c, row_tiles(c.bm) * (double)ceil_div(N, c.bn),
+            const double whole = with_stream(estimate(c, row_tiles(c.bm) * (double)ceil_div(N, c.bn), grouped,
                                                       wgrad || !grouped, out, K, s, cus, es));
             const bool copied = may_copy && whole + copying < whole * in_place;
             const double t = copied ? whole + copying : whole * in_place;
@@ -287,14 +287,15 @@ bool valid_workspace(const void *ws, int64_t bytes, int64_t need)
 // all, a block walks all of a group's rows and its sums are the result, without
 // a second launch (28 groups of 26 rows, whole backward pass: 15.0 us against
 // 21.6; but 484 rows of one: 31 against 26.5).  Beyond, chunks of rows, a row of
-// N sums each: 64 rows, or 16 where 64 would leave fewer than two blocks per
-// compute unit (777 x 1025 fp32: 19 us with 65 blocks of 64 rows).
-
+// N sums each: 64 rows; 32 with groups, whose last chunks are short (16 groups,
+// 8192 x 4096: 58 us against 64; one group: 50 against 44); 16 where 64 would
+// leave fewer than two blocks per compute unit (777 x 1025 fp32: 19 us with 65
+// blocks of 64 rows).
 int act_grad_rows(const gemm_linear_params &p)
 {
     const int64_t blocks = ceil_div(p.rows, 64) * ceil_div(p.N, p.dtype == GEMM_DTYPE_F32 ? 256 : 512);
     if (p.rows <= 1024 && p.rows <= 128 * std::max<int64_t>(1, p.groups)) return 0;
-    return blocks < 512 ? 16 : 64;
+    return blocks < 512 ? 16 : p.groups > 0 ? 32 : 64;
 }
 
 int64_t act_grad_chunks(const gemm_linear_params &p)
