@@ -63,9 +63,9 @@ struct Plan {
 // cut into s slices: rounds of blocks over the compute units, k-tiles at the
 // rate of a full unit or of a block alone, whichever is longer, and the reduce.
 // The entries' constants, the reduce's 3.5 us + bytes / 4.6 TB/s and the model's
-// form were fitted to 30000 measurements (every entry, 1 to 16 slices, M 40 to
+// form were fitted to 23000 measurements (every entry, 1 to 16 slices, M 40 to
 // 4096, N 256 to 8192, K 512 to 8192, all forms): the choice by the model was
-// 1.5% (bf16) and 1.1% (fp32) slower in the mean than the best of all.  With
+// 2.1% (bf16) and 1.1% (fp32) slower in the mean than the best of all.  With
 // groups the smaller bf16 tiles run a quarter slower than that: the weights come
 // from HBM and each is read by a few row tiles only (12000 rows of 10 groups,
 // 2048 x 2048: 0.58 us per k-tile of 128 x 128, against 0.45).
@@ -141,10 +141,13 @@ Plan find_plan(const gemm_linear_params &p, bool wgrad, int64_t cus)
     const double copying = (x_odd ? 3.0 + (double)p.rows * (double)px * 4.0 / 3e6 : 0.0) +
                            (w_odd ? 3.0 + (double)w_rows * (double)pw * 4.0 / 3e6 : 0.0);
 
-    // An entry's time t, or that of the weights from HBM at 4.7 TB/s, whichever
-    // is longer, and a little of the other.
-    const double stream = wgrad ? 0.0 : row_tiles((int64_t(1) << 31)) * (double)K * (double)N * es / 4.7e6;
-    auto with_stream = [&](double t) { return std::max(stream, t) + 0.1 * std::min(stream, t); };
+    // An entry's time t, or that of the weights (for dw, of x and dz) from HBM at
+    // 4.7 TB/s, whichever is longer, and a part of the other: a tenth, or half
+    // where two stages are all that covers HBM's latency (512 x 8192 x 8192, one
+    // 128 x 128 block per unit: 106 us, 76 by the cached rate; 256 x 256: 81).
+    const double stream = (wgrad ? (double)p.rows * (double)(p.K + p.N)
+                                 : row_tiles((int64_t(1) << 31)) * (double)K * (double)N) * es / 4.7e6;
+    auto with_stream = [&](double t, double part) { return std::max(stream, t) + part * std::min(stream, t); };
 
     int count = 0;
     const LinearConfig *tab = linear_configs(p.dtype, &count);
@@ -154,7 +157,7 @@ Plan find_plan(const gemm_linear_params &p, bool wgrad, int64_t cus)
         const LinearConfig &c = tab[i];
         if (c.fn[pl.form][0] == nullptr || (t_cfg >= 0 && i != t_cfg)) continue;
         if (c.stages == 0) {
-            const double t = with_stream(estimate_rows(c, row_tiles(16), N, K, per, cus, es));
+            const double t = with_stream(estimate_rows(c, row_tiles(16), N, K, per, cus, es), 0.1);
             if (pl.cfg < 0 || t < best) {
                 pl.cfg = i;
                 pl.splits = 1;
@@ -170,7 +173,8 @@ Plan find_plan(const gemm_linear_params &p, bool wgrad, int64_t cus)
             int64_t s = std::min<int64_t>(want, std::min<int64_t>(ktiles, 64));
             if (!wgrad) s = ceil_div(ktiles, ceil_div(ktiles, s));   // every slice has a k-tile
             const double whole = with_stream(estimate(c, row_tiles(c.bm) * (double)ceil_div(N, c.bn), grouped,
-                                                      wgrad || !grouped, out, K, s, cus, es));
+                                                      wgrad || !grouped, out, K, s, cus, es),
+                                             es == 2 && c.stages == 2 && c.bm < 256 ? 0.5 : 0.1);
             const bool copied = may_copy && whole + copying < whole * in_place;
             const double t = copied ? whole + copying : whole * in_place;
             if (pl.cfg < 0 || t < best) {

@@ -246,10 +246,10 @@ __device__ __forceinline__ int xcd_place(int active)
 // One block of a large tile fills a compute unit, so n tiles take n / slots
 // rounds of the XCD's `slots` units, and a last round that is not full leaves
 // units idle for a whole tile's time.  If its r = n % slots tiles make no more
-// than one round of quarters, they are cut into those (128 tiles on 256 units, K
-// = 4096: 67 us whole, 82 in two rounds of quarters; 64 tiles: 64 against 44 in
-// one).  A small tile is two quarters.  slots == 0: no pieces.  There are at
-// most 3/4 slots + small pieces more than tiles.
+// than one round of quarters, they are cut into those (K = 4096 on 256 units: 64
+// tiles take 38 us in a round of quarters, 72 whole ones 55; but 128 tiles 77
+// whole and 82 in two rounds of quarters).  A small tile is two quarters.  slots
+// == 0: no pieces.  There are at most 3/4 slots + small pieces more than tiles.
 struct Piece {
     int at;       // position in the list, or -1
     int which;    // -1: the whole tile; quarter 0 .. 3: row half + 2 * column half
