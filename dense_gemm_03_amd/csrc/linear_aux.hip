@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(256) bias_reduce_kernel(ActGradArgs p, int col
                                                 false, lo, m);
             const int upto = GroupRows::scan(t, lane);
             const int at = min(63, group - base);   // the group itself, or the last of these 64
-            first += __builtin_amdgcn_readlane(upto, at);
+            first = min(first + __builtin_amdgcn_readlane(upto, at), GroupRows::CAP);
             mine = __builtin_amdgcn_readlane(t, at);
         }
         first -= mine;

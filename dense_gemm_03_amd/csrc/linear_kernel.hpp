@@ -156,7 +156,12 @@ __device__ __forceinline__ void group_span(const int32_t *offsets, int g, int ro
 // the lanes), so no launch before this one and no memory is needed.  With
 // `half` > 0 a group's last tile of at most that many rows is small, and the
 // small tiles form a list of their own behind the others.
+//
+// Offsets that fall can claim the same rows many times over.  Sums stop at CAP,
+// beyond any that offsets in order can have, and the lists at what those can
+// have: the grid, the workspaces and 32-bit products of either are made for that.
 struct GroupRows {
+    static constexpr int CAP = (1 << 30) - 1;
     int total, small;   // tiles of all groups: all but the small ones, the small ones
 
     __device__ __forceinline__ static int lane_tiles(const int32_t *offsets, int g, int groups,
@@ -175,7 +180,7 @@ struct GroupRows {
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
             const int o = __shfl_up(v, d);
-            if (lane >= d) v += o;
+            if (lane >= d) v = min(v + o, CAP);
         }
         return v;
     }
@@ -192,10 +197,12 @@ struct GroupRows {
         for (int base = 0; base < groups; base += 64) {
             int lo, m;
             const int t = lane_tiles(offsets, base + lane, groups, rows, bm, half, false, lo, m);
-            total += __builtin_amdgcn_readlane(scan(t, lane), 63);
+            total = min(total + __builtin_amdgcn_readlane(scan(t, lane), 63), CAP);
             if (half > 0)
                 small += __builtin_popcountll(__ballot(m % bm > 0 && m % bm <= half));
         }
+        total = min(total, rows / bm + min(groups, rows));
+        small = min(small, min(groups, rows));
     }
     // Group, its first row, its rows and the tile inside it of tile `t` of
     // either list.
@@ -223,7 +230,7 @@ struct GroupRows {
                                 : t - (__builtin_amdgcn_readlane(upto, at) - __builtin_amdgcn_readlane(mine, at));
                 return;
             }
-            before = __builtin_amdgcn_readlane(upto, 63);
+            before = min(__builtin_amdgcn_readlane(upto, 63), CAP);
         }
     }
 };

@@ -324,6 +324,31 @@ def test_offsets_outside_the_rows_are_clamped(cuda, dtype):
         assert bool(torch.isfinite(dw).all()) and bool(torch.isfinite(db).all())
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_offsets_that_claim_the_rows_many_times(cuda, dtype):
+    """Falling offsets whose groups take all rows 300 times over: more tiles and
+    chunks than offsets in order can have.  Guards around the outputs stay, and
+    dw, whose blocks walk their own group only, is right."""
+    dt, rows, n, k, g = DTYPES[dtype], 1200, 64, 48, 601
+    off = torch.tensor([0, rows] * 301, dtype=torch.int32, device="cuda")
+    x, dy = rand(rows, k, dtype=dt, seed=1), rand(rows, n, dtype=dt, seed=2)
+    w = rand(1, k, n, dtype=dt, seed=3).expand(g, k, n).contiguous()
+    whole = torch.full((rows + 8, n), 7.0, device="cuda")
+    for cfg in range(dg.gemm_linear_num_configs(1 if dtype == "bf16" else 0)):
+        if dg.gemm_linear_config_forms(1 if dtype == "bf16" else 0, cfg) & 1:
+            dg.gemm_linear_force_config(cfg)
+            try:
+                dg.grouped_linear(x, w, off, out=whole[4:-4])
+            finally:
+                dg.gemm_linear_force_config()
+            assert bool((whole[:4] == 7).all()) and bool((whole[-4:] == 7).all())
+    dx, dw, db = dg.grouped_linear_grad(dy, x, w, off)
+    want, bound = ref.backward(dy, x, w[0], "none", None, 1.0, False, torch.float32)["dw"]
+    for i in (0, 300, 600):
+        check("dw", dw[i], want, bound)
+    assert not dw[1].any() and not dw[599].any()
+
+
 @pytest.mark.parametrize("act", ref.ACTS)
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_backward(cuda, dtype, act):
