@@ -83,7 +83,7 @@ double estimate(const LinearConfig &c, double tiles, bool grouped, bool exact, i
         rounds = std::max(1.0, busy / (double)per_cu);
     } else if (es == 2 && c.bm == 256) {   // pieces in the last round (xcd_piece)
         const double whole = std::floor(blocks / (double)cus), rest = blocks - whole * (double)cus;
-        busy = whole + (rest <= 0 ? 0.0 : 4 * rest <= cus ? 0.4 : std::max(0.72, rest / (double)cus));
+        busy = whole + (rest <= 0 ? 0.0 : 4 * rest <= cus ? 0.4 : 2 * rest <= cus ? 0.6 : std::max(0.72, rest / (double)cus));
         rounds = whole + (rest > 0 ? 1.0 : 0.0);
     }
     double t = 3.0 + c.block * rounds + ktiles * std::max(step * busy, c.alone * rounds);

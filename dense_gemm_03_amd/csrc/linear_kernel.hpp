@@ -253,21 +253,22 @@ __device__ __forceinline__ int xcd_place(int active)
 // One block of a large tile fills a compute unit, so n tiles take n / slots
 // rounds of the XCD's `slots` units, and a last round that is not full leaves
 // units idle for a whole tile's time.  If its r = n % slots tiles make no more
-// than one round of quarters, they are cut into those (K = 4096 on 256 units: 64
-// tiles take 38 us in a round of quarters, 72 whole ones 55; but 128 tiles 77
-// whole and 82 in two rounds of quarters).  A small tile is two quarters.  slots
-// == 0: no pieces.  There are at most 3/4 slots + small pieces more than tiles.
+// than one round of quarters or of halves, they are cut into those (K = 4096 on
+// 256 units: 64 tiles take 38 us in quarters, 128 tiles 65 in halves, 77 whole
+// and 82 in two rounds of quarters).  A small tile is two quarters.  slots == 0:
+// no pieces.  There are at most 3/4 slots + small pieces more than tiles.
 struct Piece {
     int at;       // position in the list, or -1
-    int which;    // -1: the whole tile; quarter 0 .. 3: row half + 2 * column half
+    int which;    // -1: the whole tile; quarter 0 .. 3: row half + 2 * column half; 4, 5: row half
 };
 __device__ __forceinline__ Piece xcd_piece(int j, int n, int small, int slots)
 {
     if (slots == 0) return {j < n ? j : -1, -1};
-    const int r = n % slots, cut = 4 * r <= slots ? r : 0, whole = n - cut;
+    const int r = n % slots, of = 4 * r <= slots ? 4 : 2 * r <= slots ? 2 : 1;
+    const int whole = of > 1 ? n - r : n;
     if (j < whole) return {j, -1};
-    const int h = j - whole - 4 * cut;   // among the small tiles' quarters
-    if (h < 0) return {whole + (j - whole) / 4, (j - whole) % 4};
+    const int h = j - whole - of * (n - whole);   // among the small tiles' quarters
+    if (h < 0) return {whole + (j - whole) / of, (j - whole) % of + (of == 2 ? 4 : 0)};
     return {h < 2 * small ? n + h / 2 : -1, h % 2 * 2};
 }
 
@@ -698,8 +699,11 @@ __global__ void __launch_bounds__(64 * WM * WN) linear_kernel(LinearArgs p)
     // one block per compute unit, and pieces of a tile to choose from
     constexpr bool PIECES = BF16 && BM == 256 && BN == 256 && WM * WN == 4;
 
-    __shared__ __attribute__((aligned(1024))) unsigned char lds0[G::STAGE_BYTES];
-    __shared__ __attribute__((aligned(1024))) unsigned char lds1[G::STAGE_BYTES];
+    // pieces divide one array in ways of their own
+    __shared__ __attribute__((aligned(1024))) unsigned char all[PIECES ? 9 * G::STAGE_BYTES / 4 : 1];
+    __shared__ __attribute__((aligned(1024))) unsigned char first[PIECES ? 1 : G::STAGE_BYTES];
+    __shared__ __attribute__((aligned(1024))) unsigned char second[PIECES ? 1 : G::STAGE_BYTES];
+    unsigned char *const lds0 = PIECES ? all : first, *const lds1 = PIECES ? all + G::STAGE_BYTES : second;
     __shared__ __attribute__((aligned(1024))) unsigned char lds2[STAGES > 2 ? G::STAGE_BYTES : 1];
     __shared__ __attribute__((aligned(1024))) unsigned char lds3[STAGES > 3 ? G::STAGE_BYTES : 1];
 
@@ -754,9 +758,15 @@ __global__ void __launch_bounds__(64 * WM * WN) linear_kernel(LinearArgs p)
     if constexpr (PIECES) {
         if (piece.which >= 0) {
             t.row0 += (piece.which & 1) * (BM / 2);
-            t.col0 += (piece.which >> 1) * (BN / 2);
+            t.col0 += (piece.which >> 1 & 1) * (BN / 2);
             if (t.row0 >= (WGRAD ? p.M : t.m) || t.col0 >= p.N) return;
-            // alone on its unit: four stages, or each k-tile waits for its loads
+            // alone on their unit: three or four stages, or each k-tile waits
+            // for its loads
+            if (piece.which >= 4) {
+                using H = Geo16<BN, BM / 2, BK, 4, 1, 3, LW, LX>;
+                linear_tile<H, ALIGNED>(p, t, all, all + H::STAGE_BYTES, all + 2 * H::STAGE_BYTES, all);
+                return;
+            }
             using Q = Geo16<BN / 2, BM / 2, BK, 2, 2, 4, LW, LX>;
             linear_tile<Q, ALIGNED>(p, t, lds0, lds1, lds0 + Q::STAGE_BYTES, lds1 + Q::STAGE_BYTES);
             return;

@@ -181,11 +181,11 @@ def offsets_of(counts, before=0):
     return out
 
 
-# Tiles of 256 x 256 on 256 compute units, 32 per XCD: 81 tiles are whole ones,
-# 272 leave a last round that is cut into quarters, and so do 9.
+# Tiles of 256 x 256 on 256 compute units, 32 per XCD: 143 tiles are whole ones,
+# 81 are cut into halves, and quarters are what 9 tiles and the last of 272 give.
 @pytest.mark.parametrize("transb", [False, True])
-@pytest.mark.parametrize("size", [(2100, 2060, 200), (4250, 4096, 136), (700, 600, 192)], ids=str)
-def test_whole_tiles_and_quarters(cuda, size, transb):
+@pytest.mark.parametrize("size", [(3300, 2800, 72), (2100, 2060, 200), (4250, 4096, 136), (700, 600, 192)], ids=str)
+def test_whole_tiles_halves_and_quarters(cuda, size, transb):
     m, n, k = size
     try:
         for split in (1, 2):
