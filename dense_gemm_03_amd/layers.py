@@ -177,7 +177,7 @@ def _pitch(t, rows, cols, what):
 def _weights(w, groups, transb):
     """(K, N, leading dimension, stride between groups) of w."""
     a, b = w.shape[-2], w.shape[-1]
-    ld = _pitch(w, a * b, b, "w") if a > 1 else b
+    ld = _pitch(w, a, b, "w")   # a matrix of one row has contiguous values too
     stride = 0
     if groups:
         stride = w.stride(0) if groups > 1 and a * b else a * ld
