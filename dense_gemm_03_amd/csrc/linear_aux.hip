@@ -76,10 +76,12 @@ __global__ void __launch_bounds__(256) linear_reduce_kernel(LinearArgs p)
 // dz = dy act'(pre), and each column's sum over the block's rows.  A block
 // takes 64 V columns of one chunk of rows of one group, or (CHUNKS false) of a
 // whole group, whose sums are then the result; its WV waves walk the rows in
-// turn, V columns per lane, and the sums meet in LDS.  Bound by HBM: 2 reads
-// and 1 write of rows x N.  16-byte rows are taken 16 bytes per lane (1 KiB of
-// a row per wave), others with the lanes side by side, element by element.  V
-// == 1 spreads few columns over more blocks.
+// turn, V columns per lane, and the sums meet in LDS.  dz is rounded to the
+// operands' type, once: the matrix cores multiply bf16 with bf16 only, and dz as
+// two bf16 terms would double both products.  The sums take it unrounded.
+// Bound by HBM: 2 reads and 1 write of rows x N.  16-byte rows are taken 16
+// bytes per lane (1 KiB of a row per wave), others with the lanes side by side,
+// element by element.  V == 1 spreads few columns over more blocks.
 template <bool BF16, int V, bool CHUNKS>
 __global__ void __launch_bounds__(CHUNKS ? 256 : 1024) act_grad_kernel(ActGradArgs p, int col_blocks)
 {

@@ -413,8 +413,12 @@ def linear_grad(dy, x, w, act="none", pre=None, *, alpha=1.0, transb=False, out_
     (the residual's gradient is dy itself).  ``pre`` is what the forward pass
     stored; not needed without an activation.  dx and dw are ``out_dtype``
     (default float32), dw in w's layout, dbias float32.  Between an activation
-    and the two products dz is rounded once to x's type; dbias sums the values
-    before that.  ``dw`` receives the weight gradient when given, added to what
+    and the two products dz is rounded once to x's type, the one that the matrix
+    cores read it in; dbias sums the values before that.  Where that rounding of
+    a bfloat16 layer is too coarse (it adds as much to the error of dx and dw as
+    their own rounding to bfloat16), pass dy, x and w as float32: nothing is
+    rounded on the way then, at the float32 products' rate, and the gradients can
+    still be bfloat16 (``out_dtype``).  ``dw`` receives the weight gradient when given, added to what
     it holds with ``accumulate``.  What is not needed comes back as None."""
     return _backward(dy, x, w, None, 0, act, pre, alpha, transb, out_dtype, need_dx, need_dw,
                      need_dbias, dw, accumulate, stream)
