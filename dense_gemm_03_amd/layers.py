@@ -185,16 +185,17 @@ def _weights(w, groups, transb):
 
 
 class _Launch:
-    """Device, stream and temporaries of one call: the library launches on the
-    calling thread's current device, and memory taken from torch's allocator
-    for a stream that is not torch's current one has to be told so."""
-    __slots__ = ("device", "index", "stream", "foreign", "guard")
+    """Device, stream and memory of one call: the library launches on the
+    calling thread's current device.  Memory for a stream that is not torch's
+    current one comes from that stream's pool: a block of the current stream's
+    pool may have been freed while kernels queued there still use it."""
+    __slots__ = ("device", "index", "stream", "side", "guard")
 
     def __init__(self, device, stream):
         self.device, self.index = device, device.index
         current = _raw_stream(self.index)
         self.stream = current if stream is None else stream
-        self.foreign = stream is not None and stream != current
+        self.side = None if self.stream == current else torch.cuda.ExternalStream(self.stream, device=device)
         self.guard = None
         if torch.cuda.current_device() != self.index:
             self.guard = torch.cuda.device(device)
@@ -204,10 +205,17 @@ class _Launch:
         if self.guard is not None:
             self.guard.__exit__(None, None, None)
 
+    def _take(self, shape, dtype):
+        if self.side is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        with torch.cuda.stream(self.side):
+            return torch.empty(shape, dtype=dtype, device=self.device)
+
     def empty(self, shape, dtype):
-        t = torch.empty(shape, dtype=dtype, device=self.device)
-        if self.foreign and t.numel():
-            t.record_stream(torch.cuda.ExternalStream(self.stream, device=self.device))
+        """An output, which the caller may go on to use on the current stream."""
+        t = self._take(shape, dtype)
+        if self.side is not None and t.numel():
+            t.record_stream(torch.cuda.current_stream(self.device))
         return t
 
     def scratch(self, need):
@@ -216,7 +224,7 @@ class _Launch:
             _status(need)
         if need == 0:
             return None, None
-        t = self.empty((need,), torch.uint8)
+        t = self._take((need,), torch.uint8)
         return t, t.data_ptr()
 
 
@@ -325,8 +333,10 @@ def linear(x, w, bias=None, act="none", residual=None, *, alpha=1.0, transb=Fals
     "gelu", "gelu_tanh" or "silu".  ``pre`` (M x N, y's type) receives the value
     before the activation, which the backward pass needs.  y is float32 or
     bfloat16 (``out_dtype``, default float32), created when ``out`` is not
-    given; ``residual`` may be ``out`` itself.  Runs on ``stream`` (default:
-    torch's current stream) and returns without synchronising."""
+    given; ``residual`` may be ``out`` itself.  Runs on ``stream`` (a handle;
+    default: torch's current stream) and returns without synchronising.  On
+    another stream than the current one the inputs have to be ready there, and
+    whoever uses the outputs elsewhere waits for that stream first."""
     return _forward(x, w, None, 0, bias, act, residual, alpha, transb, pre, out, out_dtype, stream)
 
 
@@ -419,7 +429,8 @@ def linear_grad(dy, x, w, act="none", pre=None, *, alpha=1.0, transb=False, out_
     their own rounding to bfloat16), pass dy, x and w as float32: nothing is
     rounded on the way then, at the float32 products' rate, and the gradients can
     still be bfloat16 (``out_dtype``).  ``dw`` receives the weight gradient when given, added to what
-    it holds with ``accumulate``.  What is not needed comes back as None."""
+    it holds with ``accumulate``.  What is not needed comes back as None.
+    ``stream`` as in ``linear``."""
     return _backward(dy, x, w, None, 0, act, pre, alpha, transb, out_dtype, need_dx, need_dw,
                      need_dbias, dw, accumulate, stream)
 

@@ -49,3 +49,108 @@ def test_one_row_of_weights_on_the_gpu(cuda):
         rows = [0, 1, 1] if groups else [0, 0, 0]
         want = torch.stack([w.reshape(-1, 12)[g] for g in rows])
         assert torch.equal(forward(w.contiguous()), want)
+
+
+# ---------------------------------------------------------------- streams --
+
+class FakeStream:
+    def __init__(self, handle, device=None):
+        self.handle = handle
+
+
+class FakeTensor:
+    def __init__(self, stream):
+        self.stream, self.recorded = stream, []
+
+    def numel(self):
+        return 1
+
+    def data_ptr(self):
+        return 4096
+
+    def record_stream(self, stream):
+        self.recorded.append(stream.handle)
+
+
+class FakeTorch:
+    """Streams and allocations, as much of them as a launch uses: a tensor
+    remembers the stream that was current when it was made, whose pool it is
+    from."""
+    uint8 = "uint8"
+
+    def __init__(self):
+        self.now, self.cuda, self.made = 111, self, []
+        self.ExternalStream = FakeStream
+
+    def stream(self, stream):
+        outer, before = self, self.now
+
+        class Guard:
+            def __enter__(self):
+                outer.now = stream.handle
+
+            def __exit__(self, *a):
+                outer.now = before
+        return Guard()
+
+    def current_device(self):
+        return 0
+
+    def current_stream(self, device=None):
+        return FakeStream(self.now)
+
+    def empty(self, shape, dtype=None, device=None):
+        self.made.append(FakeTensor(self.now))
+        return self.made[-1]
+
+
+@pytest.mark.parametrize("stream", [None, 111, 222])
+def test_memory_of_a_call_is_from_the_pool_of_its_stream(monkeypatch, stream):
+    """A block from another stream's pool may have been freed while work that
+    is queued on that stream still uses it: the kernels of this call must not
+    write to such a block."""
+    fake = FakeTorch()
+    monkeypatch.setattr(layers, "torch", fake)
+    monkeypatch.setattr(layers, "_raw_stream", lambda index: fake.now)
+    at = layers._Launch(torch.device("cuda:0"), stream)
+    out = at.empty((4, 4), "float32")
+    _, pointer = at.scratch(256)
+    at.done()
+    ran_on = 111 if stream is None else stream
+    assert at.stream == ran_on and pointer == 4096 and fake.now == 111
+    assert [t.stream for t in fake.made] == [ran_on, ran_on]
+    # an output is handed to code that runs on the current stream
+    assert out.recorded == ([111] if ran_on != 111 else [])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("act", ["none", "silu"])
+def test_another_stream_next_to_pending_work(cuda, act):
+    """Outputs and scratch of a call on another stream do not share memory with
+    a tensor that was just freed and that the current stream still works on."""
+    x = torch.randn(48, 4096, device="cuda").bfloat16()
+    w, dy = torch.randn(1024, 4096, device="cuda").bfloat16(), torch.randn(48, 1024, device="cuda").bfloat16()
+    z = torch.randn(48, 1024, device="cuda").bfloat16() if act != "none" else None
+    busy = torch.randn(4096, 4096, device="cuda")
+    made = torch.empty_like(busy)
+    want = [dg.linear(x, w, transb=True, act=act), *dg.linear_grad(dy, x, w, act=act, pre=z, transb=True)]
+    sizes = [t.shape for t in want] + [(1 << 18,), (1 << 20,)]
+    s = torch.cuda.Stream()
+    for _ in range(3):
+        torch.cuda.synchronize()
+        for _ in range(4):
+            dg.gemm(busy, busy, out=made)      # about a millisecond each
+        old, kept = [], []
+        for shape in sizes:
+            t = torch.full(shape, 3.0, device="cuda")
+            kept.append(t.add(1.0))            # reads t behind the products
+            old.append((t.data_ptr(), t.data_ptr() + t.numel() * 4))
+            del t
+        got = [dg.linear(x, w, transb=True, act=act, stream=s.cuda_stream),
+               *dg.linear_grad(dy, x, w, act=act, pre=z, transb=True, stream=s.cuda_stream)]
+        for t in got:
+            assert not any(lo <= t.data_ptr() < hi for lo, hi in old)
+        s.synchronize()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        assert all(bool((t == 4.0).all()) for t in kept)
