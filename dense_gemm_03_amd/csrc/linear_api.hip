@@ -334,6 +334,8 @@ int linear(const gemm_linear_params *p, const void *x, const void *w, const int3
         (uintptr_t)offsets % 4)
         return GEMM_ERR_INVALID_ARG;
     if (p->groups > 1 && bias && p->stride_bias < p->N) return GEMM_ERR_INVALID_ARG;
+    // in place: row r of y lies over row r of the residual and no other
+    if (residual && residual == y && p->rows > 1 && p->ldr != p->ldy) return GEMM_ERR_INVALID_ARG;
     gemm_linear_params q = *p;
     if (!sums) q.K = 0;
     const Plan pl = make_plan(q, false);
@@ -383,6 +385,7 @@ int act_grad(const gemm_linear_params *p, const void *dy, int64_t lddy, const vo
     if (misaligned(dy, p->dtype) || misaligned(dz, p->dtype) || misaligned(pre, p->dtype_y) ||
         (uintptr_t)dbias % 4 || (uintptr_t)offsets % 4)
         return GEMM_ERR_INVALID_ARG;
+    if (dz && dz == dy && p->rows > 1 && lddz != lddy) return GEMM_ERR_INVALID_ARG;   // as residual and y
     const int64_t need = dbias && p->N > 0 ? act_grad_bytes(*p) : 0;
     if (!valid_workspace(workspace, workspace_bytes, need)) return GEMM_ERR_INVALID_ARG;
     if (p->N == 0 || (!dz && !dbias) || (p->rows == 0 && !dbias)) return GEMM_OK;

@@ -46,7 +46,8 @@
  *
  * Memory: every pointer is a device pointer of the caller's, aligned to its
  * element; outputs must not overlap inputs, except that residual may be y
- * itself (same leading dimension).  The calls take their scratch memory from
+ * itself, and dz of gemm_linear_act_grad may be dy itself, with the same leading
+ * dimension (GEMM_ERR_INVALID_ARG otherwise).  The calls take their scratch memory from
  * the caller (workspace, 16-byte aligned, at least the bytes that the
  * *_workspace_size function of the same parameters returns; contents on entry
  * do not matter); the library allocates nothing and keeps nothing, so the
@@ -111,7 +112,7 @@ int64_t gemm_linear_act_grad_workspace_size(const gemm_linear_params *params);
  * the sum of dz over rows.  dy and dz are rows x N of params->dtype with
  * leading dimensions lddy and lddz; pre is rows x N of dtype_y with ldp, and
  * not read (may be NULL) for GEMM_ACT_NONE.  dz may be NULL (only dbias is
- * formed) and may be dy itself; dbias may be NULL.
+ * formed) and may be dy itself (lddz == lddy); dbias may be NULL.
  */
 int gemm_linear_act_grad(const gemm_linear_params *params, const void *dy, int64_t lddy,
                          const void *pre, const int32_t *offsets, void *dz, int64_t lddz,

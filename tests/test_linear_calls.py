@@ -154,3 +154,70 @@ def test_another_stream_next_to_pending_work(cuda, act):
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
         assert all(bool((t == 4.0).all()) for t in kept)
+
+
+# ---------------------------------------------------------------- aliases --
+
+P = 1 << 20     # stands in for a device address: refused calls read nothing
+BAD = dg.GEMM_ERR_INVALID_ARG
+
+
+def params(**kw):
+    """Parameters of a valid layer: 100 rows, 64 inputs, 48 outputs, bf16."""
+    p = dict(dtype=1, dtype_y=1, dtype_bias=0, transw=0, act=dg.GEMM_ACT_SILU, alpha=1.0, rows=100, N=48, K=64,
+             groups=0, ldx=64, ldw=48, ldy=48, ldr=48, ldp=48, stride_w=0, stride_bias=0)
+    p.update(kw)
+    return dg.LinearParams(**p)
+
+
+def test_in_place_needs_the_same_pitch():
+    """With another pitch one row's output lies over an input row that is not
+    read yet."""
+    big = 1 << 40
+    for kw in (dict(ldr=49), dict(ldy=56), dict(rows=2, ldr=96)):
+        assert dg.gemm_linear(params(**kw), P, P, None, None, P, None, P, P, big) == BAD, kw
+    for lddy, lddz in ((48, 49), (56, 48)):
+        for rows in (100, 2000):
+            p = params(rows=rows)
+            assert dg.gemm_linear_act_grad(p, P, lddy, P, None, P, lddz, P, P, big) == BAD, (lddy, lddz, rows)
+            assert dg.gemm_linear_act_grad(p, P, lddy, P, None, P, lddz, None, None, 0) == BAD
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("rows,n,pitch", [(40, 48, 48), (40, 51, 53), (900, 200, 208), (3000, 264, 264), (3000, 77, 81)])
+def test_dz_in_the_place_of_dy(cuda, dtype, rows, n, pitch):
+    """gemm_linear_act_grad with dz == dy, with and without chunks of rows,
+    16-byte rows and others: the same dz and dbias as apart, and nothing behind
+    the rows."""
+    code = dg.GEMM_DTYPE_F32 if dtype == torch.float32 else dg.GEMM_DTYPE_BF16
+    gen = torch.Generator().manual_seed(rows + n)
+    wide = torch.randn(rows, pitch, generator=gen).to(dtype).cuda()
+    pre = torch.randn(rows, n, generator=gen).to(dtype).cuda()
+    offsets = torch.tensor([0, rows // 3, rows // 3, rows - 5], dtype=torch.int32, device="cuda")
+    for groups, off in ((0, None), (3, offsets)):
+        p = params(dtype=code, dtype_y=code, rows=rows, N=n, groups=groups, ldp=n)
+        need = dg.gemm_linear_act_grad_workspace_size(p)
+        found = []
+        for in_place in (False, True):
+            dy = wide.clone()
+            dz = dy if in_place else wide.clone()
+            dbias = torch.zeros(max(groups, 1), n, device="cuda")
+            ws = torch.empty(max(need, 16), dtype=torch.uint8, device="cuda")
+            assert dg.gemm_linear_act_grad(p, dy.data_ptr(), pitch, pre.data_ptr(), off.data_ptr() if groups else None,
+                                           dz.data_ptr(), pitch, dbias.data_ptr(), ws.data_ptr(), need,
+                                           torch.cuda.current_stream().cuda_stream) == dg.GEMM_OK
+            torch.cuda.synchronize()
+            assert torch.equal(dz[:, n:], wide[:, n:])
+            if groups:
+                assert torch.equal(dz[rows - 5:], wide[rows - 5:])
+            found.append((dz, dbias))
+        assert torch.equal(found[0][0], found[1][0]) and torch.equal(found[0][1], found[1][1])
+        z, d = pre.double(), wide[:, :n].double()
+        q = torch.sigmoid(z)
+        want = d * (q + z * q * (1 - q))
+        live = slice(0, rows - 5 if groups else rows)
+        # as linear_ref: the slope within 2^-20 (1 + |z|), one product, one rounding
+        bound = d.abs() * 2.0 ** -20 * (1 + z.abs()) + 2.0 ** -23 * want.abs()
+        bound = bound + torch.finfo(dtype).eps / 2 * (want.abs() + bound) + 1e-37
+        assert bool(((found[1][0][:, :n].double() - want).abs() <= bound)[live].all())
