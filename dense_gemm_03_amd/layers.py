@@ -137,10 +137,10 @@ def _torch():
     if _CODES is None:
         import torch as t
         torch = t
-        _CODES = {t.float32: 0, t.bfloat16: 1}
         # torch's current stream as a handle, without making a Stream object
         _raw_stream = getattr(t._C, "_cuda_getCurrentRawStream",
                               lambda index: t.cuda.current_stream(index).cuda_stream)
+        _CODES = {t.float32: 0, t.bfloat16: 1}   # last: it tells other threads that the rest is there
     return torch
 
 

@@ -221,3 +221,69 @@ def test_dz_in_the_place_of_dy(cuda, dtype, rows, n, pitch):
         bound = d.abs() * 2.0 ** -20 * (1 + z.abs()) + 2.0 ** -23 * want.abs()
         bound = bound + torch.finfo(dtype).eps / 2 * (want.abs() + bound) + 1e-37
         assert bool(((found[1][0][:, :n].double() - want).abs() <= bound)[live].all())
+
+
+# ---------------------------------------------------------------- threads --
+
+def test_first_calls_of_two_threads(monkeypatch):
+    """A thread that finds the module set up finds all of it: the name that says
+    so is set last."""
+    layers._torch()
+    ready = layers._CODES
+    assert ready is not None and layers._raw_stream is not None
+    monkeypatch.setattr(layers, "_CODES", None)
+    monkeypatch.setattr(layers, "_raw_stream", None)
+    seen = []
+
+    def looked_up(obj, name, *default):   # another thread's view at that moment
+        seen.append(layers._CODES)
+        return getattr(obj, name, *default)
+
+    monkeypatch.setattr(layers, "getattr", looked_up, raising=False)
+    layers._torch()
+    assert seen == [None] and layers._CODES == ready and layers._raw_stream is not None
+
+
+@pytest.mark.gpu
+def test_two_threads_at_once(cuda):
+    """Calls of two host threads on streams of their own, one of them with a
+    forced entry and slices: each thread's results are those it gets alone."""
+    import threading
+    torch.manual_seed(3)
+    jobs = []
+    for m, n, k in ((300, 200, 264), (40, 512, 1024)):
+        x, w = torch.randn(m, k, device="cuda").bfloat16(), torch.randn(k, n, device="cuda").bfloat16()
+        dy, z = torch.randn(m, n, device="cuda").bfloat16(), torch.randn(m, n, device="cuda").bfloat16()
+        jobs.append((x, w, dy, z))
+
+    def work(i):
+        x, w, dy, z = jobs[i]
+        dg.gemm_linear_force_config(1 if i else -1, 3 if i else 0)
+        try:
+            return [dg.linear(x, w, act="gelu", alpha=1.0 + i), *dg.linear_grad(dy, x, w, act="silu", pre=z)]
+        finally:
+            dg.gemm_linear_force_config()
+
+    want = [work(i) for i in range(2)]
+    torch.cuda.synchronize()
+    start, wrong = threading.Barrier(2), []
+
+    def thread(i):
+        stream = torch.cuda.Stream()
+        start.wait()
+        try:
+            with torch.cuda.stream(stream):
+                for _ in range(50):
+                    got = work(i)
+                    stream.synchronize()
+                    if not all(torch.equal(a, b) for a, b in zip(got, want[i])):
+                        wrong.append(i)
+        except Exception as e:   # a failed call of a thread is the test's failure
+            wrong.append(e)
+
+    threads = [threading.Thread(target=thread, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong, wrong
