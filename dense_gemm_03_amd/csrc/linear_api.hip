@@ -15,6 +15,7 @@ namespace {
 
 constexpr int64_t kMaxSize = int64_t(1) << 30;   // as gemm.h
 constexpr int64_t kMaxGroups = 65535;
+constexpr int64_t kMaxThreads = UINT32_MAX;      // of one launch
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int size_of(int dtype) { return dtype == GEMM_DTYPE_F32 ? 4 : 2; }
@@ -99,6 +100,26 @@ double estimate_rows(const LinearConfig &c, double tiles, int64_t N, int64_t K, 
     return 3.3 + busy * ((double)c.bn + std::min(rows, 16.0)) * (double)K * es / 38e3;
 }
 
+// Compute units per XCD that pieces of a last round go to (xcd_piece); 0 for
+// entries without pieces.
+int64_t piece_slots(const LinearConfig &c, int dtype, int64_t cus)
+{
+    return c.bm == 256 && c.bn == 256 && dtype == GEMM_DTYPE_BF16 ? cus / 8 : 0;
+}
+
+// Blocks of an entry's grid.  Per XCD: the tiles (or, grouped, the most there
+// can be), rounded up for either list, and room for the pieces of a last round:
+// at most 3/4 of the slots more, and one more per group's last row of tiles.
+int64_t grid_blocks(int64_t tiles_m, int64_t tiles_n, bool wgrad, int64_t groups, int64_t rows, int64_t splits,
+                    int64_t slots)
+{
+    const int64_t tiles = tiles_m * tiles_n;
+    if (tiles > kMaxThreads) return INT64_MAX;   // and the products below stay in 64 bits
+    const int64_t lasts = wgrad ? 0 : std::min(groups, rows) * tiles_n * splits;
+    return 8 * ((wgrad ? ceil_div(tiles, 8) * groups * splits : tiles * splits / 8 + 2) +
+                (slots > 0 ? ceil_div(slots * 3, 4) + lasts / 8 + 2 : 0));
+}
+
 Plan find_plan(const gemm_linear_params &p, bool wgrad, int64_t cus)
 {
     Plan pl;
@@ -149,6 +170,14 @@ Plan find_plan(const gemm_linear_params &p, bool wgrad, int64_t cus)
                                  : row_tiles((int64_t(1) << 31)) * (double)K * (double)N) * es / 4.7e6;
     auto with_stream = [&](double t, double part) { return std::max(stream, t) + part * std::min(stream, t); };
 
+    auto tiles_m = [&](const LinearConfig &c) {
+        return !wgrad && grouped ? M / c.bm + std::min(groups, M) : ceil_div(M, c.bm);
+    };
+    auto launchable = [&](const LinearConfig &c, int64_t s) {
+        return grid_blocks(tiles_m(c), ceil_div(N, c.bn), wgrad, groups, p.rows, s, piece_slots(c, p.dtype, cus)) <=
+               kMaxThreads / c.threads;
+    };
+
     int count = 0;
     const LinearConfig *tab = linear_configs(p.dtype, &count);
     double best = 0.0;
@@ -158,7 +187,7 @@ Plan find_plan(const gemm_linear_params &p, bool wgrad, int64_t cus)
         if (c.fn[pl.form][0] == nullptr || (t_cfg >= 0 && i != t_cfg)) continue;
         if (c.stages == 0) {
             const double t = with_stream(estimate_rows(c, row_tiles(16), N, K, per, cus, es), 0.1);
-            if (pl.cfg < 0 || t < best) {
+            if (launchable(c, 1) && (pl.cfg < 0 || t < best)) {
                 pl.cfg = i;
                 pl.splits = 1;
                 best = t;
@@ -177,7 +206,7 @@ Plan find_plan(const gemm_linear_params &p, bool wgrad, int64_t cus)
                                              es == 2 && c.stages == 2 && c.bm < 256 ? 0.5 : 0.1);
             const bool copied = may_copy && whole + copying < whole * in_place;
             const double t = copied ? whole + copying : whole * in_place;
-            if (pl.cfg < 0 || t < best) {
+            if (launchable(c, s) && (pl.cfg < 0 || t < best)) {
                 pl.cfg = i;
                 pl.splits = (int)s;
                 best = t;
@@ -189,8 +218,7 @@ Plan find_plan(const gemm_linear_params &p, bool wgrad, int64_t cus)
     if (pl.cfg < 0) return pl;
     const LinearConfig &c = tab[pl.cfg];
     pl.tiles_n = ceil_div(N, c.bn);
-    pl.tiles_m = wgrad ? ceil_div(M, c.bm)
-                       : grouped ? M / c.bm + std::min(groups, M) : ceil_div(M, c.bm);
+    pl.tiles_m = tiles_m(c);
     if (pl.splits > 1) pl.ws_bytes = (pl.splits * out * 4 + 255) / 256 * 256;
 
     if (copies && x_odd) {
@@ -266,17 +294,8 @@ int launch_plan(const Plan &pl, int dtype, LinearArgs &a, bool wgrad, void *work
     a.group_m = c.group_m;
     a.k_per_split = (int)(ceil_div(ceil_div(a.K, c.bk), pl.splits) * c.bk);
     a.ws = pl.splits > 1 ? static_cast<float *>(workspace) : nullptr;
-    // Blocks per XCD, for all eight: the tiles (or, grouped, the most there can
-    // be), rounded up for either list, and room for the pieces of a last round
-    // (xcd_piece): at most 3/4 of the slots more, and one more per group's last
-    // row of tiles.
-    const int64_t tiles = pl.tiles_m * pl.tiles_n;
-    a.slots = c.bm == 256 && c.bn == 256 && dtype == GEMM_DTYPE_BF16 ? device_compute_units() / 8 : 0;
-    const int64_t lasts = wgrad ? 0 : std::min<int64_t>(a.groups, a.rows) * pl.tiles_n * pl.splits;
-    const int64_t per = (wgrad ? ceil_div(tiles, 8) * a.groups * pl.splits : tiles * pl.splits / 8 + 2) +
-                        (a.slots > 0 ? ceil_div(a.slots * 3, 4) + lasts / 8 + 2 : 0);
-    if (per > INT32_MAX / 8) return GEMM_ERR_INVALID_ARG;
-    const int64_t blocks = per * 8;
+    a.slots = (int)piece_slots(c, dtype, device_compute_units());
+    const int64_t blocks = grid_blocks(pl.tiles_m, pl.tiles_n, wgrad, a.groups, a.rows, pl.splits, a.slots);
     if (c.fn[pl.form][x16 && w16 ? 0 : 1](a, (int)blocks, stream) != hipSuccess) return GEMM_ERR_HIP;
     if (pl.splits > 1 && launch_linear_reduce(a, wgrad, stream) != hipSuccess) return GEMM_ERR_HIP;
     return GEMM_OK;
@@ -311,6 +330,17 @@ int64_t act_grad_chunks(const gemm_linear_params &p)
 
 int64_t act_grad_bytes(const gemm_linear_params &p) { return act_grad_chunks(p) * p.N * 4; }
 
+// Whether launch_act_grad's grids hold in a launch: blocks of 16 bytes per lane
+// (below 1024 of those there may be 8 times as many, still few), and the reduce.
+bool act_grad_fits(const gemm_linear_params &p, bool dbias)
+{
+    const bool whole = act_grad_rows(p) == 0;
+    const int64_t groups = std::max<int64_t>(1, p.groups);
+    const int64_t blocks = (whole ? groups : act_grad_chunks(p)) * ceil_div(p.N, p.dtype == GEMM_DTYPE_F32 ? 256 : 512);
+    return blocks <= kMaxThreads / (whole ? 1024 : 256) &&
+           (!dbias || whole || groups * ceil_div(p.N, 64) <= kMaxThreads / 256);
+}
+
 int need_device()
 {
     int device = -1;
@@ -339,7 +369,7 @@ int linear(const gemm_linear_params *p, const void *x, const void *w, const int3
     gemm_linear_params q = *p;
     if (!sums) q.K = 0;
     const Plan pl = make_plan(q, false);
-    if (pl.cfg < 0) return t_cfg >= 0 ? GEMM_ERR_INVALID_ARG : GEMM_ERR_INTERNAL;
+    if (pl.cfg < 0) return GEMM_ERR_INVALID_ARG;   // no entry, or no forced one, for this form and size
     if (!valid_workspace(workspace, workspace_bytes, empty ? 0 : pl.ws_bytes)) return GEMM_ERR_INVALID_ARG;
     if (empty) return GEMM_OK;
     if (const int rc = need_device()) return rc;
@@ -389,7 +419,7 @@ int act_grad(const gemm_linear_params *p, const void *dy, int64_t lddy, const vo
     const int64_t need = dbias && p->N > 0 ? act_grad_bytes(*p) : 0;
     if (!valid_workspace(workspace, workspace_bytes, need)) return GEMM_ERR_INVALID_ARG;
     if (p->N == 0 || (!dz && !dbias) || (p->rows == 0 && !dbias)) return GEMM_OK;
-    if (p->groups > 0 && !offsets) return GEMM_ERR_INVALID_ARG;
+    if ((p->groups > 0 && !offsets) || !act_grad_fits(*p, dbias != nullptr)) return GEMM_ERR_INVALID_ARG;
     if (const int rc = need_device()) return rc;
     ActGradArgs a{};
     a.dy = dy;
@@ -409,11 +439,8 @@ int act_grad(const gemm_linear_params *p, const void *dy, int64_t lddy, const vo
     a.pre_bf16 = p->dtype_y == GEMM_DTYPE_BF16;
     a.vec = aligned16(dy, lddy, 0, p->dtype) && (!dz || aligned16(dz, lddz, 0, p->dtype)) &&
             (!act || p->dtype_y != p->dtype || aligned16(pre, p->ldp, 0, p->dtype_y));
-    const int64_t chunks = act_grad_chunks(*p);
-    a.chunks = (int)chunks;
+    a.chunks = (int)act_grad_chunks(*p);
     a.chunk_rows = act_grad_rows(*p);
-    if (chunks * ceil_div(p->N, 64) > INT32_MAX || a.groups * ceil_div(p->N, 64) > INT32_MAX)
-        return GEMM_ERR_INVALID_ARG;
     return launch_act_grad(a, stream) == hipSuccess ? GEMM_OK : GEMM_ERR_HIP;
 }
 
@@ -431,7 +458,7 @@ int weight_grad(const gemm_linear_params *p, const void *x, const void *dz, cons
     gemm_linear_params q = *p;
     if (!sums) q.rows = 0;
     const Plan pl = make_plan(q, true);
-    if (pl.cfg < 0) return t_cfg >= 0 ? GEMM_ERR_INVALID_ARG : GEMM_ERR_INTERNAL;
+    if (pl.cfg < 0) return GEMM_ERR_INVALID_ARG;   // no entry, or no forced one, for this form and size
     if (!valid_workspace(workspace, workspace_bytes, empty ? 0 : pl.ws_bytes)) return GEMM_ERR_INVALID_ARG;
     if (empty) return GEMM_OK;
     if (const int rc = need_device()) return rc;
@@ -469,7 +496,7 @@ struct GradParts {
     gemm_linear_params act, dx, dw;
     int64_t lddz = 0, dz_bytes = 0, act_bytes = 0, dx_bytes = 0, dw_bytes = 0, total = 0;
     bool need_act = false, need_dz = false;
-    bool forms = true;   // false: a forced entry lacks a form
+    bool forms = true;   // false: no entry, or not the forced one, has a form and its size
 };
 
 int64_t round16(int64_t n) { return (n + 15) / 16 * 16; }
@@ -537,7 +564,7 @@ int grad(const gemm_linear_params *p, const gemm_linear_grad_outputs *o, const v
     if (p->ldy < std::max<int64_t>(p->N, 1) ||
         (g.need_act && p->act != GEMM_ACT_NONE && (p->ldp < std::max<int64_t>(p->N, 1) || (some && !pre))) ||
         (some && !dy) || (p->groups > 0 && !offsets) || misaligned(dy, p->dtype) || misaligned(pre, p->dtype_y) ||
-        (uintptr_t)dbias % 4 || (uintptr_t)offsets % 4)
+        (uintptr_t)dbias % 4 || (uintptr_t)offsets % 4 || (g.need_act && !act_grad_fits(*p, dbias != nullptr)))
         return GEMM_ERR_INVALID_ARG;
     if (dx && (o->lddx < std::max<int64_t>(p->K, 1) || misaligned(dx, o->dtype_dx) || misaligned(w, p->dtype) ||
                (some && p->K > 0 && sums && !w)))
@@ -652,7 +679,7 @@ int gemm_linear_select_config(const gemm_linear_params *p, int weight_grad)
 {
     if (!dg::valid_sizes(p)) return GEMM_ERR_INVALID_ARG;
     const int cfg = dg::make_plan(*p, weight_grad != 0).cfg;
-    return cfg >= 0 ? cfg : dg::t_cfg >= 0 ? GEMM_ERR_INVALID_ARG : GEMM_ERR_INTERNAL;
+    return cfg >= 0 ? cfg : GEMM_ERR_INVALID_ARG;
 }
 
 int gemm_linear_force_config(int cfg, int split_k)

@@ -47,19 +47,21 @@
  * Memory: every pointer is a device pointer of the caller's, aligned to its
  * element; outputs must not overlap inputs, except that residual may be y
  * itself, and dz of gemm_linear_act_grad may be dy itself, with the same leading
- * dimension (GEMM_ERR_INVALID_ARG otherwise).  The calls take their scratch memory from
- * the caller (workspace, 16-byte aligned, at least the bytes that the
- * *_workspace_size function of the same parameters returns; contents on entry
- * do not matter); the library allocates nothing and keeps nothing, so the
- * calls may be captured into HIP graphs, and calls with workspaces of their
- * own may run at the same time.
+ * dimension (GEMM_ERR_INVALID_ARG otherwise).  The calls take their scratch
+ * memory from the caller (workspace, 16-byte aligned, at least the bytes that
+ * the _workspace_size function of the same parameters returns; contents on entry
+ * do not matter); the library allocates nothing and keeps nothing, so the calls
+ * may be captured into HIP graphs, and calls with workspaces of their own may
+ * run at the same time.
  *
  * Streams, threads, errors: as in gemm.h.  Argument checks come before any HIP
  * call: GEMM_ERR_INVALID_ARG for an unknown type, activation or transposition,
  * negative sizes or sizes above 2^30, a leading dimension shorter than its row,
- * a null or misaligned pointer of a non-empty operand, or a workspace that is
- * too small.  rows == 0 or N == 0 launches nothing (the gradients of empty
- * sums are still written: dw and dbias of no rows are zeros, or beta * dw).
+ * a null or misaligned pointer of a non-empty operand, a workspace that is too
+ * small, or a call whose kernels would need 2^32 threads or more (from about
+ * 2^39 outputs on, or groups x N of 2^30 in dbias).  rows == 0 or N == 0
+ * launches nothing (the gradients of empty sums are still written: dw and dbias
+ * of no rows are zeros, or beta * dw).
  */
 #ifndef DENSE_GEMM_03_AMD_GEMM_LINEAR_H
 #define DENSE_GEMM_03_AMD_GEMM_LINEAR_H

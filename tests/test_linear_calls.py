@@ -287,3 +287,54 @@ def test_two_threads_at_once(cuda):
     for t in threads:
         t.join()
     assert not wrong, wrong
+
+
+# ----------------------------------------------------------- largest sizes --
+
+def blocks_and_threads(dtype, cfg, rows, n):
+    """Blocks (at least) of the dense forward product and threads of a block,
+    from the entry's name."""
+    import re
+    name = dg.gemm_linear_config_name(dtype, cfg)
+    few = re.search(r"rows_[nt]_w(\d+)x(\d+)", name)
+    if few:
+        bm, bn, waves = 16, 16 * int(few[1]), int(few[2])
+    else:
+        bm, bn, wm, wn = map(int, re.search(r"_(\d+)x(\d+)x\d+_w(\d+)x(\d+)_", name).groups())
+        waves = wm * wn
+    return -(-rows // bm) * -(-n // bn), 64 * waves
+
+
+@pytest.mark.parametrize("dtype", [0, 1])
+@pytest.mark.parametrize("rows,n", [(1, 1 << 30), (1, 1 << 29), (1 << 30, 1), (16, 1 << 30), (1 << 30, 16), (1 << 29, 64)])
+def test_the_largest_sizes_get_an_entry_that_a_launch_can_hold(dtype, rows, n):
+    """A launch has fewer than 2^32 threads."""
+    for transw in (0, 1):
+        for k in (1, 64):
+            p = params(dtype=dtype, rows=rows, N=n, K=k, transw=transw, ldx=k, ldw=k if transw else n, ldy=n, ldr=n, ldp=n)
+            cfg = dg.gemm_linear_select_config(p)
+            assert cfg >= 0
+            blocks, threads = blocks_and_threads(dtype, cfg, rows, n)
+            assert blocks * threads < 1 << 32, (dg.gemm_linear_config_name(dtype, cfg), blocks, threads)
+
+
+def test_sums_too_long_for_a_launch_are_refused_before_it():
+    big = 1 << 60
+    for kw in (dict(dtype=0, dtype_y=0, rows=1, N=1 << 30), dict(rows=1 << 11, groups=65535, N=1 << 20)):
+        n = kw["N"]
+        p = params(ldp=n, ldw=n, ldy=n, stride_w=64 * n, **kw)
+        assert dg.gemm_linear_act_grad(p, P, n, P, P, None, n, P, P, big) == BAD, kw
+        o = dg.LinearGradOutputs(0, 0, 0.0, 0, 64, n, 64 * n)
+        assert dg.gemm_linear_grad(p, o, P, P, P, P, P, None, None, P, P, big) == BAD, kw
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("transb", [False, True])
+def test_half_a_billion_outputs_of_one_row(cuda, transb):
+    """More columns than few-row blocks can cover in one launch."""
+    n = (1 << 29) + 64
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    w = torch.randn(n, generator=gen, device="cuda").bfloat16()
+    x = torch.full((1, 1), 2.0, device="cuda", dtype=torch.bfloat16)
+    y = dg.linear(x, w.view(n, 1) if transb else w.view(1, n), transb=transb, out_dtype=torch.bfloat16)
+    assert torch.equal(y.view(-1), w * 2)
