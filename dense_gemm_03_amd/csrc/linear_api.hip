@@ -546,32 +546,34 @@ GradParts grad_parts(const gemm_linear_params &p, const gemm_linear_grad_outputs
     return g;
 }
 
-bool valid_outputs(const gemm_linear_grad_outputs *o)
+// Sizes, types and leading dimensions of a backward pass that forms dx and dw if asked to.
+bool valid_backward(const gemm_linear_params *p, const gemm_linear_grad_outputs *o, bool dx, bool dw)
 {
-    return o != nullptr && known(o->dtype_dx) && known(o->dtype_dw);
+    if (!valid_sizes(p) || o == nullptr || !known(o->dtype_dx) || !known(o->dtype_dw) || !valid_operands(p) ||
+        p->ldy < std::max<int64_t>(p->N, 1) || (dx && o->lddx < std::max<int64_t>(p->K, 1)))
+        return false;
+    gemm_linear_params q = *p;   // dw lies as w does
+    q.ldw = o->lddw;
+    q.stride_w = o->stride_dw;
+    return !dw || valid_operands(&q);
 }
 
 int grad(const gemm_linear_params *p, const gemm_linear_grad_outputs *o, const void *dy, const void *x,
          const void *w, const int32_t *offsets, const void *pre, void *dx, void *dw, float *dbias,
          void *workspace, int64_t workspace_bytes, hipStream_t stream)
 {
-    if (!valid_sizes(p) || !valid_outputs(o) || !valid_operands(p)) return GEMM_ERR_INVALID_ARG;
+    if (!valid_backward(p, o, dx != nullptr, dw != nullptr)) return GEMM_ERR_INVALID_ARG;
     const GradParts g = grad_parts(*p, *o, dx != nullptr, dw != nullptr, dbias != nullptr);
     if (!g.forms || !valid_workspace(workspace, workspace_bytes, g.total)) return GEMM_ERR_INVALID_ARG;
     // what the parts check before they launch, checked for all of them before the first
     const bool some = p->rows > 0 && p->N > 0, sums = p->alpha != 0.0f;
-    const int64_t wrow = p->transw == GEMM_OP_T ? p->K : p->N, wrows = p->transw == GEMM_OP_T ? p->N : p->K;
-    if (p->ldy < std::max<int64_t>(p->N, 1) ||
-        (g.need_act && p->act != GEMM_ACT_NONE && (p->ldp < std::max<int64_t>(p->N, 1) || (some && !pre))) ||
+    if ((g.need_act && p->act != GEMM_ACT_NONE && (p->ldp < std::max<int64_t>(p->N, 1) || (some && !pre))) ||
         (some && !dy) || (p->groups > 0 && !offsets) || misaligned(dy, p->dtype) || misaligned(pre, p->dtype_y) ||
         (uintptr_t)dbias % 4 || (uintptr_t)offsets % 4 || (g.need_act && !act_grad_fits(*p, dbias != nullptr)))
         return GEMM_ERR_INVALID_ARG;
-    if (dx && (o->lddx < std::max<int64_t>(p->K, 1) || misaligned(dx, o->dtype_dx) || misaligned(w, p->dtype) ||
-               (some && p->K > 0 && sums && !w)))
+    if (dx && (misaligned(dx, o->dtype_dx) || misaligned(w, p->dtype) || (some && p->K > 0 && sums && !w)))
         return GEMM_ERR_INVALID_ARG;
-    if (dw && (o->lddw < std::max<int64_t>(wrow, 1) || o->lddw > (int64_t(1) << 40) ||
-               (p->groups > 1 && wrow > 0 && wrows > 0 && o->stride_dw < (wrows - 1) * o->lddw + wrow) ||
-               misaligned(dw, o->dtype_dw) || misaligned(x, p->dtype) || (some && p->K > 0 && sums && !x)))
+    if (dw && (misaligned(dw, o->dtype_dw) || misaligned(x, p->dtype) || (some && p->K > 0 && sums && !x)))
         return GEMM_ERR_INVALID_ARG;
     void *dz = g.need_dz ? workspace : const_cast<void *>(dy);
     void *scratch = workspace ? static_cast<char *>(workspace) + g.dz_bytes : nullptr;
@@ -596,8 +598,9 @@ extern "C" {
 int64_t gemm_linear_grad_workspace_size(const gemm_linear_params *p, const gemm_linear_grad_outputs *o, int dx,
                                         int dw, int dbias)
 {
-    if (!dg::valid_sizes(p) || !dg::valid_outputs(o)) return GEMM_ERR_INVALID_ARG;
-    return dg::grad_parts(*p, *o, dx != 0, dw != 0, dbias != 0).total;
+    if (!dg::valid_backward(p, o, dx != 0, dw != 0)) return GEMM_ERR_INVALID_ARG;
+    const dg::GradParts g = dg::grad_parts(*p, *o, dx != 0, dw != 0, dbias != 0);
+    return g.forms ? g.total : GEMM_ERR_INVALID_ARG;
 }
 
 int gemm_linear_grad(const gemm_linear_params *p, const gemm_linear_grad_outputs *o, const void *dy,
@@ -609,10 +612,12 @@ int gemm_linear_grad(const gemm_linear_params *p, const gemm_linear_grad_outputs
 
 int64_t gemm_linear_workspace_size(const gemm_linear_params *p)
 {
-    if (!dg::valid_sizes(p)) return GEMM_ERR_INVALID_ARG;
+    if (!dg::valid_sizes(p) || !dg::valid_operands(p)) return GEMM_ERR_INVALID_ARG;
     gemm_linear_params q = *p;
     if (p->alpha == 0.0f) q.K = 0;
-    return p->rows == 0 || p->N == 0 ? 0 : dg::make_plan(q, false).ws_bytes;
+    const dg::Plan pl = dg::make_plan(q, false);
+    if (pl.cfg < 0) return GEMM_ERR_INVALID_ARG;
+    return p->rows == 0 || p->N == 0 ? 0 : pl.ws_bytes;
 }
 
 int gemm_linear(const gemm_linear_params *p, const void *x, const void *w, const int32_t *offsets,
@@ -637,10 +642,13 @@ int gemm_linear_act_grad(const gemm_linear_params *p, const void *dy, int64_t ld
 
 int64_t gemm_linear_weight_grad_workspace_size(const gemm_linear_params *p)
 {
-    if (!dg::valid_sizes(p)) return GEMM_ERR_INVALID_ARG;
+    if (!dg::valid_sizes(p) || !dg::valid_operands(p) || p->ldy < std::max<int64_t>(p->N, 1))
+        return GEMM_ERR_INVALID_ARG;
     gemm_linear_params q = *p;
     if (p->alpha == 0.0f) q.rows = 0;
-    return p->K == 0 || p->N == 0 ? 0 : dg::make_plan(q, true).ws_bytes;
+    const dg::Plan pl = dg::make_plan(q, true);
+    if (pl.cfg < 0) return GEMM_ERR_INVALID_ARG;
+    return p->K == 0 || p->N == 0 ? 0 : pl.ws_bytes;
 }
 
 int gemm_linear_weight_grad(const gemm_linear_params *p, const void *x, const void *dz,

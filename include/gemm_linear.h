@@ -49,7 +49,7 @@
  * itself, and dz of gemm_linear_act_grad may be dy itself, with the same leading
  * dimension (GEMM_ERR_INVALID_ARG otherwise).  The calls take their scratch
  * memory from the caller (workspace, 16-byte aligned, at least the bytes that
- * the _workspace_size function of the same parameters returns; contents on entry
+ * the *_workspace_size function of the same parameters returns; contents on entry
  * do not matter); the library allocates nothing and keeps nothing, so the calls
  * may be captured into HIP graphs, and calls with workspaces of their own may
  * run at the same time.

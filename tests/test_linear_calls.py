@@ -338,3 +338,30 @@ def test_half_a_billion_outputs_of_one_row(cuda, transb):
     x = torch.full((1, 1), 2.0, device="cuda", dtype=torch.bfloat16)
     y = dg.linear(x, w.view(n, 1) if transb else w.view(1, n), transb=transb, out_dtype=torch.bfloat16)
     assert torch.equal(y.view(-1), w * 2)
+
+
+# -------------------------------------------------------- workspace sizes --
+
+def test_size_functions_refuse_what_the_calls_refuse():
+    grouped = dict(groups=3, stride_bias=48)
+    outputs = lambda **kw: dg.LinearGradOutputs(**{**dict(dtype_dx=0, dtype_dw=0, beta=0.0, lddx=64, lddw=48,  # noqa: E731
+                                                          stride_dw=64 * 48), **kw})
+    for kw in (dict(ldx=63), dict(ldw=47), dict(ldx=-64), dict(transw=1, ldw=63), dict(stride_w=64 * 48 - 1, **grouped)):
+        assert dg.gemm_linear_workspace_size(params(**kw)) == BAD, kw
+        assert dg.gemm_linear_weight_grad_workspace_size(params(**kw)) == BAD, kw
+        assert dg.gemm_linear_grad_workspace_size(params(**kw), outputs()) == BAD, kw
+    assert dg.gemm_linear_weight_grad_workspace_size(params(ldy=47)) == BAD
+    assert dg.gemm_linear_grad_workspace_size(params(ldy=47), outputs()) == BAD
+    assert dg.gemm_linear_grad_workspace_size(params(), outputs(lddx=63)) == BAD
+    assert dg.gemm_linear_grad_workspace_size(params(), outputs(lddx=63), 0, 1, 1) > 0     # not asked for
+    assert dg.gemm_linear_grad_workspace_size(params(), outputs(lddw=47)) == BAD
+    assert dg.gemm_linear_grad_workspace_size(params(), outputs(lddw=47), 1, 0, 1) > 0
+    rows = [c for c in range(dg.gemm_linear_num_configs(1)) if dg.gemm_linear_config_forms(1, c) == 1]
+    dg.gemm_linear_force_config(rows[0])      # has w as K x N only
+    try:
+        assert dg.gemm_linear_workspace_size(params()) == 0
+        assert dg.gemm_linear_workspace_size(params(transw=1, ldw=64)) == BAD
+        assert dg.gemm_linear_weight_grad_workspace_size(params()) == BAD
+        assert dg.gemm_linear_grad_workspace_size(params(), outputs()) == BAD
+    finally:
+        dg.gemm_linear_force_config()
