@@ -365,3 +365,67 @@ def test_size_functions_refuse_what_the_calls_refuse():
         assert dg.gemm_linear_grad_workspace_size(params(), outputs()) == BAD
     finally:
         dg.gemm_linear_force_config()
+
+
+# ------------------------------------------------------------- alignments --
+
+def placed(t, shift):
+    """t in rows of a 16-byte pitch that begin `shift` elements past a 16-byte
+    boundary, NaN around them."""
+    pitch = -(-(t.shape[-1] + shift) // 8) * 8
+    rows = t[..., 0].numel()
+    flat = torch.full((rows * pitch + shift + 8,), float("nan"), dtype=t.dtype, device="cuda")
+    assert flat.data_ptr() % 16 == 0
+    strides = [pitch, 1] if t.dim() == 2 else [t.shape[1] * pitch, pitch, 1]
+    v = flat.as_strided(t.shape, strides, shift)
+    v.copy_(t)
+    return v, flat
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("transb", [False, True])
+@pytest.mark.parametrize("which", ["x", "w", "both", "outputs"])
+def test_aligned_pitches_at_other_addresses(cuda, dtype, transb, which):
+    """Operands and outputs whose pitch is a whole number of 16 bytes and whose
+    address is not, through every entry: whole numbers, so the sums are exact."""
+    code = dg.GEMM_DTYPE_BF16 if dtype == torch.bfloat16 else dg.GEMM_DTYPE_F32
+    gen = torch.Generator().manual_seed(5)
+    ints = lambda *s: torch.randint(-3, 4, s, generator=gen).to(dtype).cuda()  # noqa: E731
+    m, n, k = 300, 296, 344
+    x, w, dz = ints(m, k), ints(*((n, k) if transb else (k, n))), ints(m, n)
+    residual = ints(m, n)
+    w3, off = torch.stack([w, -w]), torch.tensor([0, 130, 290], dtype=torch.int32, device="cuda")
+    y64 = x.double() @ (w.double().t() if transb else w.double())
+    dw64 = (dz.double().t() @ x.double()) if transb else (x.double().t() @ dz.double())
+    dx64 = dz.double() @ (w.double() if transb else w.double().t())
+    for shift in (1, 2, 3, 4):
+        sx = shift if which in ("x", "both") else 0
+        sw = shift if which in ("w", "both") else 0
+        so = shift if which == "outputs" else 0
+        xs, ws, dzs = placed(x, sx)[0], placed(w, sw)[0], placed(dz, sw)[0]
+        w3s, rs = placed(w3, sw)[0], placed(residual.float(), so)[0]
+        for cfg in [-1, *range(dg.gemm_linear_num_configs(code))]:
+            forms = 7 if cfg < 0 else dg.gemm_linear_config_forms(code, cfg)
+            out, around = placed(torch.zeros(m, n, device="cuda"), so)
+            grad, around_grad = placed(torch.zeros(*w.shape, device="cuda"), so)
+            before = int(torch.isnan(around).sum()), int(torch.isnan(around_grad).sum())
+            dg.gemm_linear_force_config(cfg)
+            try:
+                if forms >> transb & 1:
+                    dg.linear(xs, ws, transb=transb, residual=rs, out=out)
+                    grouped = dg.grouped_linear(xs, w3s, off, transb=transb)
+                if forms & 4:
+                    dg.linear_grad(dzs, xs, ws, transb=transb, need_dx=False, need_dbias=False, dw=grad)
+                if cfg < 0:
+                    dx = dg.linear_grad(dzs, xs, ws, transb=transb, need_dw=False)[0]
+                    assert torch.equal(dx.double(), dx64)
+            finally:
+                dg.gemm_linear_force_config()
+            if forms >> transb & 1:
+                assert torch.equal(out.double(), y64 + residual.double()), (shift, cfg)
+                assert torch.equal(grouped[:130].double(), y64[:130]), (shift, cfg)
+                assert torch.equal(grouped[130:290].double(), -y64[130:290]), (shift, cfg)
+            if forms & 4:
+                assert torch.equal(grad.double(), dw64), (shift, cfg)
+            assert before == (int(torch.isnan(around).sum()), int(torch.isnan(around_grad).sum()))
