@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(CHUNKS ? 256 : 1024) act_grad_kernel(ActGradAr
         load(p.dy, row * p.lddy + col0, BF16, g);
         if (p.act != ACT_NONE) {
             load(p.pre, row * p.ldp + col0, p.pre_bf16 != 0, z);
-            act_slope<V>(p.act, z);
+            act_slope<V, !BF16>(p.act, z);
 #pragma unroll
             for (int i = 0; i < V; ++i) g[i] *= z[i];
         }

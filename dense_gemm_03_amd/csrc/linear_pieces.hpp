@@ -20,7 +20,9 @@ struct Piece {
     int which;    // -1: the whole tile; quarter 0 .. 3: row half + 2 * column half; 4, 5: row half
 };
 
-constexpr Piece xcd_piece(int j, int n, int small, int slots)
+// Inlined whatever its size: behind a call the compiler would take the place for
+// one that differs from lane to lane, and addresses made from it with it.
+__attribute__((always_inline)) constexpr inline Piece xcd_piece(int j, int n, int small, int slots)
 {
     if (slots == 0) return {j < n + small ? j : -1, -1};
     const int r = n % slots, of = 4 * r <= slots ? 4 : 2 * r <= slots ? 2 : 1;
