@@ -64,12 +64,16 @@ struct Plan {
 // cut into s slices: rounds of blocks over the compute units, k-tiles at the
 // rate of a full unit or of a block alone, whichever is longer, and the reduce.
 // The entries' constants, the reduce's 3.5 us + bytes / 4.6 TB/s and the model's
-// form were fitted to 23000 measurements (every entry, 1 to 16 slices, M 40 to
-// 4096, N 256 to 8192, K 512 to 8192, all forms): the choice by the model was
-// 2.1% (bf16) and 1.1% (fp32) slower in the mean than the best of all.  With
-// groups the smaller bf16 tiles run a quarter slower than that: the weights come
-// from HBM and each is read by a few row tiles only (12000 rows of 10 groups,
-// 2048 x 2048: 0.58 us per k-tile of 128 x 128, against 0.45).
+// form were fitted to timings of every entry in 1 to 16 slices (dense, M 40 to
+// 4096, N 256 to 8192, K 512 to 8192, all forms); the pieces' factors and the
+// grouped rates come from single shapes.  Against the fastest of all entries and
+// slices the choice is, in the mean, 3.1% slower over 417 dense bf16 shapes and
+// 1.2% over 363 fp32 ones, 5.2% and 2.6% for grouped y (96 and 84 shapes), but 25%
+// and 35% for grouped dw (48 and 42): the bytes of the outputs are not in the
+// model, and dw of groups of few rows is mostly those.  With groups the smaller
+// bf16 tiles are taken to run a quarter slower: the weights come from HBM and each
+// is read by a few row tiles only (12000 rows of 10 groups, 2048 x 2048: 0.58 us per
+// k-tile of 128 x 128, against 0.45).
 double estimate(const LinearConfig &c, double tiles, bool grouped, bool exact, int64_t out, int64_t K, int64_t s,
                 int64_t cus, int es)
 {

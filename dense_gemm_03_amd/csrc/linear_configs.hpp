@@ -48,9 +48,9 @@ hipError_t launch_linear(const LinearArgs &args, int blocks, hipStream_t stream)
 // Small bf16 tiles have three or four stages: two leave less than a k-tile's
 // products to cover a load, and where a unit has one block every k-tile waits
 // (0.44 us per k-tile of 64 x 64 with two stages, 0.20 with four).  With two,
-// five blocks share a unit, which is better where a block has a k-tile or two
-// and its stores are what counts (12 groups of about one row, 1088 x 4864, the
-// backward pass: 80 us against 92 with three).
+// five blocks share a unit, which is better than three stages where a block has a
+// k-tile or two and its stores are what counts (12 groups of about one row, 1088 x
+// 4864, the backward pass: 80 us against 92).
 #define DG_LIN_BF16_TABLE(X)                                                                 \
     X("bf16_256x256x64_w2x2_s2", true, 256, 256, 64, 2, 2, 2, 8, 1.45f, 0.60f, 6.6f)         \
     X("bf16_128x128x64_w2x2_s2", true, 128, 128, 64, 2, 2, 2, 8, 0.45f, 0.565f, 1.1f)        \
