@@ -1,7 +1,9 @@
 """Linear layers over torch tensors: ``linear`` and ``grouped_linear`` (products
 with bias, activation and residual, dense or grouped by expert) and their
 gradients ``linear_grad`` and ``grouped_linear_grad``; a thin binding over
-``include/gemm_linear.h``.  The C entry points are here under their own names
+``include/gemm_linear.h``.  Like the rest of the package they take no part in
+torch's autograd: outputs carry no graph, whatever ``requires_grad`` says, and the
+backward pass is the ``*_grad`` functions.  The C entry points are here under their own names
 (``gemm_linear*``), taking parameters, device pointers and a stream."""
 from __future__ import annotations
 
@@ -331,7 +333,8 @@ def linear(x, w, bias=None, act="none", residual=None, *, alpha=1.0, transb=Fals
     bfloat16 with contiguous rows.  ``bias`` (N; float32 or bfloat16) and
     ``residual`` (M x N, y's type) are optional; ``act`` is "none", "relu",
     "gelu", "gelu_tanh" or "silu".  ``pre`` (M x N, y's type) receives the value
-    before the activation, which the backward pass needs.  y is float32 or
+    before the activation, which the backward pass (``linear_grad``; autograd sees
+    none of this) needs.  y is float32 or
     bfloat16 (``out_dtype``, default float32), created when ``out`` is not
     given; ``residual`` may be ``out`` itself.  Runs on ``stream`` (a handle;
     default: torch's current stream) and returns without synchronising.  On
