@@ -45,14 +45,14 @@
  * Results are bitwise reproducible: no atomics, fixed order of sums.
  *
  * Memory: every pointer is a device pointer of the caller's, aligned to its
- * element; outputs must not overlap inputs, except that residual may be y
- * itself, and dz of gemm_linear_act_grad may be dy itself, with the same leading
- * dimension (GEMM_ERR_INVALID_ARG otherwise).  The calls take their scratch
- * memory from the caller (workspace, 16-byte aligned, at least the bytes that
- * the *_workspace_size function of the same parameters returns; contents on entry
- * do not matter); the library allocates nothing and keeps nothing, so the calls
- * may be captured into HIP graphs, and calls with workspaces of their own may
- * run at the same time.
+ * element; outputs must not overlap inputs or one another, except that residual
+ * may be y itself, and dz of gemm_linear_act_grad may be dy itself, with the same
+ * leading dimension (GEMM_ERR_INVALID_ARG otherwise).  The calls take their
+ * scratch memory from the caller (workspace, 16-byte aligned, at least the bytes
+ * that the *_workspace_size function of the same parameters returns; contents on
+ * entry do not matter); the library allocates nothing and keeps nothing, so the
+ * calls may be captured into HIP graphs, and calls with workspaces of their own
+ * may run at the same time.
  *
  * Streams, threads, errors: as in gemm.h.  Argument checks come before any HIP
  * call: GEMM_ERR_INVALID_ARG for an unknown type, activation or transposition,
