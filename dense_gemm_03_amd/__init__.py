@@ -2,11 +2,11 @@
 generalised C = alpha * op(A) * op(B) + beta * C with fp32 or bf16 C; and 2-D
 convolution (forward and filter gradient) as im2col + that GEMM; and linear
 layers (bias, activation and residual in the product, dense or grouped by
-expert, with their gradients).
+expert, with their gradients); and what a model that answers needs next to them.
 
 A thin ctypes binding over the C ABI of ``include/gemm.h``,
-``include/conv.h`` and ``include/gemm_linear.h`` (library
-``libdense_gemm.so`` next to this file).  The functions of the same names take
+``include/conv.h``, ``include/gemm_linear.h`` and ``include/gemm_serving.h``
+(library ``libdense_gemm.so`` next to this file).  The functions of the same names take
 the same arguments as the C entry points -- sizes, device pointers as
 integers, leading dimensions and a stream handle -- and only marshal them;
 every step of the product runs in the HIP kernels.  ``gemm`` is a convenience
@@ -117,6 +117,10 @@ from .layers import (  # noqa: E402,F401
     gemm_linear_weight_grad_workspace_size, gemm_linear_workspace_size, grouped_linear,
     grouped_linear_grad, linear, linear_grad)
 from .layers import SIGNATURES as _LINEAR_SIGNATURES  # noqa: E402
+from .serving import (  # noqa: E402,F401
+    LogProbs, LogProbsParams, gemm_log_probs, gemm_log_probs_grad, gemm_log_probs_workspace_size, log_probs,
+    log_probs_grad)
+from .serving import SIGNATURES as _SERVING_SIGNATURES  # noqa: E402
 
 _lib = None
 
@@ -145,7 +149,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     except ImportError:  # pragma: no cover - C callers without torch
         pass
     lib = ctypes.CDLL(path)
-    for name, (res, args) in [*SIGNATURES.items(), *_LINEAR_SIGNATURES.items()]:
+    for name, (res, args) in [*SIGNATURES.items(), *_LINEAR_SIGNATURES.items(), *_SERVING_SIGNATURES.items()]:
         fn = getattr(lib, name)
         fn.restype = res
         fn.argtypes = args

@@ -1,0 +1,169 @@
+"""What stands around a model's products when it answers, over torch tensors:
+``log_probs`` (log probabilities of given tokens, entropy, alternatives) and its
+gradient ``log_probs_grad``; a thin binding over ``include/gemm_serving.h``.  Like
+the rest of the package they take no part in torch's autograd.  The C entry points
+are here under their own names (``gemm_*``), taking parameters, device pointers and
+a stream."""
+from __future__ import annotations
+
+import collections
+import ctypes
+
+from . import layers
+from .layers import _code, _i64, _int, _Launch, _library, _matrix, _p, _pitch, _status, _f, _torch
+
+
+class LogProbsParams(ctypes.Structure):
+    """gemm_log_probs_params of include/gemm_serving.h."""
+    _fields_ = [("dtype", ctypes.c_int32), ("top", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("reserved", ctypes.c_int32), ("rows", ctypes.c_int64), ("vocab", ctypes.c_int64),
+                ("ld", ctypes.c_int64)]
+
+
+_plp = ctypes.POINTER(LogProbsParams)
+# Every symbol include/gemm_serving.h declares, with its ctypes signature.
+SIGNATURES = {
+    "gemm_log_probs_workspace_size": (_i64, [_plp]),
+    "gemm_log_probs": (_int, [_plp] + [_p] * 8 + [_i64, _p]),
+    "gemm_log_probs_grad": (_int, [_plp] + [_p] * 7 + [_i64, _p]),
+}
+
+
+# ---------------------------------------------------------------- C names --
+
+def gemm_log_probs_workspace_size(params) -> int:
+    return _library().gemm_log_probs_workspace_size(params)
+
+
+def gemm_log_probs(params, logits, tokens, logprob, entropy, stats, top_ids, top_logprobs, workspace,
+                   workspace_bytes, stream=None) -> int:
+    return _library().gemm_log_probs(params, logits, tokens, logprob, entropy, stats, top_ids, top_logprobs,
+                                     workspace, workspace_bytes, stream)
+
+
+def gemm_log_probs_grad(params, logits, tokens, stats, entropy, dlogprob, dentropy, dlogits, ldd,
+                        stream=None) -> int:
+    return _library().gemm_log_probs_grad(params, logits, tokens, stats, entropy, dlogprob, dentropy, dlogits, ldd,
+                                          stream)
+
+
+# ---------------------------------------------------------- torch helpers --
+
+def _vector(t, shape, dtype, device, what):
+    """Pointer of a contiguous tensor of that shape and type."""
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, not %s" % (what, dtype, t.dtype))
+    if tuple(t.shape) != shape or t.device != device or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s tensor on %s, not %s on %s"
+                         % (what, shape, device, tuple(t.shape), t.device))
+    return t.data_ptr()
+
+
+# Parameter blocks by their type and values, so that a repeated call does not
+# fill one again.
+_blocks: dict = {}
+
+
+def _block(kind, *values):
+    found = _blocks.get((kind, values))
+    if found is None:
+        if len(_blocks) >= 4096:
+            _blocks.clear()
+        found = _blocks[kind, values] = kind(*values)
+    return found
+
+
+def _logits(logits):
+    if logits.dim() != 2 or logits.shape[1] < 1:
+        raise ValueError("logits must be 2-D, rows x vocabulary")
+    if logits.device.type != "cuda":
+        raise ValueError("logits must be a GPU tensor")
+    rows, vocab = logits.shape
+    return _code(logits.dtype, "logits"), rows, vocab, _pitch(logits, rows, vocab, "logits")
+
+
+LogProbs = collections.namedtuple("LogProbs", "logprob entropy stats top_ids top_logprobs")
+
+
+def log_probs(logits, tokens=None, top=0, *, scale=1.0, stream=None):
+    """Log probabilities of one token per row of logits, with the rows' entropy
+    and most likely alternatives.
+
+    ``logits`` (rows x vocabulary, float32 or bfloat16, contiguous rows) are
+    multiplied by ``scale`` (1 / temperature, > 0) first.  ``tokens`` is an int32
+    tensor of one place per row; one outside the vocabulary is padding.  ``top`` (0
+    to 64) alternatives come in falling order, equal logits by the lower place.
+    Returns ``LogProbs``, float32 but for the places (int32):
+
+        logprob        rows         of the token (0 for padding); None without tokens
+        entropy        rows
+        stats          rows x 2     the largest logit m, and log sum exp(scale (z - m)),
+                                    which ``log_probs_grad`` takes
+        top_ids        rows x top   None if top is 0
+        top_logprobs   rows x top
+
+    With a router's logits, ``top_ids`` are the experts and ``top_logprobs`` the
+    logarithms of their shares, for ``moe_layer``.  -infinity is a forbidden place;
+    NaN and +infinity make their row NaN.  Runs on ``stream`` (as in ``linear``) and
+    returns without synchronising."""
+    _torch()
+    t = layers.torch
+    dtype, rows, vocab, ld = _logits(logits)
+    device = logits.device
+    token_ptr = _vector(tokens, (rows,), t.int32, device, "tokens") if tokens is not None else None
+    params = _block(LogProbsParams, dtype, top, float(scale), 0, rows, vocab, ld)
+    lib = _library()
+    need = lib.gemm_log_probs_workspace_size(params)
+    if need < 0:
+        raise ValueError("top must be 0 .. 64 and at most the vocabulary, scale finite and positive; not %r and %r"
+                         % (top, scale))
+    at = _Launch(device, stream)
+    try:
+        logprob = at.empty((rows,), t.float32) if tokens is not None else None
+        entropy, stats = at.empty((rows,), t.float32), at.empty((rows, 2), t.float32)
+        ids = at.empty((rows, top), t.int32) if top else None
+        alternatives = at.empty((rows, top), t.float32) if top else None
+        ws, ws_ptr = at.scratch(need)
+        rc = lib.gemm_log_probs(params, logits.data_ptr(), token_ptr, logprob.data_ptr() if tokens is not None else None,
+                                entropy.data_ptr(), stats.data_ptr(), ids.data_ptr() if top else None,
+                                alternatives.data_ptr() if top else None, ws_ptr, need, at.stream)
+    finally:
+        at.done()
+    _status(rc)
+    return LogProbs(logprob, entropy, stats, ids, alternatives)
+
+
+def log_probs_grad(logits, tokens, stats, entropy=None, dlogprob=None, dentropy=None, *, scale=1.0, out=None,
+                   stream=None):
+    """The gradient of sum(dlogprob * logprob + dentropy * entropy) with respect to
+    the logits, in their type, from what ``log_probs`` returned for them (``stats``,
+    and ``entropy`` where ``dentropy`` is given).
+
+    ``dlogprob`` and ``dentropy`` are float32, one value per row; either may be
+    left out.  Rows of padding tokens get zeros for the former.  ``out`` may be
+    ``logits`` itself.  ``scale`` has to be the forward pass's."""
+    _torch()
+    t = layers.torch
+    dtype, rows, vocab, ld = _logits(logits)
+    device = logits.device
+    stats_ptr = _vector(stats, (rows, 2), t.float32, device, "stats")
+    token_ptr = _vector(tokens, (rows,), t.int32, device, "tokens") if tokens is not None else None
+    entropy_ptr = _vector(entropy, (rows,), t.float32, device, "entropy") if entropy is not None else None
+    dlogprob_ptr = _vector(dlogprob, (rows,), t.float32, device, "dlogprob") if dlogprob is not None else None
+    dentropy_ptr = _vector(dentropy, (rows,), t.float32, device, "dentropy") if dentropy is not None else None
+    if dlogprob is not None and tokens is None:
+        raise ValueError("dlogprob needs tokens")
+    if dentropy is not None and entropy is None:
+        raise ValueError("dentropy needs entropy")
+    params = _block(LogProbsParams, dtype, 0, float(scale), 0, rows, vocab, ld)
+    ldd = _matrix(out, rows, vocab, logits.dtype, device, "out") if out is not None else vocab
+    at = _Launch(device, stream)
+    try:
+        if out is None:
+            out = at.empty((rows, vocab), logits.dtype)
+        rc = _library().gemm_log_probs_grad(params, logits.data_ptr(), token_ptr, stats_ptr, entropy_ptr, dlogprob_ptr,
+                                            dentropy_ptr, out.data_ptr(), ldd, at.stream)
+    finally:
+        at.done()
+    _status(rc)
+    return out

@@ -1,0 +1,89 @@
+/*
+ * What stands around the products of a model that answers, on one MI355X
+ * (gfx950): log probabilities of given tokens with entropy and alternatives,
+ * and their gradient.
+ *
+ * Memory: every pointer is a device pointer of the caller's, aligned to its
+ * element; outputs must not overlap inputs or one another, except where an
+ * entry point says so.  The calls take their scratch memory from the caller
+ * (workspace, 16-byte aligned, at least the bytes that the *_workspace_size
+ * function of the same parameters returns; contents on entry do not matter);
+ * the library allocates nothing and keeps nothing, so the calls may be captured
+ * into HIP graphs, and calls with workspaces of their own may run at the same
+ * time.  Results are bitwise reproducible: no sum's order depends on timing.
+ *
+ * Streams, threads, errors: as in gemm.h.  Argument checks come before any HIP
+ * call: GEMM_ERR_INVALID_ARG for an unknown type or activation, negative sizes
+ * or sizes above 2^30, a leading dimension shorter than its row or above 2^40, a
+ * null or misaligned pointer of a non-empty operand, a workspace that is too
+ * small, and the limits named below.  Calls without rows launch nothing.
+ */
+#ifndef DENSE_GEMM_03_AMD_GEMM_SERVING_H
+#define DENSE_GEMM_03_AMD_GEMM_SERVING_H
+
+#include "gemm_linear.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* ------------------------------------------------------ log probabilities --
+ *
+ * For each row z of logits (`vocab` values), with m its largest value,
+ *
+ *     d_j = scale (z_j - m)      L = log sum_j exp(d_j)      p_j = exp(d_j - L)
+ *     logprob = d_token - L      entropy = L - sum_j p_j d_j
+ *
+ * and the `top` largest logits: their places, in falling order (equal logits:
+ * the lower place first), and their log probabilities.  The distances are formed
+ * before they are scaled, and m and L are kept apart, so that logits of any size
+ * lose nothing; sums are in fp32.
+ *
+ * A token outside 0 .. vocab-1 (padding) has logprob 0 and no gradient through it.
+ * -infinity is a forbidden place: p = 0, and it adds 0 to the entropy.  A row of
+ * nothing else has logprob and L = -infinity, entropy 0 and gradient 0.  The type's
+ * lowest value is a number like any other.  A row that holds NaN or +infinity has
+ * NaN for logprob (of a token), entropy, m, L and the log probabilities of its
+ * alternatives; NaN ranks with -infinity among the alternatives.
+ */
+typedef struct {
+    int32_t dtype;   /* of the logits: GEMM_DTYPE_F32 or GEMM_DTYPE_BF16 */
+    int32_t top;     /* alternatives: 0 .. 64, at most vocab */
+    float scale;     /* 1 / temperature: finite, > 0 */
+    int32_t reserved; /* 0 */
+    int64_t rows, vocab;   /* vocab >= 1 */
+    int64_t ld;      /* of the logits */
+} gemm_log_probs_params;
+
+int64_t gemm_log_probs_workspace_size(const gemm_log_probs_params *params);
+
+/*
+ * tokens: int32, one per row, or NULL with logprob NULL.  logprob, entropy: fp32,
+ * one per row; stats: fp32, rows x 2, m and L; top_ids (int32) and top_logprobs
+ * (fp32): rows x top.  Each output may be NULL and is then left out, but not
+ * logprob with tokens, nor top_ids with top > 0.
+ */
+int gemm_log_probs(const gemm_log_probs_params *params, const void *logits, const int32_t *tokens,
+                   float *logprob, float *entropy, float *stats, int32_t *top_ids, float *top_logprobs,
+                   void *workspace, int64_t workspace_bytes, hipStream_t stream);
+
+/*
+ * dlogits = the gradient of sum over rows of dlogprob * logprob + dentropy * entropy:
+ *
+ *     dz_j = scale (dlogprob (1[j = token] - p_j) - dentropy p_j (log p_j + entropy))
+ *
+ * rounded once to the logits' type.  stats and entropy are gemm_log_probs' outputs
+ * of the same logits and scale (top is not used).  dlogprob (with tokens) or
+ * dentropy (with entropy) may be NULL: taken as zero.  dlogits has leading dimension
+ * ldd and may be the logits themselves, with ldd == ld.  A row whose two factors
+ * are zero has gradient 0 whatever its logits hold.
+ */
+int gemm_log_probs_grad(const gemm_log_probs_params *params, const void *logits, const int32_t *tokens,
+                        const float *stats, const float *entropy, const float *dlogprob,
+                        const float *dentropy, void *dlogits, int64_t ldd, hipStream_t stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* DENSE_GEMM_03_AMD_GEMM_SERVING_H */

@@ -1,0 +1,100 @@
+"""The operators of gemm_serving.h from their definition in 64 bits, with bounds
+on how far a kernel that rounds where the documentation says may be from it.
+
+Log probabilities.  An exponent t = a (z - m) is formed with three roundings (a, the
+difference, the product) and exp2 is off by one unit, so a term of the sum is off by
+(3 |t| ln2 / 2 + 1) 2^-23 of itself; in the mean over the terms, weighted by p, that is
+(1.5 D + 1) 2^-23 with D = sum p |d|.  A lane sums n / 64 terms on four chains that are
+joined per 32, the lanes' sums and the moves to larger maxima (each of one unit and of
+its exponent's rounding; what a move shrinks below its own size no longer counts, so
+the exponents that count add up to few) take some tens of roundings more.  Twice the
+sum of these is allowed: sum_error(n, D).  L = ln s adds one unit of L, the distance
+d_token two roundings; the entropy weighs the terms' errors with |d|.
+"""
+from __future__ import annotations
+
+import math
+
+import torch
+
+from tests.linear_ref import half_step, worst  # noqa: F401
+
+U = 2.0 ** -23
+
+
+def sum_error(n, spread):
+    return 2 * U * (n / 256 + 40 + 2 * spread)
+
+
+def ranks(z, top):
+    """Places of the largest values of each row: falling, equal ones by place, NaN with -infinity."""
+    key = torch.where(torch.isnan(z), torch.full_like(z, -math.inf), z)
+    return torch.sort(-key, dim=1, stable=True)[1][:, :top]
+
+
+def log_probs(logits, tokens, top, scale):
+    """{name: (value, bound)} in float64 on the CPU; top_ids whole numbers."""
+    z = logits.cpu().double()
+    rows, n = z.shape
+    m = torch.where(torch.isnan(z), torch.full_like(z, -math.inf), z).max(dim=1, keepdim=True).values
+    empty = torch.isneginf(z).all(dim=1, keepdim=True)
+    bad = (torch.isnan(z) | torch.isposinf(z)).any(dim=1, keepdim=True)
+    base = torch.where(empty | bad, torch.zeros_like(m), m)
+    d = torch.where(bad, torch.zeros_like(z), scale * (z - base))
+    e = torch.exp(d)
+    s = e.sum(dim=1, keepdim=True)
+    L = torch.log(s)
+    p = torch.where(empty, torch.zeros_like(e), e / s)
+    pd = torch.where(p > 0, p * d, torch.zeros_like(p))
+    spread = pd.abs().sum(dim=1, keepdim=True)
+    H = torch.where(empty, torch.zeros_like(L), L - pd.sum(dim=1, keepdim=True))
+    rel = sum_error(n, spread)
+    Lerr = rel + U * L.abs().nan_to_num(0, 0, 0)
+    nan = torch.full_like(m, math.nan)
+    found = {"L": (torch.where(bad, nan, L), Lerr + 1e-37),
+             "entropy": (torch.where(bad, nan, H), Lerr + 2 * rel * (1 + spread) + 1e-37),
+             "m": (torch.where(bad, nan, m), torch.full_like(m, 1e-300))}
+
+    def at(place):
+        dist = torch.gather(d, 1, place)
+        value = torch.where(empty, torch.full_like(dist, -math.inf), dist - L)
+        return torch.where(bad, nan, value), Lerr + 2 * U * (dist.abs().nan_to_num(0, 0, 0) + L.abs().nan_to_num(0, 0, 0))
+
+    if tokens is not None:
+        t = tokens.cpu().long()[:, None]
+        held = (t >= 0) & (t < n)
+        value, bound = at(torch.where(held, t, torch.zeros_like(t)))
+        found["logprob"] = torch.where(held, value, torch.zeros_like(value)), bound + 1e-37
+    if top:
+        place = ranks(z, top)
+        found["top_ids"] = place
+        found["top_logprobs"] = at(place)
+    return found
+
+
+def log_probs_grad(logits, tokens, stats, entropy, dlogprob, dentropy, scale):
+    """(value, bound) of the gradient for the given stats and entropy."""
+    z, st = logits.cpu().double(), stats.cpu().double()
+    rows, n = z.shape
+    zero = torch.zeros(rows, 1, dtype=torch.float64)
+    m, L = st[:, :1], st[:, 1:]
+    H = entropy.cpu().double()[:, None] if entropy is not None else zero
+    t = tokens.cpu().long()[:, None] if tokens is not None else torch.full((rows, 1), -1)
+    held = (t >= 0) & (t < n)
+    g = torch.where(held, dlogprob.cpu().double()[:, None], zero) if dlogprob is not None else zero
+    h = dentropy.cpu().double()[:, None] if dentropy is not None else zero
+    none = ((g == 0) & (h == 0)) | torch.isneginf(m)
+    logp = scale * (z - m) - L
+    p = torch.exp(logp)
+    hit = torch.arange(n)[None, :] == torch.where(held, t, torch.full_like(t, -1))
+    info = torch.where(p > 0, p * (logp + H), torch.zeros_like(p))
+    dz = scale * (torch.where(hit, g, zero) - g * p - h * info)
+    dz = torch.where(none, torch.zeros_like(dz), dz)
+    # p: exponent a (z - m) - L log2(e), each part rounded, and exp2
+    size = (scale * (z - m)).abs() + L.abs()
+    size = torch.where(p > 0, size, torch.zeros_like(size))
+    err = scale * p * 4 * U * ((g.abs() + h.abs() * (size + H.abs())) * (2 + size) + h.abs() * (size + H.abs() + 1))
+    err = torch.where(none, torch.zeros_like(err), err)
+    err = err + torch.where(hit, 4 * U * scale * g.abs(), zero)
+    hs = half_step(logits.dtype)
+    return dz, err + hs * (dz.abs() + err) + 1e-37
