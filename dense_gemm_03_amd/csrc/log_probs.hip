@@ -1,7 +1,10 @@
 // Log probabilities of given tokens, entropy and alternatives, and their gradient.
 //
-//     t_j = a (z_j - m),  a = scale log2(e),  m = max z      s = sum 2^t_j      u = sum t_j 2^t_j
-//     L = ln s          entropy = ln s - ln2 u / s          logprob = scale (z_token - m) - ln s
+//     m = max z     c = fl(a m),  a = scale log2(e)     t_j = a z_j - c     s = sum 2^t_j     u = sum t_j 2^t_j
+//     L = ln s - ln2 (a m - c)     entropy = ln s - ln2 u / s     logprob = scale (z_token - m) - L
+//
+// t_j is one fused multiply-add; what c lacks of a m is the same for all terms and
+// known exactly (a m - c is another), so a large m costs no digits.
 //
 // One pass over the logits: each lane keeps (m, s, u) of what it has read and moves
 // them to a larger m when it finds one, 32 logits at a time.
@@ -20,13 +23,19 @@ constexpr int CHUNK = 64 * 32;   // logits per wave and step: 32 per lane
 // multiplied, so that a forbidden place (t = -infinity) adds 0 and not NaN.
 __device__ __forceinline__ float bounded(float t) { return fmaxf(t, -200.0f); }
 
+// Whether c = a m is out of fp32's range, or so near its end that some a z may be.
+// Distances are then formed before they are scaled, and c is a m itself.
+__device__ __forceinline__ bool huge(float m, float a) { return !(fabsf(a * m) < 1e38f); }
+
 struct Sums {
     float m = kLowest, s = 0.0f, u = 0.0f;   // m is a number even where nothing or -infinity was read
 
     // to the larger maximum `to`
     __device__ __forceinline__ void move(float to, float a)
     {
-        const float t = bounded(a * (m - to)), f = __builtin_amdgcn_exp2f(t);
+#pragma clang fp contract(off)   // a m and a to are the c's that the sums were formed with
+        const float t = bounded(huge(m, a) || huge(to, a) ? a * (m - to) : a * m - a * to);
+        const float f = __builtin_amdgcn_exp2f(t);
         u = __builtin_fmaf(s, t, u) * f;
         s *= f;
         m = to;
@@ -59,9 +68,11 @@ __device__ __forceinline__ float logit_at(const void *logits, int64_t at)
 template <bool BF16>
 __device__ __forceinline__ void finish_row(const LogProbsArgs &p, int64_t row, const Sums &x, uint64_t list, int lane)
 {
-    const bool empty = x.s == 0.0f;   // the largest logit adds 1, so: nothing but -infinity
+    const bool empty = x.s == 0.0f;   // the largest logit adds about 1, so: nothing but -infinity
     const float none = -__builtin_inff();
-    const float total = logf(x.s);    // -infinity of 0
+    const float log_s = logf(x.s);    // -infinity of 0
+    const float a = p.scale * kLog2e, c = a * x.m;
+    const float total = huge(x.m, a) ? log_s : __builtin_fmaf(-kLn2, __builtin_fmaf(a, x.m, -c), log_s);
     if (lane == 0) {
         if (p.tokens != nullptr) {
             const int t = p.tokens[row];
@@ -70,7 +81,7 @@ __device__ __forceinline__ void finish_row(const LogProbsArgs &p, int64_t row, c
                 lp = empty ? none : p.scale * (logit_at<BF16>(p.logits, row * p.ld + t) - x.m) - total;
             p.logprob[row] = lp;
         }
-        if (p.entropy != nullptr) p.entropy[row] = empty ? 0.0f : total - kLn2 * (x.u / x.s);
+        if (p.entropy != nullptr) p.entropy[row] = empty ? 0.0f : log_s - kLn2 * (x.u / x.s);
         if (p.stats != nullptr) {
             p.stats[2 * row] = empty ? none : x.s != x.s ? x.s : x.m;
             p.stats[2 * row + 1] = total;
@@ -119,6 +130,7 @@ __global__ void __launch_bounds__(256) log_probs_kernel(LogProbsArgs p)
     const float a = p.scale * kLog2e;
     __shared__ float team_sums[4][3];
     __shared__ uint64_t team_lists[4][64];
+    __shared__ __attribute__((aligned(16))) float spread[4][32];
 
     for (int64_t unit0 = (int64_t)blockIdx.x * (4 / p.team); unit0 < units; unit0 += (int64_t)gridDim.x * (4 / p.team)) {
         const int64_t unit = unit0 + (p.team == 1 ? wave : 0);
@@ -140,36 +152,42 @@ __global__ void __launch_bounds__(256) log_probs_kernel(LogProbsArgs p)
         if (c < end) cur.load(row16, c, vectors, lane);
         for (; c < end; c += p.team) {
             if (c + p.team < end) nxt.load(row16, c + p.team, vectors, lane);
-            // place of this lane's first value; value j lies VEC * 64 further per vector
-            const int64_t first = ((int64_t)c * C::U * 64 + lane) * C::VEC - head;
-            auto place = [&](int j) { return first + j / C::VEC * (64 * C::VEC) + j % C::VEC; };
-            const bool whole = (int64_t)c * CHUNK - head >= 0 && (int64_t)(c + 1) * CHUNK - head <= p.vocab;
+            // place of this lane's first value; value j lies 64 VEC further per vector
+            const int first = (c * C::U * 64 + lane) * C::VEC - head;
+            auto place = [](int first, int j) { return first + j / C::VEC * (64 * C::VEC) + j % C::VEC; };
+            const bool whole = c * CHUNK >= head && (c + 1) * CHUNK - head <= p.vocab;
             float z[32];
 #pragma unroll
             for (int j = 0; j < 32; ++j) z[j] = cur[j];
             if (!whole) {
 #pragma unroll
                 for (int j = 0; j < 32; ++j)
-                    if (place(j) < 0 || place(j) >= p.vocab) z[j] = -__builtin_inff();
+                    if ((unsigned)place(first, j) >= (unsigned)p.vocab) z[j] = -__builtin_inff();
             }
             float largest = z[0];
 #pragma unroll
             for (int j = 1; j < 32; ++j) largest = fmaxf(largest, z[j]);
             // Later chunks have higher places, so a value has to exceed the last one's.
             if (TOP && __ballot(!(largest <= bar)) != 0) {
-                top.template absorb<32>([&](int j) -> uint64_t {
-                    const int64_t at = place(j);
-                    return at >= 0 && at < p.vocab ? key_of(z[j], (int)at) : 0;
-                });
+                top.template absorb_values<32>(z, largest, p.vocab, first, place, spread[wave]);
                 if (top.least != 0) bar = value_of((uint32_t)(top.least >> 32));
             }
             x.move(fmaxf(x.m, largest), a);
             float s[4] = {0, 0, 0, 0}, u[4] = {0, 0, 0, 0};
+            auto terms = [&](auto exponent) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-                const float t = a * (z[j] - x.m), e = __builtin_amdgcn_exp2f(t);
-                s[j & 3] += e;
-                u[j & 3] = __builtin_fmaf(e, bounded(t), u[j & 3]);
+                for (int j = 0; j < 32; ++j) {
+                    const float t = exponent(z[j]), e = __builtin_amdgcn_exp2f(t);
+                    s[j & 3] += e;
+                    u[j & 3] = __builtin_fmaf(e, bounded(t), u[j & 3]);
+                }
+            };
+            const float c_m = a * x.m;
+            if (__ballot(huge(x.m, a)) == 0) {
+                terms([&](float v) { return __builtin_fmaf(a, v, -c_m); });
+            } else {
+                const float rest = huge(x.m, a) ? 0.0f : __builtin_fmaf(a, x.m, -c_m);
+                terms([&](float v) { return a * (v - x.m) + rest; });
             }
             x.s += (s[0] + s[1]) + (s[2] + s[3]);
             x.u += (u[0] + u[1]) + (u[2] + u[3]);
@@ -185,12 +203,15 @@ __global__ void __launch_bounds__(256) log_probs_kernel(LogProbsArgs p)
             }
             if (TOP) team_lists[wave][lane] = list;
             __syncthreads();
+            if (TOP && wave < 2) {
+                list = merged(list, team_lists[wave + 2][lane]);
+                if (wave == 1) team_lists[1][lane] = list;
+            }
+            __syncthreads();
             if (wave == 0) {
 #pragma unroll
-                for (int w = 1; w < 4; ++w) {
-                    x.add(Sums{team_sums[w][0], team_sums[w][1], team_sums[w][2]}, a);
-                    if (TOP) list = merged(list, team_lists[w][lane], lane);
-                }
+                for (int w = 1; w < 4; ++w) x.add(Sums{team_sums[w][0], team_sums[w][1], team_sums[w][2]}, a);
+                if (TOP) list = merged(list, team_lists[1][lane]);
             }
             __syncthreads();
             if (wave != 0) continue;
@@ -204,32 +225,44 @@ __global__ void __launch_bounds__(256) log_probs_kernel(LogProbsArgs p)
     }
 }
 
-// The parts of a row, by one wave per row.
+// The parts of a row: four waves take every fourth list each and merge them (they
+// are sorted), then their own.
 template <bool BF16>
-__global__ void __launch_bounds__(64) log_probs_join_kernel(LogProbsArgs p)
+__global__ void __launch_bounds__(256) log_probs_join_kernel(LogProbsArgs p)
 {
-    const int lane = (int)threadIdx.x;
+    const int lane = (int)threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const float a = p.scale * kLog2e;
+    __shared__ uint64_t lists[4][64];
     for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
-        Sums x;
-        for (int i = lane; i < p.parts; i += 64) {
-            const floatx4 v = *reinterpret_cast<const floatx4 *>(p.ws + 4 * (row * p.parts + i));
-            x.add(Sums{v[0], v[1], v[2]}, a);
-        }
-        x.add_lanes(a);
-        TopList top(lane, p.top);
-        const int count = p.parts * p.top;
-        const uint64_t *keys = p.ws_keys + row * count;
-        for (int at = 0; at < count; at += 64 * 16) {
-            uint64_t k[16];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                const int i = at + 64 * j + lane;
-                k[j] = i < count ? keys[i] : 0;
+        const uint64_t *keys = p.ws_keys + row * p.parts * p.top;
+        uint64_t list = 0;
+        if (p.top > 0) {
+            auto part = [&](int i) { return i < p.parts && lane < p.top ? keys[i * p.top + lane] : 0; };
+            list = part(wave);
+            uint64_t next = part(wave + 4);
+            for (int i = wave + 4; i < p.parts; i += 4) {
+                const uint64_t k = next;
+                next = part(i + 4);
+                list = merged(list, k);
             }
-            top.template absorb<16>([&](int j) { return k[j]; });
+            lists[wave][lane] = list;
         }
-        finish_row<BF16>(p, row, x, top.list, lane);
+        Sums x;
+        if (wave == 0) {
+            for (int i = lane; i < p.parts; i += 64) {
+                const floatx4 v = *reinterpret_cast<const floatx4 *>(p.ws + 4 * (row * p.parts + i));
+                x.add(Sums{v[0], v[1], v[2]}, a);
+            }
+            x.add_lanes(a);
+        }
+        __syncthreads();
+        if (wave == 0) {
+            if (p.top > 0)
+#pragma nounroll
+                for (int w = 1; w < 4; ++w) list = merged(list, lists[w][lane]);
+            finish_row<BF16>(p, row, x, list, lane);
+        }
+        __syncthreads();
     }
 }
 
@@ -333,7 +366,7 @@ hipError_t launch_log_probs(const LogProbsArgs &a, bool bf16, hipStream_t stream
     hipError_t err = hipGetLastError();
     if (err != hipSuccess || a.parts == 1) return err;
     auto join = bf16 ? log_probs_join_kernel<true> : log_probs_join_kernel<false>;
-    hipLaunchKernelGGL(join, dim3(grid_of(a.rows)), dim3(64), 0, stream, a);
+    hipLaunchKernelGGL(join, dim3(grid_of(a.rows)), dim3(256), 0, stream, a);
     return hipGetLastError();
 }
 

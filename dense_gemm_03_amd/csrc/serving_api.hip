@@ -52,7 +52,7 @@ Shares shares_of(const gemm_log_probs_params &p)
 {
     const int64_t vec = 16 / size_of(p.dtype);
     const int64_t chunks = ceil_div(p.vocab + vec - 1, log_probs_chunk());   // one more where a row starts off a boundary
-    const int64_t waves = 16 * (int64_t)device_compute_units();
+    const int64_t waves = 8 * (int64_t)device_compute_units();
     Shares s{1, 1, (int)chunks};
     if (p.rows >= waves || chunks == 1) return s;
     s.team = 4;

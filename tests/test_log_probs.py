@@ -267,6 +267,21 @@ def test_nan_and_infinity(cuda, dtype, vocab):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("vocab", [70, 3000, 20000])
+def test_nan_among_the_alternatives(cuda, vocab):
+    """NaN ranks with -infinity, by place, wherever the list has to take either."""
+    gen = torch.Generator().manual_seed(7)
+    kind = torch.randint(0, 2, (8, vocab), generator=gen)
+    z = torch.where(kind == 0, torch.tensor(-INF), torch.tensor(math.nan))
+    z[1:4, ::vocab // 9] = 1.0
+    z[4, -5:] = 2.0
+    for dtype in DTYPES.values():
+        for top in (3, 20, 64):
+            got = dg.log_probs(z.to(dtype).cuda(), None, top)
+            assert torch.equal(got.top_ids.cpu().long(), ref.ranks(z.double(), top))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("rows", [1, 4100])
 def test_ties_and_orders(cuda, dtype, rows):
