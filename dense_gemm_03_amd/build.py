@@ -32,7 +32,8 @@ SOURCES = [("gemm_api.hip", "gemm_api", []),
            ("linear_aux.hip", "linear_aux", []),
            ("linear_rows.hip", "linear_rows", []),
            ("serving_api.hip", "serving_api", []),
-           ("log_probs.hip", "log_probs", [])]
+           ("log_probs.hip", "log_probs", []),
+           ("moe.hip", "moe", [])]
 for _dtype in ("F32", "BF16"):
     for _layout in ("NN", "NT", "TN", "TT", "CF", "CW", "CFT", "CWT", "C3F", "C3W", "CFP", "CWP",
                     "C3FP", "C3WP", "CFW", "CWW", "C4F", "C4W", "C4FP", "C4WP"):

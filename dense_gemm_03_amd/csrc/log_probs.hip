@@ -8,7 +8,6 @@
 //
 // One pass over the logits: each lane keeps (m, s, u) of what it has read and moves
 // them to a larger m when it finds one, 32 logits at a time.
-#include "mma16.hpp"
 #include "serving.hpp"
 #include "topk.hpp"
 

@@ -4,6 +4,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "linear_kernel.hpp"
+
 namespace dg {
 
 struct LogProbsArgs {
@@ -36,5 +38,31 @@ struct LogProbsGradArgs {
     float scale;
 };
 hipError_t launch_log_probs_grad(const LogProbsGradArgs &args, bool bf16, hipStream_t stream);
+
+constexpr int MOE_MAX_TOP = 32;
+constexpr int MOE_MAX_EXPERTS = 1024;
+
+struct MoeArgs {
+    const void *x, *up, *down;
+    const int32_t *ids;
+    const float *weights;
+    void *h;                     // the first product's results: a row of ldh per place (token, j)
+    int64_t h_plane;             // elements from h's upper halves to its lower ones (bf16)
+    float *ws;                   // y of `parts` > 1 parts
+    EpilogueArgs e;
+    int64_t ldx, ldup, lddown, ldh, stride_up, stride_down;
+    int tokens, hidden, inner, experts, top, act, gated;
+    int strips_up, strips_down;
+    int max_used;                // experts that a chunk of tokens can name
+    int parts;                   // of the second product's sum
+};
+struct MoePlan {
+    int rows;                    // tokens of a chunk: 16, 32 or 64
+    int64_t blocks_up, blocks_down;
+};
+// Columns of a block of either kernel.
+int moe_strip_up(bool transw, bool gated);
+int moe_strip_down(bool transw, int rows);
+hipError_t launch_moe(const MoeArgs &args, const MoePlan &plan, bool bf16, bool transw, hipStream_t stream);
 
 }  // namespace dg

@@ -126,10 +126,134 @@ int log_probs_grad(const gemm_log_probs_params *p, const void *logits, const int
     return launch_log_probs_grad(a, p->dtype == GEMM_DTYPE_BF16, stream) == hipSuccess ? GEMM_OK : GEMM_ERR_HIP;
 }
 
+// ---------------------------------------------------- mixture of experts --
+
+constexpr int64_t kMaxWidth = int64_t(1) << 24;
+constexpr int64_t kMaxTokens = 512;
+
+int64_t up_columns(const gemm_moe_params &p) { return p.gated ? 2 * p.inner : p.inner; }
+
+bool valid(const gemm_moe_params *p)
+{
+    if (p == nullptr || !known(p->dtype) || !known(p->dtype_y) ||
+        (p->transw != GEMM_OP_N && p->transw != GEMM_OP_T) || p->act < GEMM_ACT_NONE || p->act > GEMM_ACT_SILU ||
+        (p->gated != 0 && p->gated != 1))
+        return false;
+    if (p->tokens < 0 || p->tokens > kMaxTokens || p->hidden < 0 || p->hidden > kMaxWidth || p->inner < 0 ||
+        p->inner > kMaxWidth || p->experts < 0 || p->experts > MOE_MAX_EXPERTS || p->top < 0 || p->top > MOE_MAX_TOP)
+        return false;
+    const bool t = p->transw == GEMM_OP_T;
+    const int64_t n = up_columns(*p), up_row = t ? p->hidden : n, up_rows = t ? n : p->hidden;
+    const int64_t down_row = t ? p->inner : p->hidden, down_rows = t ? p->hidden : p->inner;
+    if (!valid_ld(p->ldx, p->hidden) || !valid_ld(p->ldy, p->hidden) || !valid_ld(p->ldup, up_row) ||
+        !valid_ld(p->lddown, down_row))
+        return false;
+    // the experts' weights do not overlap
+    return p->experts <= 1 || up_rows * up_row == 0 || down_rows * down_row == 0 ||
+           (p->stride_up >= (up_rows - 1) * p->ldup + up_row && p->stride_down >= (down_rows - 1) * p->lddown + down_row);
+}
+
+struct MoeShares {
+    MoePlan plan;
+    int strips_up, strips_down, max_used, parts;
+    int64_t ldh, h_bytes, total;
+    bool launchable;
+};
+
+MoeShares shares_of(const gemm_moe_params &p)
+{
+    MoeShares s{};
+    s.plan.rows = p.tokens <= 16 ? 16 : p.tokens <= 32 ? 32 : 64;
+    const int64_t chunks = ceil_div(p.tokens, s.plan.rows);
+    s.max_used = (int)std::min(p.experts, std::min<int64_t>(p.tokens, s.plan.rows) * p.top);
+    s.strips_up = (int)ceil_div(p.inner, moe_strip_up(p.transw == GEMM_OP_T, p.gated != 0));
+    s.strips_down = (int)ceil_div(p.hidden, moe_strip_down(p.transw == GEMM_OP_T, s.plan.rows));
+    s.plan.blocks_up = chunks * s.max_used * s.strips_up;
+    const int64_t blocks = chunks * s.strips_down;
+    // parts until there is a block for each compute unit, of at least one expert each
+    s.parts = (int)std::max<int64_t>(1, std::min<int64_t>(device_compute_units() / std::max<int64_t>(1, blocks),
+                                                          std::min<int64_t>(s.max_used, 8)));
+    s.plan.blocks_down = blocks * s.parts;
+    const int64_t vec = 16 / size_of(p.dtype);
+    s.ldh = ceil_div(p.inner, vec) * vec;
+    const int64_t planes = p.dtype == GEMM_DTYPE_BF16 ? 2 : 1;
+    s.h_bytes = planes * p.tokens * p.top * s.ldh * size_of(p.dtype);   // whole 16 bytes
+    s.total = s.h_bytes + (s.parts > 1 ? s.parts * p.tokens * p.hidden * 4 : 0);
+    const int64_t most = int64_t(UINT32_MAX) / 512;   // blocks of a launch
+    s.launchable = s.plan.blocks_up <= most && s.plan.blocks_down <= most;
+    return s;
+}
+
+int moe_layer(const gemm_moe_params *p, const void *x, const void *up, const void *down, const int32_t *ids,
+              const float *weights, const void *residual, void *y, void *workspace, int64_t workspace_bytes,
+              hipStream_t stream)
+{
+    if (!valid(p) || (residual && !valid_ld(p->ldr, p->hidden))) return GEMM_ERR_INVALID_ARG;
+    const bool empty = p->tokens == 0 || p->hidden == 0, places = p->top > 0 && p->experts > 0;
+    if (!empty && (!y || (places && (!x || !ids || !weights || (p->inner > 0 && (!up || !down))))))
+        return GEMM_ERR_INVALID_ARG;
+    const int es = size_of(p->dtype);
+    if (misaligned(x, es) || misaligned(up, es) || misaligned(down, es) || misaligned(ids, 4) ||
+        misaligned(weights, 4) || misaligned(residual, size_of(p->dtype_y)) || misaligned(y, size_of(p->dtype_y)))
+        return GEMM_ERR_INVALID_ARG;
+    // in place: row r of y lies over row r of the residual and no other
+    if (residual && residual == y && p->tokens > 1 && p->ldr != p->ldy) return GEMM_ERR_INVALID_ARG;
+    const MoeShares s = shares_of(*p);
+    if (!s.launchable || !valid_workspace(workspace, workspace_bytes, empty ? 0 : s.total)) return GEMM_ERR_INVALID_ARG;
+    if (empty) return GEMM_OK;
+    if (const int rc = need_device()) return rc;
+    MoeArgs a{};
+    a.x = x;
+    a.up = up;
+    a.down = down;
+    a.ids = ids;
+    a.weights = weights;
+    a.h = workspace;
+    a.h_plane = p->tokens * p->top * s.ldh;
+    if (s.parts > 1) a.ws = reinterpret_cast<float *>(static_cast<char *>(workspace) + s.h_bytes);
+    a.e = EpilogueArgs{y, nullptr, residual, nullptr, p->ldy, p->ldr, 0, 1.0f, 1.0f, GEMM_ACT_NONE,
+                       p->dtype_y == GEMM_DTYPE_BF16, 0, 0};
+    a.ldx = p->ldx;
+    a.ldup = p->ldup;
+    a.lddown = p->lddown;
+    a.ldh = s.ldh;
+    a.stride_up = p->experts > 1 ? p->stride_up : 0;
+    a.stride_down = p->experts > 1 ? p->stride_down : 0;
+    a.tokens = (int)p->tokens;
+    a.hidden = (int)p->hidden;
+    a.inner = (int)p->inner;
+    a.experts = (int)p->experts;
+    a.top = places ? (int)p->top : 0;
+    a.act = p->act;
+    a.gated = p->gated;
+    a.strips_up = s.strips_up;
+    a.strips_down = s.strips_down;
+    a.max_used = s.max_used;
+    a.parts = s.parts;
+    return launch_moe(a, s.plan, p->dtype == GEMM_DTYPE_BF16, p->transw == GEMM_OP_T, stream) == hipSuccess
+               ? GEMM_OK
+               : GEMM_ERR_HIP;
+}
+
 }  // namespace
 }  // namespace dg
 
 extern "C" {
+
+int64_t gemm_moe_layer_workspace_size(const gemm_moe_params *p)
+{
+    if (!dg::valid(p)) return GEMM_ERR_INVALID_ARG;
+    const dg::MoeShares s = dg::shares_of(*p);
+    if (!s.launchable) return GEMM_ERR_INVALID_ARG;
+    return p->tokens == 0 || p->hidden == 0 ? 0 : s.total;
+}
+
+int gemm_moe_layer(const gemm_moe_params *p, const void *x, const void *w_up, const void *w_down, const int32_t *ids,
+                   const float *weights, const void *residual, void *y, void *workspace, int64_t workspace_bytes,
+                   hipStream_t stream)
+{
+    return dg::moe_layer(p, x, w_up, w_down, ids, weights, residual, y, workspace, workspace_bytes, stream);
+}
 
 int64_t gemm_log_probs_workspace_size(const gemm_log_probs_params *p)
 {

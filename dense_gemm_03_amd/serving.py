@@ -1,6 +1,7 @@
 """What stands around a model's products when it answers, over torch tensors:
-``log_probs`` (log probabilities of given tokens, entropy, alternatives) and its
-gradient ``log_probs_grad``; a thin binding over ``include/gemm_serving.h``.  Like
+``moe_layer`` (a whole mixture-of-experts layer for a few tokens), ``log_probs`` (log
+probabilities of given tokens, entropy, alternatives) and its gradient
+``log_probs_grad``; a thin binding over ``include/gemm_serving.h``.  Like
 the rest of the package they take no part in torch's autograd.  The C entry points
 are here under their own names (``gemm_*``), taking parameters, device pointers and
 a stream."""
@@ -10,7 +11,7 @@ import collections
 import ctypes
 
 from . import layers
-from .layers import _code, _i64, _int, _Launch, _library, _matrix, _p, _pitch, _status, _f, _torch
+from .layers import _activation, _code, _i64, _int, _Launch, _library, _matrix, _p, _pitch, _status, _torch, _weights
 
 
 class LogProbsParams(ctypes.Structure):
@@ -20,9 +21,20 @@ class LogProbsParams(ctypes.Structure):
                 ("ld", ctypes.c_int64)]
 
 
+class MoeParams(ctypes.Structure):
+    """gemm_moe_params of include/gemm_serving.h."""
+    _fields_ = [(name, ctypes.c_int32) for name in ("dtype", "dtype_y", "transw", "act", "gated", "reserved")] + \
+        [(name, ctypes.c_int64) for name in (
+            "tokens", "hidden", "inner", "experts", "top", "ldx", "ldy", "ldr", "ldup", "lddown", "stride_up",
+            "stride_down")]
+
+
 _plp = ctypes.POINTER(LogProbsParams)
+_pmoe = ctypes.POINTER(MoeParams)
 # Every symbol include/gemm_serving.h declares, with its ctypes signature.
 SIGNATURES = {
+    "gemm_moe_layer_workspace_size": (_i64, [_pmoe]),
+    "gemm_moe_layer": (_int, [_pmoe] + [_p] * 8 + [_i64, _p]),
     "gemm_log_probs_workspace_size": (_i64, [_plp]),
     "gemm_log_probs": (_int, [_plp] + [_p] * 8 + [_i64, _p]),
     "gemm_log_probs_grad": (_int, [_plp] + [_p] * 7 + [_i64, _p]),
@@ -30,6 +42,15 @@ SIGNATURES = {
 
 
 # ---------------------------------------------------------------- C names --
+
+def gemm_moe_layer_workspace_size(params) -> int:
+    return _library().gemm_moe_layer_workspace_size(params)
+
+
+def gemm_moe_layer(params, x, w_up, w_down, ids, weights, residual, y, workspace, workspace_bytes, stream=None) -> int:
+    return _library().gemm_moe_layer(params, x, w_up, w_down, ids, weights, residual, y, workspace, workspace_bytes,
+                                     stream)
+
 
 def gemm_log_probs_workspace_size(params) -> int:
     return _library().gemm_log_probs_workspace_size(params)
@@ -71,6 +92,67 @@ def _block(kind, *values):
             _blocks.clear()
         found = _blocks[kind, values] = kind(*values)
     return found
+
+
+def moe_layer(x, w_up, w_down, ids, weights, act="silu", residual=None, *, gated=True, transb=False, out=None,
+              out_dtype=None, stream=None):
+    """A whole mixture-of-experts layer for a few tokens (at most 512):
+
+        h[t, j] = act(x_t . gate) * (x_t . up)   of expert ids[t, j]; act(x_t . up) without a gate
+        y_t = sum_j weights[t, j] h[t, j] . down + residual_t
+
+    x is tokens x hidden, ``ids`` (int32) and ``weights`` (float32) are contiguous,
+    tokens x top, on the GPU and read there only.  ``w_up`` is experts x hidden x 2
+    inner (the gate's columns first; inner without ``gated``), ``w_down`` experts x
+    inner x hidden; with ``transb`` both are stored transposed.  x and the weights are
+    all float32 or all bfloat16, with contiguous rows.  An id outside the experts counts
+    for nothing.  y is ``out_dtype`` (default float32), created when ``out`` is not
+    given; ``residual`` (y's type) may be ``out`` itself.  The router's part is
+    ``log_probs``: its ``top_ids``, and the softmax of its ``top_logprobs``.  For long
+    batches sort the rows by expert and use ``grouped_linear``, which reads the weights
+    once for any number of rows.  ``stream`` as in ``linear``."""
+    _torch()
+    t = layers.torch
+    if x.dim() != 2 or w_up.dim() != 3 or w_down.dim() != 3 or ids.dim() != 2:
+        raise ValueError("x and ids must be 2-D, w_up and w_down 3-D (experts first)")
+    device = x.device
+    if device.type != "cuda":
+        raise ValueError("x must be a GPU tensor")
+    if w_up.device != device or w_down.device != device:
+        raise ValueError("x, w_up and w_down must be on the same GPU")
+    if w_up.dtype != x.dtype or w_down.dtype != x.dtype:
+        raise TypeError("x, w_up and w_down must all be float32 or all bfloat16")
+    dtype, act = _code(x.dtype, "x"), _activation(act)
+    tokens, hidden = x.shape
+    experts, top = w_up.shape[0], ids.shape[1]
+    hidden2, columns, ldup, stride_up = _weights(w_up, experts, transb)
+    inner, hidden3, lddown, stride_down = _weights(w_down, experts, transb)
+    if hidden2 != hidden or hidden3 != hidden or w_down.shape[0] != experts or columns != (2 * inner if gated else inner):
+        raise ValueError("sizes differ: x is %dx%d, w_up %s, w_down %s" % (tokens, hidden, tuple(w_up.shape),
+                                                                         tuple(w_down.shape)))
+    ids_ptr = _vector(ids, (tokens, top), t.int32, device, "ids")
+    weights_ptr = _vector(weights, (tokens, top), t.float32, device, "weights")
+    if out_dtype is None:
+        out_dtype = out.dtype if out is not None else t.float32
+    dtype_y = _code(out_dtype, "y")
+    ldr = _matrix(residual, tokens, hidden, out_dtype, device, "residual") if residual is not None else 0
+    ldy = _matrix(out, tokens, hidden, out_dtype, device, "out") if out is not None else max(hidden, 1)
+    params = _block(MoeParams, dtype, dtype_y, 1 if transb else 0, act, 1 if gated else 0, 0, tokens, hidden, inner,
+                    experts, top, _pitch(x, tokens, hidden, "x"), ldy, ldr, ldup, lddown, stride_up, stride_down)
+    at = _Launch(device, stream)
+    try:
+        lib = _library()
+        need = lib.gemm_moe_layer_workspace_size(params)
+        ws, ws_ptr = at.scratch(need)
+        if out is None:
+            out = at.empty((tokens, hidden), out_dtype)
+        rc = lib.gemm_moe_layer(params, x.data_ptr(), w_up.data_ptr(), w_down.data_ptr(), ids_ptr, weights_ptr,
+                                residual.data_ptr() if residual is not None else None, out.data_ptr(), ws_ptr, need,
+                                at.stream)
+    finally:
+        at.done()
+    _status(rc)
+    return out
 
 
 def _logits(logits):

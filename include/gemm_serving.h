@@ -1,7 +1,7 @@
 /*
  * What stands around the products of a model that answers, on one MI355X
- * (gfx950): log probabilities of given tokens with entropy and alternatives,
- * and their gradient.
+ * (gfx950): a whole mixture-of-experts layer for a few tokens; log probabilities
+ * of given tokens with entropy and alternatives, and their gradient.
  *
  * Memory: every pointer is a device pointer of the caller's, aligned to its
  * element; outputs must not overlap inputs or one another, except where an
@@ -26,6 +26,52 @@
 #ifdef __cplusplus
 extern "C" {
 #endif
+
+/* ----------------------------------------------------- mixture of experts --
+ *
+ * A whole layer for a few tokens, each of which goes to `top` of the experts:
+ *
+ *     h[t, j] = act(x_t . gate_e) * (x_t . up_e)      e = ids[t, j]    (gated)
+ *     h[t, j] = act(x_t . up_e)                                        (not gated)
+ *     y_t = sum_j weights[t, j] h[t, j] . down_e + residual_t
+ *
+ * w_up holds, per expert (stride_up elements apart), hidden x inner values, or
+ * with a gate hidden x 2 inner: the gate's columns first.  w_down holds inner x
+ * hidden per expert.  transw == GEMM_OP_T: both are stored transposed (2 inner x
+ * hidden and hidden x inner).  ids (int32) and weights (fp32) are tokens x top,
+ * contiguous, on the device and read by the kernels alone.  An id outside 0 ..
+ * experts-1 counts for nothing (its weight is not read): padding, or an expert that lives
+ * elsewhere; a token without experts gets its residual, or zeros.  Only the
+ * weights of experts that a token names are read.
+ *
+ * Both products are formed as in gemm_linear; h is kept to 16 bits of mantissa
+ * (bf16 operands) or as it is (fp32) between them, sums over experts are in fp32,
+ * and y is rounded once, to dtype_y.  An expert that a token names twice counts
+ * with the sum of the two weights.
+ *
+ * For a few tokens: at most 512, 32 experts each out of at most 1024, hidden and
+ * inner at most 2^24.  The weights are read once per 64 tokens: for long batches
+ * sort the rows by expert and use gemm_linear.
+ */
+typedef struct {
+    int32_t dtype;       /* of x, w_up and w_down: GEMM_DTYPE_F32 or GEMM_DTYPE_BF16 */
+    int32_t dtype_y;     /* of y and residual */
+    int32_t transw;      /* GEMM_OP_N or GEMM_OP_T */
+    int32_t act;         /* gemm_act */
+    int32_t gated;       /* 0 or 1 */
+    int32_t reserved;    /* 0 */
+    int64_t tokens, hidden, inner, experts, top;
+    int64_t ldx, ldy, ldr;                 /* x, y, residual */
+    int64_t ldup, lddown;                  /* w_up, w_down */
+    int64_t stride_up, stride_down;        /* elements between consecutive experts */
+} gemm_moe_params;
+
+int64_t gemm_moe_layer_workspace_size(const gemm_moe_params *params);
+
+/* residual may be NULL, or y itself with ldr == ldy. */
+int gemm_moe_layer(const gemm_moe_params *params, const void *x, const void *w_up, const void *w_down,
+                   const int32_t *ids, const float *weights, const void *residual, void *y,
+                   void *workspace, int64_t workspace_bytes, hipStream_t stream);
 
 /* ------------------------------------------------------ log probabilities --
  *

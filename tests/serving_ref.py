@@ -10,6 +10,14 @@ its exponent's rounding; what a move shrinks below its own size no longer counts
 the exponents that count add up to few) take some tens of roundings more.  Twice the
 sum of these is allowed: sum_error(n, D).  L = ln s adds one unit of L, the distance
 d_token two roundings; the entropy weighs the terms' errors with |d|.
+
+Mixture of experts.  The first product's sums are off by sum_bound(K) S as in
+linear_ref, the activation by act_bound and 1.13 of its argument's error, the product
+with the gate by both factors' errors.  h is stored as two bf16 values, which keep 2^-16
+of it (each conversion is off by half a step, 2^-8 and then 2^-8 of the rest), or in
+fp32; the smallest numbers of bf16's lower half are 2^-133.  The second product adds
+sum_bound of its magnitudes, the weighting and the sums over experts and waves some
+roundings of the terms' magnitudes (16 are allowed for).
 """
 from __future__ import annotations
 
@@ -17,7 +25,7 @@ import math
 
 import torch
 
-from tests.linear_ref import half_step, worst  # noqa: F401
+from tests.linear_ref import act64, act_bound, half_step, slope64, sum_bound, worst  # noqa: F401
 
 U = 2.0 ** -23
 
@@ -98,3 +106,43 @@ def log_probs_grad(logits, tokens, stats, entropy, dlogprob, dentropy, scale):
     err = err + torch.where(hit, 4 * U * scale * g.abs(), zero)
     hs = half_step(logits.dtype)
     return dz, err + hs * (dz.abs() + err) + 1e-37
+
+
+def moe_layer(x, up, down, ids, weights, act, residual, gated, transb, out_dtype):
+    """(value, bound), float64 on the CPU."""
+    x64 = x.cpu().double()
+    ids, weights = ids.cpu().long(), weights.cpu().double()
+    y = torch.zeros_like(x64)
+    err, mag = torch.zeros_like(x64), torch.zeros_like(x64)
+    keep = 2.0 ** -16 if x.dtype == torch.bfloat16 else 0.0
+    for e in range(up.shape[0]):
+        t, j = torch.nonzero(ids == e, as_tuple=True)
+        if t.numel() == 0:
+            continue
+        u, d = up[e].cpu().double(), down[e].cpu().double()
+        if transb:
+            u, d = u.T, d.T
+        z, s = x64[t] @ u, x64[t].abs() @ u.abs()
+        zerr = sum_bound(x.shape[1]) * s
+        if gated:
+            n = z.shape[1] // 2
+            a = act64(z[:, :n], act)
+            aerr = 1.13 * zerr[:, :n] + (act_bound(z[:, :n]) if act not in ("none", "relu") else 0)
+            h = a * z[:, n:]
+            herr = aerr * (z[:, n:].abs() + zerr[:, n:]) + a.abs() * zerr[:, n:] + U * h.abs()
+        else:
+            h = act64(z, act)
+            herr = 1.13 * zerr + (act_bound(z) if act not in ("none", "relu") else 0)
+        herr = herr + keep * (h.abs() + herr) + 2.0 ** -130
+        m = (h.abs() + herr) @ d.abs()
+        w = weights[t, j][:, None]
+        y.index_add_(0, t, w * (h @ d))
+        err.index_add_(0, t, w.abs() * (herr @ d.abs() + sum_bound(d.shape[0]) * m))
+        mag.index_add_(0, t, w.abs() * m)
+    err = err + 16 * U * mag
+    if residual is not None:
+        r = residual.cpu().double()
+        y = y + r
+        err = err + U * (y.abs() + r.abs())
+    hs = half_step(out_dtype)
+    return y, err + hs * (y.abs() + err) + 1e-37
