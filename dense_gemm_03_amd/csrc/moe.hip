@@ -10,15 +10,17 @@
 // for itself which experts have tokens, and which, from the ids: no launch sorts
 // them, and no weights are read for an expert without tokens.
 //
-// Tokens are taken in chunks of 16, 32 or 64, rows of 16 x 16 MFMAs.  A token that
-// names an expert twice is one row with both its weights.
+// Up to 16 tokens, an expert's tokens are one tile of rows of 16 x 16 MFMAs, and a
+// block of the second product goes through all experts for a strip of y, which it
+// finishes.  Beyond, blocks of both products take one expert each, up to 64 rows at a
+// time (its weights are read once per 64 tokens that name it), and a third kernel adds
+// up the experts' rows of a token.  A token that names an expert twice is one row with
+// both its weights.
 #include "linear_kernel.hpp"
 #include "serving.hpp"
 
 namespace dg {
 namespace {
-
-constexpr int WV = 8;   // waves of a block
 
 // A strip of output columns over k: P panels (gate and the other) of 16 W columns
 // each, RT tiles of 16 rows of x, U steps per pass.  Lane (q, c) = (lane / 16, lane %
@@ -30,7 +32,7 @@ constexpr int WV = 8;   // waves of a block
 // alignment, whatever the pitch.
 template <bool BF16, bool T, int W, int P, int XP, int RT, int U>
 struct Strip {
-    using F = FewRows<BF16, T ? 1 : 0, W, WV>;   // its loads and products
+    using F = FewRows<BF16, T ? 1 : 0, W, 8>;   // its loads and products
     using In = typename F::In;
     static constexpr int KV = F::KV, STEP = 4 * KV, KP = U * STEP;
     struct Regs {
@@ -41,63 +43,88 @@ struct Strip {
 
     const In *xr[RT];    // this lane's rows of x
     int64_t x_plane;     // elements from a plane to the next
-    const In *w;
-    int64_t ldw;
+    const In *w;         // the expert's weights: the same for all lanes, as n0 is,
+    int64_t ldw;         // so that a load's address is a scalar and `off`
+    uint32_t off[T ? W : KV];
     int q, c, n0, N, K;
 
+    // First of this lane's columns (w as K x N): the last pieces of a strip that N
+    // ends in move back to end with it, and repeat columns.
     __device__ __forceinline__ int first_col() const { return min(n0 + W * c, max(N - W, 0)); }
 
-    template <bool TAIL, bool NARROW>
+    // Lane, strip and extents; byte offsets stay below 2^32 (weights' pitch at most 2^24).
+    __device__ __forceinline__ void place(int lane, int n0_, int N_, int K_, int64_t ldw_)
+    {
+        q = lane >> 4;
+        c = lane & 15;
+        n0 = n0_;
+        N = N_;
+        K = K_;
+        ldw = ldw_;
+        const uint32_t pitch = (uint32_t)ldw;
+        if constexpr (T) {
+#pragma unroll
+            for (int f = 0; f < W; ++f)
+                off[f] = ((uint32_t)(min(n0 + 16 * f + c, N - 1) - n0) * pitch + q * KV) * (uint32_t)sizeof(In);
+        } else {
+#pragma unroll
+            for (int i = 0; i < KV; ++i) off[i] = ((q * KV + i) * pitch + first_col()) * (uint32_t)sizeof(In);
+        }
+    }
+
+    // The pass at k0.  TAIL: K may end in it.  A lane whose values would pass the end
+    // (K >= KV) loads the last KV values instead, and zeros in both operands for those
+    // that a lower lane has: no branches.
+    template <bool TAIL>
     __device__ __forceinline__ void load(int k0, Regs &r) const
     {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int k = k0 + u * STEP + q * KV;
+            const int from = TAIL ? min(k, K - KV) : k, lost = k - from;   // values of a lane that do not count
+            auto keep = [&](u32x4 v) {
+                if constexpr (TAIL) {
+#pragma unroll
+                    for (int d = 0; d < 4; ++d) {
+                        if constexpr (BF16)
+                            v[d] &= (2 * d >= lost ? 0xFFFFu : 0u) | (2 * d + 1 >= lost ? 0xFFFF0000u : 0u);
+                        else
+                            v[d] = d >= lost ? v[d] : 0u;
+                    }
+                }
+                return v;
+            };
 #pragma unroll
             for (int p = 0; p < P; ++p) {
                 if constexpr (T) {
+                    const unsigned char *base =
+                        reinterpret_cast<const unsigned char *>(w + (int64_t)(p * N + n0) * ldw + k0) + u * STEP * sizeof(In);
 #pragma unroll
-                    for (int f = 0; f < W; ++f) {
-                        const In *row = w + (int64_t)(p * N + min(n0 + 16 * f + c, N - 1)) * ldw;
-                        r.w[(u * P + p) * W + f] = TAIL ? F::load_masked(row, k, K) : F::load_chunk(row + k);
-                    }
+                    for (int f = 0; f < W; ++f)
+                        r.w[(u * P + p) * W + f] = keep(F::load_chunk(reinterpret_cast<const In *>(base + off[f]) - lost));
                 } else {
-                    const int col = first_col();
+                    const unsigned char *base =
+                        reinterpret_cast<const unsigned char *>(w + (int64_t)(k0 + u * STEP) * ldw + p * (int64_t)N);
+                    const In *row = w + from * ldw + p * (int64_t)N + first_col();   // of a tail
 #pragma unroll
                     for (int i = 0; i < KV; ++i) {
-                        const In *row = w + (int64_t)(TAIL ? min(k + i, K - 1) : k + i) * ldw + p * (int64_t)N;
                         union {
                             typename F::piece v;
-                            In e[W];
                             uint32_t d[F::PD];
                         } t;
-                        if constexpr (NARROW) {
-#pragma unroll
-                            for (int j = 0; j < W; ++j) t.e[j] = row[min(col + j, N - 1)];
-                        } else {
-                            t.v = *reinterpret_cast<const typename F::piece *>(row + col);
-                        }
+                        t.v = TAIL ? *reinterpret_cast<const typename F::piece *>(row + i * ldw)
+                                   : *reinterpret_cast<const typename F::piece *>(base + off[i]);
 #pragma unroll
                         for (int d = 0; d < F::PD; ++d)
-                            r.v[(u * P + p) * KV + i][d] = !TAIL || k + i < K ? t.d[d] : 0u;
+                            r.v[(u * P + p) * KV + i][d] = !TAIL || i >= lost ? t.d[d] : 0u;
                     }
                 }
             }
 #pragma unroll
             for (int t = 0; t < RT; ++t)
 #pragma unroll
-                for (int h = 0; h < XP; ++h)
-                    r.x[u][h][t] = TAIL ? F::load_masked(xr[t] + h * x_plane, k, K) : F::load_chunk(xr[t] + h * x_plane + k);
+                for (int h = 0; h < XP; ++h) r.x[u][h][t] = keep(F::load_chunk(xr[t] + h * x_plane + from));
         }
-    }
-    // The pass at k0 < K, whole or cut.
-    template <bool NARROW>
-    __device__ __forceinline__ void load(int k0, Regs &r) const
-    {
-        if (k0 + KP <= K)
-            load<false, NARROW>(k0, r);
-        else
-            load<true, NARROW>(k0, r);
     }
     __device__ __forceinline__ void compute(const Regs &r, floatx4 (&acc)[P * W][RT]) const
     {
@@ -142,7 +169,6 @@ __device__ __forceinline__ void clear(floatx4 (&acc)[N][RT])
 
 // ------------------------------------------------------- experts and tokens --
 
-// The set of experts that a chunk's ids name: a bit each, by one wave.
 constexpr int MAX_EXPERTS = MOE_MAX_EXPERTS;
 
 __device__ __forceinline__ void wave_order()
@@ -151,15 +177,29 @@ __device__ __forceinline__ void wave_order()
     __builtin_amdgcn_wave_barrier();
 }
 
-__device__ __forceinline__ void mark_experts(const int32_t *ids, int count, int experts, uint32_t *bits, int lane)
+// Marks the experts that the ids name, by the block; ids out of range name none.
+template <int WV>
+__device__ __forceinline__ void mark_experts(const int32_t *ids, int count, int experts, uint32_t *bits, int tid)
 {
-    if (lane < MAX_EXPERTS / 32) bits[lane] = 0;
-    wave_order();
-    for (int i = lane; i < count; i += 64) {
-        const unsigned e = (unsigned)ids[i];
-        if (e < (unsigned)experts) atomicOr(&bits[e >> 5], 1u << (e & 31));
+    const int32_t first = tid < count ? ids[tid] : -1;   // under way while the bits are cleared
+    if (tid < MAX_EXPERTS / 32) bits[tid] = 0;
+    __syncthreads();
+    for (int i = tid; i < count; i += 64 * WV) {
+        const int32_t id = i == tid ? first : ids[i];
+        if ((unsigned)id < (unsigned)experts) atomicOr(&bits[(unsigned)id >> 5], 1u << (id & 31));
     }
-    wave_order();
+    __syncthreads();
+}
+
+// This block's place in a list of `count`.  Strips of w as K x N that lie side by side
+// share cache lines: they run on one XCD (16 tokens, 64 experts of 2048 x 1024: 163 us,
+// spread 168).  Strips of w as N x K share nothing, and spread (64 tokens, 8 experts of
+// 4096 x 8192: 440 us, side by side on one XCD 520).
+template <bool T>
+__device__ __forceinline__ int place_of_block(int count)
+{
+    if constexpr (!T) return xcd_place(count);
+    return (int)blockIdx.x < count ? (int)blockIdx.x : -1;
 }
 
 // Sum over the lanes below and this one.
@@ -187,307 +227,351 @@ __device__ __forceinline__ int expert_at(const uint32_t *bits, int u, int lane)
     return 32 * at + __builtin_ctz(word);
 }
 
-struct Place {
-    int slot;        // t * top + the first j that names the expert
-    float weight;    // all its weights
-};
-
-// The tokens of a chunk that name expert e, in order: their places, and how many.
-// Lane t looks after token t.
-template <bool WEIGHTS, class Ids, class Weights>
-__device__ __forceinline__ int list_tokens(int e, int tokens, int top, Ids &&id, Weights &&weight, Place *list, int lane)
+// ids[first ..] == e for a token's `top` ids: the place of the first of them, or -1.
+__device__ __forceinline__ int first_place(const int32_t *ids, int first, int top, int e)
 {
-    int slot = -1;
-    float sum = 0.0f;
-    if (lane < tokens)
-        for (int j = top - 1; j >= 0; --j)
-            if (id(lane * top + j) == e) {
-                slot = lane * top + j;
-                if (WEIGHTS) sum += weight(slot);
-            }
-    const uint64_t mine = __ballot(slot >= 0);
-    const int before = __builtin_amdgcn_mbcnt_hi((uint32_t)(mine >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mine, 0));
-    if (slot >= 0) list[before] = Place{slot, sum};
-    wave_order();
-    return __builtin_popcountll(mine);
+    int place = -1;
+#pragma unroll 4
+    for (int j = top - 1; j >= 0; --j) place = ids[first + j] == e ? first + j : place;
+    return place;
 }
 
-// ------------------------------------------------------------ first product --
-
-// h of one expert's tokens of a chunk, a strip of columns over the whole of the
-// hidden width; the waves take turns along it, and their sums meet in LDS.  h is
-// stored as the second product reads it; bf16 as the sum of two bf16 values (16 bits
-// of it: one would add as much to y's error as its own rounding does; the second
-// product waits for its weights, not for the matrix cores).
-template <bool BF16, bool T, int W, int P, int RT, int U>
-__device__ __forceinline__ void up_tile(const MoeArgs &p, int expert, int n0, int t0, int count, const Place *list,
-                                        float *sums, int lane, int wave)
+__device__ __forceinline__ int lanes_below(uint64_t mask)
 {
-    using S = Strip<BF16, T, W, P, 1, RT, U>;
+    return __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
+}
+
+// A strip of an expert's product over the whole of k, for rows list[0 .. count-1] of
+// x (`row` of an entry); waves have a run of k each, and their sums meet in LDS: out(r,
+// col, sums of the panels) for row r and column col of the strip.
+//
+// A wave goes round its run from a place that depends on the strip.  Rows of w as N x
+// K often lie a power of two apart, and blocks in step would read from a few memory
+// channels (16 tokens, 64 experts of 2048 x 1024: 129 us, in step 133).
+template <int WV, bool BF16, bool T, int W, int P, int XP, int RT, int U, class Row, class Out>
+__device__ __forceinline__ void product(const void *w, int64_t ldw, int N, int K, int n0, const void *x, int64_t x_plane,
+                                        int count, Row &&row, float *sums, int lane, int wave, Out &&out)
+{
+    using S = Strip<BF16, T, W, P, XP, RT, U>;
     using In = typename S::In;
     constexpr int BN = 16 * W * P, ROWS = 16 * RT;
     S s;
-    s.q = lane >> 4;
-    s.c = lane & 15;
-    s.n0 = n0;
-    s.N = p.inner;
-    s.K = p.hidden;
-    s.ldw = p.ldup;
-    s.w = static_cast<const In *>(p.up) + expert * p.stride_up;
-    s.x_plane = 0;
+    s.place(lane, n0, N, K, ldw);
+    s.w = static_cast<const In *>(w);
+    s.x_plane = x_plane;
 #pragma unroll
-    for (int t = 0; t < RT; ++t)
-        s.xr[t] = static_cast<const In *>(p.x) + (int64_t)(t0 + list[min(16 * t + s.c, count - 1)].slot / p.top) * p.ldx;
+    for (int t = 0; t < RT; ++t) s.xr[t] = static_cast<const In *>(x) + row(min(16 * t + s.c, count - 1));
     floatx4 acc[P * W][RT];
     clear(acc);
-    auto run = [&](auto narrow_c) {
-        constexpr bool NARROW = decltype(narrow_c)::value;
-        typename S::Regs cur, nxt;
-        int k = wave * S::KP;
-        if (k < p.hidden) s.template load<NARROW>(k, cur);
-        for (; k < p.hidden; k += WV * S::KP) {
-            if (k + WV * S::KP < p.hidden) s.template load<NARROW>(k + WV * S::KP, nxt);
-            s.compute(cur, acc);
-            cur = nxt;
-        }
-    };
-    if (T || p.inner >= W)
-        run(std::false_type());
-    else
-        run(std::true_type());
-#pragma unroll
-    for (int f = 0; f < P * W; ++f) {
-        const int col = s.column(f % W);
-        if (T || col >= 0)
-#pragma unroll
-            for (int t = 0; t < RT; ++t)
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    sums[(wave * ROWS + 16 * t + 4 * s.q + r) * BN + f / W * 16 * W + col] = acc[f][t][r];
+    typename S::Regs cur, nxt;
+    const int passes = K / S::KP;   // whole ones; the cut one is the last wave's
+    const int first = passes * wave / WV, mine = passes * (wave + 1) / WV - first;
+    const bool tail = wave == WV - 1 && passes * S::KP < K;
+    int at = mine > 0 ? n0 / (16 * W) % mine : 0;
+    if (mine > 0) s.template load<false>((first + at) * S::KP, cur);
+    for (int i = 1; i < mine; ++i) {
+        at = at + 1 == mine ? 0 : at + 1;
+        s.template load<false>((first + at) * S::KP, nxt);
+        s.compute(cur, acc);
+        cur = nxt;
     }
-    __syncthreads();
+    if (tail) s.template load<true>(passes * S::KP, nxt);
+    if (mine > 0) s.compute(cur, acc);
+    if (tail) s.compute(nxt, acc);
+    // half of the waves' sums, then the others' added to them: sums takes WV / 2 strips
+    auto meet = [&](bool add) {
+        float *mine = sums + wave % (WV / 2) * (ROWS * BN);
+#pragma unroll
+        for (int f = 0; f < P * W; ++f) {
+            const int col = s.column(f % W);
+            if (T || col >= W * s.c)   // (pieces that N's end moved back repeat columns of others)
+#pragma unroll
+                for (int t = 0; t < RT; ++t)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        float &at = mine[(16 * t + 4 * s.q + r) * BN + f / W * 16 * W + col];
+                        at = add ? at + acc[f][t][r] : acc[f][t][r];
+                    }
+        }
+        __syncthreads();
+    };
+    if (wave < WV / 2) meet(false);
+    else __syncthreads();
+    if (wave >= WV / 2) meet(true);
+    else __syncthreads();
     for (int id = (int)threadIdx.x; id < count * 16 * W; id += 64 * WV) {
-        const int row = id / (16 * W), col = id % (16 * W);
-        if (n0 + col >= p.inner) continue;
+        const int r = id / (16 * W), col = id % (16 * W);
+        if (n0 + col >= N) continue;
         float z[P];
 #pragma unroll
         for (int f = 0; f < P; ++f) {
             z[f] = 0.0f;
 #pragma unroll
-            for (int v = 0; v < WV; ++v) z[f] += sums[(v * ROWS + row) * BN + f * 16 * W + col];
+            for (int v = 0; v < WV / 2; ++v) z[f] += sums[(v * ROWS + r) * BN + f * 16 * W + col];
         }
-        float g[1] = {z[0]};
-        act_apply<1>(p.act, false, g);
-        const float h = P == 2 ? g[0] * z[P - 1] : g[0];
-        const int64_t at = ((int64_t)t0 * p.top + list[row].slot) * p.ldh + n0 + col;
-        if constexpr (BF16) {
-            uint16_t *out = static_cast<uint16_t *>(p.h);
-            const uint16_t hi = f32_to_bf16_rne(h);
-            const float rest = h - __uint_as_float((uint32_t)hi << 16);
-            out[at] = hi;
-            out[p.h_plane + at] = f32_to_bf16_rne(fabsf(rest) < __builtin_inff() ? rest : 0.0f);   // infinity has none
-        } else {
-            static_cast<float *>(p.h)[at] = h;
+        out(r, col, z);
+    }
+}
+
+// The u-th expert that the tokens name and, in `list`, the places (token * top + first
+// j) of the tokens that name it, in order.  -1: there are fewer experts.
+struct Routing {
+    uint32_t bits[MAX_EXPERTS / 32];
+    int counts[MOE_MAX_TOKENS / 64];
+    int list[MOE_MAX_TOKENS];
+};
+
+template <int WV, bool MANY>
+__device__ __forceinline__ int route(const MoeArgs &p, int u, Routing &r, int &count, int tid, int lane, int wave)
+{
+    mark_experts<WV>(p.ids, p.tokens * p.top, p.experts, r.bits, tid);
+    const int expert = expert_at(r.bits, u, lane);
+    if (expert < 0) return -1;   // all waves alike
+    // tokens in groups of 64, one per lane
+    const int groups = MANY ? (p.tokens + 63) / 64 : 1;
+    auto place_of = [&](int g) {
+        const int t = 64 * g + lane;
+        return t < p.tokens ? first_place(p.ids, t * p.top, p.top, expert) : -1;
+    };
+    int place[MANY ? MOE_MAX_TOKENS / 64 / WV : 1];
+    if (MANY || wave == 0) {
+#pragma unroll
+        for (int i = 0; i < (MANY ? MOE_MAX_TOKENS / 64 / WV : 1); ++i) {
+            const int g = wave + WV * i;
+            place[i] = g < groups ? place_of(g) : -1;
+            const uint64_t mine = __ballot(place[i] >= 0);
+            if (lane == 0 && g < groups) r.counts[g] = __builtin_popcountll(mine);
+        }
+    }
+    if (MANY) __syncthreads();
+    if (MANY || wave == 0) {
+#pragma unroll
+        for (int i = 0; i < (MANY ? MOE_MAX_TOKENS / 64 / WV : 1); ++i) {
+            int before = 0;
+            for (int g = 0; MANY && g < min(groups, wave + WV * i); ++g) before += r.counts[g];
+            const uint64_t mine = __ballot(place[i] >= 0);
+            if (place[i] >= 0) r.list[before + lanes_below(mine)] = place[i];
+        }
+    }
+    __syncthreads();
+    count = 0;
+    for (int g = 0; g < groups; ++g) count += r.counts[g];
+    count = __builtin_amdgcn_readfirstlane(count);
+    return expert;
+}
+
+// ------------------------------------------------------------ first product --
+
+// h as the second product reads it; bf16 as the sum of two bf16 values (16 bits of it:
+// one would add as much to y's error as its own rounding does; the second product
+// waits for its weights, not for the matrix cores).
+template <bool BF16>
+__device__ __forceinline__ void store_h(const MoeArgs &p, int64_t at, float h)
+{
+    if constexpr (BF16) {
+        uint16_t *out = static_cast<uint16_t *>(p.h);
+        const uint16_t hi = f32_to_bf16_rne(h);
+        const float rest = h - __uint_as_float((uint32_t)hi << 16);
+        out[at] = hi;
+        out[p.h_plane + at] = f32_to_bf16_rne(fabsf(rest) < __builtin_inff() ? rest : 0.0f);   // infinity has none
+    } else {
+        static_cast<float *>(p.h)[at] = h;
+    }
+}
+
+// h of one expert's tokens, a strip of columns.
+template <int WV, bool BF16, bool T, int W, int P, bool MANY>
+__global__ void __launch_bounds__(64 * WV, 2) moe_up_kernel(MoeArgs p)
+{
+    __shared__ Routing routing;
+    __shared__ float sums[WV / 2 * 16 * (MANY ? 4 : 1) * 16 * W * P];
+    const int tid = (int)threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int at = place_of_block<T>(p.max_used * p.strips_up);
+    if (at < 0) return;
+    const int u = at / p.strips_up, n0 = at % p.strips_up * 16 * W;
+    int count;
+    const int expert = route<WV, MANY>(p, u, routing, count, tid, lane, wave);
+    if (expert < 0) return;
+    using In = typename std::conditional<BF16, uint16_t, float>::type;
+    const In *w = static_cast<const In *>(p.up) + expert * p.stride_up;
+    auto tile = [&](auto rt_c, auto u_c, int row0, int rows) {
+        const int *list = routing.list + row0;
+        product<WV, BF16, T, W, P, 1, decltype(rt_c)::value, decltype(u_c)::value>(
+            w, p.ldup, p.inner, p.hidden, n0, p.x, 0, rows,
+            [&](int r) { return (int64_t)(list[r] / p.top) * p.ldx; }, sums, lane, wave,
+            [&](int r, int col, const float (&z)[P]) {
+                float g[1] = {z[0]};
+                act_apply<1>(p.act, false, g);
+                const float h = P == 2 ? g[0] * z[P - 1] : g[0];
+                store_h<BF16>(p, list[r] * p.ldh + n0 + col, h);
+            });
+    };
+    using std::integral_constant;
+    constexpr int STEPS = 8 / (W * P);   // per pass
+    if constexpr (!MANY) {
+        tile(integral_constant<int, 1>(), integral_constant<int, STEPS>(), 0, count);
+    } else {
+        for (int row0 = 0; row0 < count; row0 += 64) {
+            const int rows = min(64, count - row0);
+            if (row0 > 0) __syncthreads();   // the sums of the rows before are read
+            if (rows <= 16)
+                tile(integral_constant<int, 1>(), integral_constant<int, T ? STEPS : 1>(), row0, rows);
+            else if (rows <= 32)
+                tile(integral_constant<int, 2>(), integral_constant<int, T ? 2 : 1>(), row0, rows);
+            else
+                tile(integral_constant<int, 4>(), integral_constant<int, 1>(), row0, rows);
         }
     }
 }
 
-template <bool BF16, bool T, int P, int RTMAX>
-struct UpShape {
-    static constexpr int W = (T ? 2 : 4) / P;
-    static constexpr int LDS = WV * 16 * RTMAX * 16 * W * P;   // floats
+// ------------------------------------------- second product, up to 16 tokens --
+
+// y of all tokens, a strip of columns: the block goes through all experts (or through
+// its part of them), each expert's inner width in passes; the list of (expert, whole
+// pass) is cut into one run per wave, then the waves take the experts' cut passes in
+// turn.  A wave adds an expert's sums, weighted, to its own y in LDS when it leaves
+// the expert; the waves' y are added at the end, in order.
+struct Entry {
+    int place;       // token * top + the first j that names the expert
+    float weight;    // all its weights
 };
 
-template <bool BF16, bool T, int P, int RTMAX>
-__global__ void __launch_bounds__(64 * WV) moe_up_kernel(MoeArgs p)
+template <bool BF16, bool T, int W, int U>
+__device__ __forceinline__ void down_strip(const MoeArgs &p, int n0, const uint16_t *experts, const int32_t *ids,
+                                           const float *weights, Entry (*lists)[16], float *y, int begin, int end,
+                                           int cut, int cuts, int step, int lane)
 {
-    using Shape = UpShape<BF16, T, P, RTMAX>;
-    constexpr int W = Shape::W;
-    __shared__ uint32_t bits[WV][MAX_EXPERTS / 32];
-    __shared__ Place list[WV][64];
-    __shared__ float sums[Shape::LDS];
-    const int lane = (int)threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    const int strip = (int)blockIdx.x % p.strips_up, rest = (int)blockIdx.x / p.strips_up;
-    const int u = rest % p.max_used, chunk = rest / p.max_used;
-    const int t0 = chunk * 16 * RTMAX, tokens = min(16 * RTMAX, p.tokens - t0);
-    const int32_t *ids = p.ids + (int64_t)t0 * p.top;
-
-    // each wave for itself, without a barrier
-    mark_experts(ids, tokens * p.top, p.experts, bits[wave], lane);
-    const int expert = expert_at(bits[wave], u, lane);
-    if (expert < 0) return;   // all waves alike
-    const int count = list_tokens<false>(expert, tokens, p.top, [&](int i) { return ids[i]; },
-                                         [](int) { return 0.0f; }, list[wave], lane);
-    const int n0 = strip * 16 * W;
-    if (RTMAX == 1 || count <= 16)
-        up_tile<BF16, T, W, P, 1, 4>(p, expert, n0, t0, count, list[wave], sums, lane, wave);
-    else if (RTMAX == 2 || count <= 32)
-        up_tile<BF16, T, W, P, RTMAX < 2 ? 1 : 2, 2>(p, expert, n0, t0, count, list[wave], sums, lane, wave);
-    else
-        up_tile<BF16, T, W, P, RTMAX < 4 ? 1 : 4, 2>(p, expert, n0, t0, count, list[wave], sums, lane, wave);
-}
-
-// ----------------------------------------------------------- second product --
-
-// y of a chunk's tokens, a strip of columns: the block goes through all experts of
-// the chunk (or through its part of them), each expert's inner width in passes; the
-// list of (expert, pass) is cut into one run per wave.  A wave adds an expert's
-// sums, weighted, to its own y in LDS when it leaves the expert; the waves' y are
-// added at the end, in order.
-template <bool BF16, bool T, int W, int RT, int U, int NT>
-__device__ __forceinline__ void down_strip(const MoeArgs &p, int n0, int t0, int tokens, const uint16_t *experts,
-                                           const int32_t *ids, const float *weights, Place (*lists)[64], float *y,
-                                           int begin, int end, int passes, int lane)
-{
-    using S = Strip<BF16, T, W, 1, BF16 ? 2 : 1, RT, U>;
+    using S = Strip<BF16, T, W, 1, BF16 ? 2 : 1, 1, U>;
     using In = typename S::In;
+    const int passes = p.inner / S::KP;   // whole ones
     S s;
-    s.q = lane >> 4;
-    s.c = lane & 15;
-    s.n0 = n0;
-    s.N = p.hidden;
-    s.K = p.inner;
-    s.ldw = p.lddown;
+    s.place(lane, n0, p.hidden, p.inner, p.lddown);
     s.x_plane = p.h_plane;
-    if (begin >= end) return;
-    floatx4 acc[W][RT];
+    floatx4 acc[W][1];
     clear(acc);
-    int u = begin / passes, pass = begin - u * passes;
-    int which = 0, count = 0, next_count = 0;
-    // the rows and weights of the u-th expert, its list in buffer b
-    auto enter = [&](int b) {
-        const int e = experts[u];
+    // the rows and weights of the u-th expert, its list in buffer b; lane t looks after token t
+    auto enter = [&](int u, int b) {
+        const int e = __builtin_amdgcn_readfirstlane(experts[u]);
         s.w = static_cast<const In *>(p.down) + e * p.stride_down;
-        const int n = list_tokens<true>(e, tokens, p.top, [&](int i) { return ids[i]; },
-                                        [&](int i) { return weights[i]; }, lists[b], lane);
-#pragma unroll
-        for (int t = 0; t < RT; ++t)
-            s.xr[t] = static_cast<const In *>(p.h) +
-                      ((int64_t)t0 * p.top + lists[b][min(16 * t + s.c, n - 1)].slot) * p.ldh;
+        int place = -1;
+        float weight = 0.0f;
+        if (lane < p.tokens) {
+#pragma unroll 4
+            for (int j = p.top - 1; j >= 0; --j) {
+                const bool here = ids[lane * p.top + j] == e;
+                place = here ? lane * p.top + j : place;
+                weight += here ? weights[lane * p.top + j] : 0.0f;
+            }
+        }
+        const uint64_t mine = __ballot(place >= 0);
+        if (place >= 0) lists[b][lanes_below(mine)] = Entry{place, weight};
+        wave_order();
+        const int n = __builtin_popcountll(mine);
+        s.xr[0] = static_cast<const In *>(p.h) + (int64_t)lists[b][min(s.c, n - 1)].place * p.ldh;
         return n;
     };
-    auto run = [&](auto narrow_c) {
-        constexpr bool NARROW = decltype(narrow_c)::value;
-        typename S::Regs cur, nxt;
-        count = enter(which);
-        s.template load<NARROW>(pass * S::KP, cur);
+    auto leave = [&](int b, int count) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int row = 4 * s.q + r;
+            if (row >= count) continue;
+            const Entry at = lists[b][row];
+            float *out = y + at.place / p.top * (16 * W);
+#pragma unroll
+            for (int j = 0; j < W; ++j) {
+                const int col = s.column(j);
+                // (pieces that N's end moved back repeat columns of others)
+                if (T || col >= W * s.c) out[col] += at.weight * acc[j][0][r];
+            }
+        }
+        clear(acc);
+        wave_order();
+    };
+    typename S::Regs cur, nxt;
+    if (begin < end) {
+        int u = begin / passes, pass = begin - u * passes, b = 0;
+        const int rot = n0 / (16 * W) % passes;   // as in product()
+        auto k_of = [&](int pass) {
+            const int at = pass + rot;
+            return (at >= passes ? at - passes : at) * S::KP;
+        };
+        int count = enter(u, b), next_count = 0;
+        s.template load<false>(k_of(pass), cur);
         for (int i = begin; i < end; ++i) {
-            bool leave = true;
+            bool last = true;
             if (i + 1 < end) {
-                leave = ++pass == passes;
-                if (leave) {
+                last = ++pass == passes;
+                if (last) {
                     pass = 0;
-                    ++u;
-                    next_count = enter(which ^ 1);
+                    next_count = enter(++u, b ^ 1);
                 }
-                s.template load<NARROW>(pass * S::KP, nxt);
+                s.template load<false>(k_of(pass), nxt);
             }
             s.compute(cur, acc);
-            if (leave) {
-#pragma unroll
-                for (int t = 0; t < RT; ++t)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int row = 16 * t + 4 * s.q + r;
-                        if (row >= count) continue;
-                        const Place at = lists[which][row];
-                        float *out = y + at.slot / p.top * (16 * W);
-#pragma unroll
-                        for (int j = 0; j < W; ++j) {
-                            const int col = s.column(j);
-                            // (pieces that N's end moved back repeat columns of others)
-                            if (T || col >= W * s.c) out[col] += at.weight * acc[j][t][r];
-                        }
-                    }
-                clear(acc);
-                which ^= 1;
+            if (last) {
+                leave(b, count);
+                b ^= 1;
                 count = next_count;
-                wave_order();
             }
             cur = nxt;
         }
-    };
-    if (T || p.hidden >= W)
-        run(std::false_type());
-    else
-        run(std::true_type());
+    }
+    if (passes * S::KP < p.inner)
+        for (int u = cut; u < cuts; u += step) {
+            const int count = enter(u, 0);
+            s.template load<true>(passes * S::KP, cur);
+            s.compute(cur, acc);
+            leave(0, count);
+        }
 }
 
-template <bool BF16, bool T, int RTMAX>
-struct DownShape {
-    static constexpr int W = RTMAX == 1 && T ? 1 : 2;
-};
-
-template <bool BF16, bool T, int RTMAX>
-__global__ void __launch_bounds__(64 * WV) moe_down_kernel(MoeArgs p)
+template <bool BF16, bool T, int W>
+__global__ void __launch_bounds__(512) moe_down_few_kernel(MoeArgs p)
 {
-    constexpr int W = DownShape<BF16, T, RTMAX>::W, NT = 16 * RTMAX, BN = 16 * W;
+    constexpr int WV = 8, BN = 16 * W, U = 4 / W, KP = U * 4 * (BF16 ? 8 : 4);
     __shared__ uint32_t bits[MAX_EXPERTS / 32];
-    __shared__ uint16_t experts[MAX_EXPERTS];
-    __shared__ int32_t ids[NT * MOE_MAX_TOP];
-    __shared__ float weights[NT * MOE_MAX_TOP];
-    __shared__ Place lists[WV][2][64];
-    __shared__ float y[WV][NT * BN];
-    __shared__ int counts[RTMAX > 1 ? MAX_EXPERTS : 1];
-    __shared__ int shared_used, shared_most;
+    __shared__ uint16_t experts[16 * MOE_MAX_TOP];
+    __shared__ int32_t ids[16 * MOE_MAX_TOP];
+    __shared__ float weights[16 * MOE_MAX_TOP];
+    __shared__ Entry lists[WV][2][16];
+    __shared__ float y[WV][16 * BN];
+    __shared__ int shared_used;
     const int tid = (int)threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int strip = (int)blockIdx.x % p.strips_down, rest = (int)blockIdx.x / p.strips_down;
-    const int part = rest % p.parts, chunk = rest / p.parts;
-    const int t0 = chunk * NT, tokens = min(NT, p.tokens - t0), slots = tokens * p.top;
+    const int at = place_of_block<T>(p.strips_down * p.parts);
+    if (at < 0) return;
+    const int n0 = at % p.strips_down * BN, part = at / p.strips_down, places = p.tokens * p.top;
 
-    for (int i = tid; i < slots; i += 64 * WV) {
-        ids[i] = p.ids[(int64_t)t0 * p.top + i];
-        weights[i] = p.weights[(int64_t)t0 * p.top + i];
+    for (int i = tid; i < places; i += 64 * WV) {
+        ids[i] = p.ids[i];
+        weights[i] = p.weights[i];
     }
-    for (int i = tid; i < WV * NT * BN; i += 64 * WV) (&y[0][0])[i] = 0.0f;
-    if (RTMAX > 1)
-        for (int i = tid; i < MAX_EXPERTS; i += 64 * WV) counts[i] = 0;
-    if (tid == 0) shared_most = 0;
-    __syncthreads();
+    for (int i = tid; i < WV * 16 * BN; i += 64 * WV) (&y[0][0])[i] = 0.0f;
+    mark_experts<WV>(p.ids, places, p.experts, bits, tid);
     if (wave == 0) {
-        mark_experts(ids, slots, p.experts, bits, lane);
         uint32_t w = lane < MAX_EXPERTS / 32 ? bits[lane] : 0;
         const int own = __builtin_popcount(w), upto = scan(own, lane);
-        for (int at = upto - own; w != 0; ++at, w &= w - 1) experts[at] = (uint16_t)(32 * lane + __builtin_ctz(w));
+        for (int i = upto - own; w != 0; ++i, w &= w - 1) experts[i] = (uint16_t)(32 * lane + __builtin_ctz(w));
         if (lane == 63) shared_used = upto;
-    } else if (RTMAX > 1) {
-        for (int i = tid - 64; i < slots; i += 64 * (WV - 1))
-            if ((unsigned)ids[i] < (unsigned)p.experts) {
-                const int n = atomicAdd(&counts[ids[i]], 1) + 1;
-                if (n > 16) atomicMax(&shared_most, n);
-            }
     }
     __syncthreads();
-    const int used = shared_used, most = shared_most;   // (most: 0 up to 16 rows; a token that names one twice counts twice)
-    const int n0 = strip * BN;
-    auto share = [&](auto u_c, auto rt_c) {
-        constexpr int U = decltype(u_c)::value, RT = decltype(rt_c)::value;
-        constexpr int KP = U * 4 * (BF16 ? 8 : 4);
-        const int passes = (p.inner + KP - 1) / KP;
-        const int64_t items = (int64_t)used * passes;
-        const int64_t first = items * part / p.parts, last = items * (part + 1) / p.parts;
-        const int begin = (int)(first + (last - first) * wave / WV), end = (int)(first + (last - first) * (wave + 1) / WV);
-        down_strip<BF16, T, W, RT, U, NT>(p, n0, t0, tokens, experts, ids, weights, lists[wave], y[wave], begin, end,
-                                          passes, lane);
-    };
-    if (RTMAX == 1 || most <= 16)
-        share(std::integral_constant<int, 4>(), std::integral_constant<int, 1>());
-    else if (RTMAX == 2 || most <= 32)
-        share(std::integral_constant<int, 2>(), std::integral_constant<int, RTMAX < 2 ? 1 : 2>());
-    else
-        share(std::integral_constant<int, 1>(), std::integral_constant<int, RTMAX < 4 ? 1 : 4>());
+    const int used = shared_used, passes = p.inner / KP;
+    const int64_t items = (int64_t)used * passes;
+    const int64_t first = items * part / p.parts, last = items * (part + 1) / p.parts;
+    const int begin = (int)(first + (last - first) * wave / WV), end = (int)(first + (last - first) * (wave + 1) / WV);
+    down_strip<BF16, T, W, U>(p, n0, experts, ids, weights, lists[wave], y[wave], begin, end, part * WV + wave, used,
+                               p.parts * WV, lane);
     __syncthreads();
-    for (int i = tid; i < tokens * BN; i += 64 * WV) {
+    for (int i = tid; i < p.tokens * BN; i += 64 * WV) {
         const int token = i / BN, col = n0 + i % BN;
         if (col >= p.hidden) continue;
         float v[1] = {0.0f};
 #pragma unroll
         for (int w = 0; w < WV; ++w) v[0] += y[w][i];
         if (p.parts > 1) {
-            p.ws[((int64_t)part * p.tokens + t0 + token) * p.hidden + col] = v[0];
+            p.ws[((int64_t)part * p.tokens + token) * p.hidden + col] = v[0];
         } else {
             const float none[1] = {0.0f};
-            finish_piece<1>(p.e, 0, t0 + token, col, 1, none, v);
+            finish_piece<1>(p.e, 0, token, col, 1, none, v);
         }
     }
 }
@@ -505,43 +589,185 @@ __global__ void __launch_bounds__(256) moe_join_kernel(MoeArgs p)
     }
 }
 
-template <bool BF16, bool T, int RTMAX>
-hipError_t launch(const MoeArgs &a, const MoePlan &plan, hipStream_t stream)
+// --------------------------------------------- second product, more tokens --
+
+// One expert's rows, a strip of columns, to ws by place.
+template <int WV, bool BF16, bool T, int W>
+__global__ void __launch_bounds__(64 * WV, 2) moe_down_rows_kernel(MoeArgs p)
 {
-    if (plan.blocks_up > 0) {
-        auto kernel = a.gated ? moe_up_kernel<BF16, T, 2, RTMAX> : moe_up_kernel<BF16, T, 1, RTMAX>;
-        hipLaunchKernelGGL(kernel, dim3((unsigned)plan.blocks_up), dim3(64 * WV), 0, stream, a);
-        const hipError_t err = hipGetLastError();
-        if (err != hipSuccess) return err;
+    __shared__ Routing routing;
+    __shared__ float sums[WV / 2 * 64 * 16 * W];
+    const int tid = (int)threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int at = place_of_block<T>(p.max_used * p.strips_down);
+    if (at < 0) return;
+    const int u = at / p.strips_down, n0 = at % p.strips_down * 16 * W;
+    int count;
+    const int expert = route<WV, true>(p, u, routing, count, tid, lane, wave);
+    if (expert < 0) return;
+    using In = typename std::conditional<BF16, uint16_t, float>::type;
+    const In *w = static_cast<const In *>(p.down) + expert * p.stride_down;
+    auto tile = [&](auto rt_c, auto u_c, int row0, int rows) {
+        const int *list = routing.list + row0;
+        product<WV, BF16, T, W, 1, BF16 ? 2 : 1, decltype(rt_c)::value, decltype(u_c)::value>(
+            w, p.lddown, p.hidden, p.inner, n0, p.h, p.h_plane, rows, [&](int r) { return (int64_t)list[r] * p.ldh; },
+            sums, lane, wave,
+            [&](int r, int col, const float (&z)[1]) { p.ws[(int64_t)list[r] * p.hidden + n0 + col] = z[0]; });
+    };
+    using std::integral_constant;
+    for (int row0 = 0; row0 < count; row0 += 64) {
+        const int rows = min(64, count - row0);
+        if (row0 > 0) __syncthreads();   // the sums of the rows before are read
+        if (rows <= 16)
+            tile(integral_constant<int, 1>(), integral_constant<int, T ? 8 / W : 1>(), row0, rows);
+        else if (rows <= 32)
+            tile(integral_constant<int, 2>(), integral_constant<int, T ? 2 : 1>(), row0, rows);
+        else
+            tile(integral_constant<int, 4>(), integral_constant<int, 1>(), row0, rows);
     }
-    hipLaunchKernelGGL((moe_down_kernel<BF16, T, RTMAX>), dim3((unsigned)plan.blocks_down), dim3(64 * WV), 0, stream, a);
-    const hipError_t err = hipGetLastError();
-    if (err != hipSuccess || a.parts == 1) return err;
-    const int64_t blocks = ((int64_t)a.tokens * a.hidden + 255) / 256;
-    hipLaunchKernelGGL(moe_join_kernel, dim3((unsigned)(blocks < 65536 ? blocks : 65536)), dim3(256), 0, stream, a);
+}
+
+// y of a token from its experts' rows, in the order of its ids; a block has 256
+// columns of a token.
+__global__ void __launch_bounds__(256) moe_sum_kernel(MoeArgs p, int col_blocks)
+{
+    __shared__ int32_t ids[MOE_MAX_TOP];
+    __shared__ float weights[MOE_MAX_TOP], shares[MOE_MAX_TOP];
+    __shared__ int counts[MOE_MAX_TOP];   // whether a place counts: an expert's first
+    const int tid = (int)threadIdx.x, token = (int)blockIdx.x / col_blocks;
+    const int col = ((int)blockIdx.x - token * col_blocks) * 256 + tid;
+    if (tid < p.top) {
+        ids[tid] = p.ids[token * p.top + tid];
+        weights[tid] = p.weights[token * p.top + tid];
+    }
+    __syncthreads();
+    if (tid < p.top) {
+        // all the weights of an expert at its first place
+        bool first = (unsigned)ids[tid] < (unsigned)p.experts;
+        float sum = 0.0f;
+        for (int j = p.top - 1; j >= 0; --j)
+            if (ids[j] == ids[tid]) {
+                sum += weights[j];
+                if (j < tid) first = false;
+            }
+        shares[tid] = sum;
+        counts[tid] = first;
+    }
+    __syncthreads();
+    if (col >= p.hidden) return;
+    float v[1] = {0.0f};
+    const float none[1] = {0.0f};
+    for (int j = 0; j < p.top; ++j)
+        if (counts[j]) v[0] += shares[j] * p.ws[((int64_t)token * p.top + j) * p.hidden + col];
+    finish_piece<1>(p.e, 0, token, col, 1, none, v);
+}
+
+// ------------------------------------------------------------ small widths --
+
+// Widths below 8, which the vectors above do not fit: a thread per value.
+template <bool BF16>
+__device__ __forceinline__ float value(const void *x, int64_t at)
+{
+    return BF16 ? __uint_as_float((uint32_t) static_cast<const uint16_t *>(x)[at] << 16) : static_cast<const float *>(x)[at];
+}
+
+template <bool BF16, bool T>
+__global__ void __launch_bounds__(256) moe_small_up_kernel(MoeArgs p)
+{
+    const int64_t total = (int64_t)p.tokens * p.top * p.inner;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+        const int place = (int)(i / p.inner), col = (int)(i - (int64_t)place * p.inner), token = place / p.top;
+        const int e = p.ids[place];
+        if ((unsigned)e >= (unsigned)p.experts) continue;
+        float z[2] = {0.0f, 0.0f};
+        for (int k = 0; k < p.hidden; ++k) {
+            const float x = value<BF16>(p.x, token * p.ldx + k);
+            for (int f = 0; f < (p.gated ? 2 : 1); ++f) {
+                const int n = f * p.inner + col;
+                z[f] += x * value<BF16>(p.up, e * p.stride_up + (T ? n * p.ldup + k : k * p.ldup + n));
+            }
+        }
+        float g[1] = {z[0]};
+        act_apply<1>(p.act, false, g);
+        store_h<BF16>(p, place * p.ldh + col, p.gated ? g[0] * z[1] : g[0]);
+    }
+}
+
+template <bool BF16, bool T>
+__global__ void __launch_bounds__(256) moe_small_down_kernel(MoeArgs p)
+{
+    const int64_t total = (int64_t)p.tokens * p.top * p.hidden;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+        const int place = (int)(i / p.hidden), col = (int)(i - (int64_t)place * p.hidden);
+        const int e = p.ids[place];
+        if ((unsigned)e >= (unsigned)p.experts) continue;
+        float sum = 0.0f;
+        for (int k = 0; k < p.inner; ++k) {
+            float h = value<BF16>(p.h, place * p.ldh + k);
+            if (BF16) h += value<BF16>(p.h, p.h_plane + place * p.ldh + k);
+            sum += h * value<BF16>(p.down, e * p.stride_down + (T ? col * p.lddown + k : k * p.lddown + col));
+        }
+        p.ws[i] = sum;
+    }
+}
+
+// ------------------------------------------------------------------ launch --
+
+// Fragments of 16 columns of a block, both panels of the first product.
+constexpr int strip(bool t, bool wide) { return t ? (wide ? 4 : 2) : (wide ? 8 : 4); }
+// Waves of a block.  With more than 16 tokens the waves' registers leave room for 8 of
+// them on a unit either way; blocks of 4 overlap one another's start and end (64
+// tokens, 64 experts of 2048 x 1024: 186 us, with blocks of 8 200).
+constexpr int WAVES_FEW = 8, WAVES_MANY = 4;
+
+template <bool BF16, bool T, int P>
+void (*up_kernel(const MoePlan &plan))(MoeArgs)
+{
+    constexpr int WIDE = strip(T, true) / P, NARROW = strip(T, false) / P;
+    return plan.many ? (plan.wide_up ? moe_up_kernel<WAVES_MANY, BF16, T, WIDE, P, true>
+                                     : moe_up_kernel<WAVES_MANY, BF16, T, NARROW, P, true>)
+                     : (plan.wide_up ? moe_up_kernel<WAVES_FEW, BF16, T, WIDE, P, false>
+                                     : moe_up_kernel<WAVES_FEW, BF16, T, NARROW, P, false>);
+}
+
+hipError_t run(void (*kernel)(MoeArgs), int64_t blocks, int threads, const MoeArgs &a, hipStream_t stream)
+{
+    if (blocks == 0) return hipSuccess;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3((unsigned)threads), 0, stream, a);
     return hipGetLastError();
 }
 
 template <bool BF16, bool T>
 hipError_t launch(const MoeArgs &a, const MoePlan &plan, hipStream_t stream)
 {
-    return plan.rows == 16   ? launch<BF16, T, 1>(a, plan, stream)
-           : plan.rows == 32 ? launch<BF16, T, 2>(a, plan, stream)
-                             : launch<BF16, T, 4>(a, plan, stream);
+    const int threads = 64 * (plan.many ? WAVES_MANY : WAVES_FEW);
+    auto up = plan.small  ? moe_small_up_kernel<BF16, T>
+              : a.gated   ? up_kernel<BF16, T, 2>(plan)
+                          : up_kernel<BF16, T, 1>(plan);
+    hipError_t err = run(up, plan.blocks_up, plan.small ? 256 : threads, a, stream);
+    if (err != hipSuccess) return err;
+    constexpr int WIDE = strip(T, true), NARROW = strip(T, false);
+    auto down = plan.small       ? moe_small_down_kernel<BF16, T>
+                : plan.many      ? (plan.wide_down ? moe_down_rows_kernel<WAVES_MANY, BF16, T, WIDE>
+                                                   : moe_down_rows_kernel<WAVES_MANY, BF16, T, NARROW>)
+                : plan.wide_down ? moe_down_few_kernel<BF16, T, WIDE / 2>
+                                 : moe_down_few_kernel<BF16, T, NARROW / 2>;
+    err = run(down, plan.blocks_down, plan.small ? 256 : threads, a, stream);
+    if (err != hipSuccess) return err;
+    if (plan.many || plan.small) {
+        const int col_blocks = (a.hidden + 255) / 256;
+        hipLaunchKernelGGL(moe_sum_kernel, dim3((unsigned)(a.tokens * col_blocks)), dim3(256), 0, stream, a, col_blocks);
+        return hipGetLastError();
+    }
+    if (a.parts == 1) return hipSuccess;
+    const int64_t blocks = ((int64_t)a.tokens * a.hidden + 255) / 256;
+    return run(moe_join_kernel, blocks < 65536 ? blocks : 65536, 256, a, stream);
 }
 
 }  // namespace
 
-int moe_strip_up(bool t, bool gated)
-{
-    return 16 * (gated ? (t ? UpShape<true, true, 2, 1>::W : UpShape<true, false, 2, 1>::W)
-                       : (t ? UpShape<true, true, 1, 1>::W : UpShape<true, false, 1, 1>::W));
-}
-int moe_strip_down(bool t, int rows)
-{
-    return 16 * (rows == 16 ? (t ? DownShape<true, true, 1>::W : DownShape<true, false, 1>::W)
-                            : (t ? DownShape<true, true, 2>::W : DownShape<true, false, 2>::W));
-}
+// Columns of a block of the first product, and of the second.
+int moe_strip_up(bool t, bool gated, bool wide) { return 16 * strip(t, wide) / (gated ? 2 : 1); }
+int moe_strip_down(bool t, bool many, bool wide) { return (many ? 16 : 8) * strip(t, wide); }
 
 hipError_t launch_moe(const MoeArgs &a, const MoePlan &plan, bool bf16, bool transw, hipStream_t stream)
 {

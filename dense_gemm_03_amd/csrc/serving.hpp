@@ -41,6 +41,7 @@ hipError_t launch_log_probs_grad(const LogProbsGradArgs &args, bool bf16, hipStr
 
 constexpr int MOE_MAX_TOP = 32;
 constexpr int MOE_MAX_EXPERTS = 1024;
+constexpr int MOE_MAX_TOKENS = 512;
 
 struct MoeArgs {
     const void *x, *up, *down;
@@ -48,21 +49,23 @@ struct MoeArgs {
     const float *weights;
     void *h;                     // the first product's results: a row of ldh per place (token, j)
     int64_t h_plane;             // elements from h's upper halves to its lower ones (bf16)
-    float *ws;                   // y of `parts` > 1 parts
+    float *ws;                   // y of `parts` > 1 parts; with many tokens, the rows of all places
     EpilogueArgs e;
     int64_t ldx, ldup, lddown, ldh, stride_up, stride_down;
     int tokens, hidden, inner, experts, top, act, gated;
     int strips_up, strips_down;
-    int max_used;                // experts that a chunk of tokens can name
+    int max_used;                // experts that the tokens can name
     int parts;                   // of the second product's sum
 };
 struct MoePlan {
-    int rows;                    // tokens of a chunk: 16, 32 or 64
+    bool small;                  // a width below 8: a thread per value
+    bool many;                   // more than 16 tokens
+    bool wide_up, wide_down;     // strips of a block
     int64_t blocks_up, blocks_down;
 };
-// Columns of a block of either kernel.
-int moe_strip_up(bool transw, bool gated);
-int moe_strip_down(bool transw, int rows);
+// Columns of a block of the first product, and of the second.
+int moe_strip_up(bool transw, bool gated, bool wide);
+int moe_strip_down(bool transw, bool many, bool wide);
 hipError_t launch_moe(const MoeArgs &args, const MoePlan &plan, bool bf16, bool transw, hipStream_t stream);
 
 }  // namespace dg

@@ -128,8 +128,8 @@ int log_probs_grad(const gemm_log_probs_params *p, const void *logits, const int
 
 // ---------------------------------------------------- mixture of experts --
 
-constexpr int64_t kMaxWidth = int64_t(1) << 24;
-constexpr int64_t kMaxTokens = 512;
+constexpr int64_t kMaxWidth = int64_t(1) << 22;
+constexpr int64_t kMaxWeightLd = int64_t(1) << 24;   // byte offsets inside a strip stay below 2^32
 
 int64_t up_columns(const gemm_moe_params &p) { return p.gated ? 2 * p.inner : p.inner; }
 
@@ -139,14 +139,14 @@ bool valid(const gemm_moe_params *p)
         (p->transw != GEMM_OP_N && p->transw != GEMM_OP_T) || p->act < GEMM_ACT_NONE || p->act > GEMM_ACT_SILU ||
         (p->gated != 0 && p->gated != 1))
         return false;
-    if (p->tokens < 0 || p->tokens > kMaxTokens || p->hidden < 0 || p->hidden > kMaxWidth || p->inner < 0 ||
+    if (p->tokens < 0 || p->tokens > MOE_MAX_TOKENS || p->hidden < 0 || p->hidden > kMaxWidth || p->inner < 0 ||
         p->inner > kMaxWidth || p->experts < 0 || p->experts > MOE_MAX_EXPERTS || p->top < 0 || p->top > MOE_MAX_TOP)
         return false;
     const bool t = p->transw == GEMM_OP_T;
     const int64_t n = up_columns(*p), up_row = t ? p->hidden : n, up_rows = t ? n : p->hidden;
     const int64_t down_row = t ? p->inner : p->hidden, down_rows = t ? p->hidden : p->inner;
     if (!valid_ld(p->ldx, p->hidden) || !valid_ld(p->ldy, p->hidden) || !valid_ld(p->ldup, up_row) ||
-        !valid_ld(p->lddown, down_row))
+        !valid_ld(p->lddown, down_row) || p->ldup > kMaxWeightLd || p->lddown > kMaxWeightLd)
         return false;
     // the experts' weights do not overlap
     return p->experts <= 1 || up_rows * up_row == 0 || down_rows * down_row == 0 ||
@@ -163,24 +163,59 @@ struct MoeShares {
 MoeShares shares_of(const gemm_moe_params &p)
 {
     MoeShares s{};
-    s.plan.rows = p.tokens <= 16 ? 16 : p.tokens <= 32 ? 32 : 64;
-    const int64_t chunks = ceil_div(p.tokens, s.plan.rows);
-    s.max_used = (int)std::min(p.experts, std::min<int64_t>(p.tokens, s.plan.rows) * p.top);
-    s.strips_up = (int)ceil_div(p.inner, moe_strip_up(p.transw == GEMM_OP_T, p.gated != 0));
-    s.strips_down = (int)ceil_div(p.hidden, moe_strip_down(p.transw == GEMM_OP_T, s.plan.rows));
-    s.plan.blocks_up = chunks * s.max_used * s.strips_up;
-    const int64_t blocks = chunks * s.strips_down;
-    // parts until there is a block for each compute unit, of at least one expert each
-    s.parts = (int)std::max<int64_t>(1, std::min<int64_t>(device_compute_units() / std::max<int64_t>(1, blocks),
-                                                          std::min<int64_t>(s.max_used, 8)));
-    s.plan.blocks_down = blocks * s.parts;
-    const int64_t vec = 16 / size_of(p.dtype);
+    const bool t = p.transw == GEMM_OP_T, gated = p.gated != 0;
+    const int64_t cus = device_compute_units();
+    s.max_used = (int)std::min(p.experts, p.tokens * p.top);
+    s.plan.small = p.hidden < 8 || p.inner < 8;
+    s.plan.many = p.tokens > 16;
+    s.parts = 1;
+    auto eights = [](int64_t n) { return ceil_div(n, 8) * 8; };   // xcd_place
+    auto strips_up = [&](bool wide) { return ceil_div(p.inner, moe_strip_up(t, gated, wide)); };
+    auto strips_down = [&](bool wide) { return ceil_div(p.hidden, moe_strip_down(t, s.plan.many, wide)); };
+    // Wide strips where there are blocks for all units four times over.  N x K weights: 1
+    // token, 4 experts of 4096 x 2048, 26 us in 512 narrow blocks, 29 in 256 wide ones; 16
+    // tokens, 64 of 2048 x 1024, 82 in 4096 narrow ones, 79 in 2048 wide ones.  K x N: 37
+    // and 48 us, 114 and 97.  With more tokens narrow strips of N x K weights read too
+    // much of x again (20 tokens, 1001 x 2003: 45 us wide, 56 narrow).
+    s.plan.wide_up = (t && s.plan.many) || s.max_used * strips_up(true) >= 4 * cus;
+    s.strips_up = (int)strips_up(s.plan.wide_up);
+    s.plan.blocks_up = eights((int64_t)s.max_used * s.strips_up);
+    if (s.plan.small) {
+        auto blocks = [&](int64_t width) { return std::min<int64_t>(ceil_div(p.tokens * p.top * width, 256), 65536); };
+        s.strips_down = 0;
+        s.plan.blocks_up = blocks(p.inner);
+        s.plan.blocks_down = blocks(p.hidden);
+    } else if (s.plan.many) {
+        s.plan.wide_down = t || s.max_used * strips_down(true) >= 4 * cus;
+        s.strips_down = (int)strips_down(s.plan.wide_down);
+        s.plan.blocks_down = eights((int64_t)s.max_used * s.strips_down);
+    } else {
+        // Strips and parts by the time that the weights take, at 20 KB per us and unit in
+        // wide strips, 17 and 14 in narrow ones of N x K and K x N weights (189 MB, 256
+        // units: 40, 47 and 62 us), and 4.5 us for a launch that joins parts.
+        const double bytes = (double)s.max_used * (double)p.inner * (double)p.hidden * size_of(p.dtype);
+        double best = 0.0;
+        for (int wide = 0; wide < 2; ++wide)
+            for (int parts = 1; parts <= 8; ++parts) {
+                const int64_t blocks = strips_down(wide != 0) * parts;
+                if (parts > 1 && (blocks > cus || parts > s.max_used)) break;
+                const double rate = wide ? 20e3 : t ? 17e3 : 14e3;
+                const double us = bytes / (rate * (double)std::min(cus, blocks)) + (parts > 1 ? 4.5 : 0.0);
+                if ((wide == 0 && parts == 1) || us < best) {
+                    best = us;
+                    s.plan.wide_down = wide != 0;
+                    s.parts = parts;
+                }
+            }
+        s.strips_down = (int)strips_down(s.plan.wide_down);
+        s.plan.blocks_down = eights((int64_t)s.strips_down * s.parts);
+    }
+    const int64_t vec = 16 / size_of(p.dtype), places = p.tokens * p.top;
     s.ldh = ceil_div(p.inner, vec) * vec;
-    const int64_t planes = p.dtype == GEMM_DTYPE_BF16 ? 2 : 1;
-    s.h_bytes = planes * p.tokens * p.top * s.ldh * size_of(p.dtype);   // whole 16 bytes
-    s.total = s.h_bytes + (s.parts > 1 ? s.parts * p.tokens * p.hidden * 4 : 0);
+    s.h_bytes = (p.dtype == GEMM_DTYPE_BF16 ? 2 : 1) * places * s.ldh * size_of(p.dtype);   // whole 16 bytes
+    s.total = s.h_bytes + (s.plan.many || s.plan.small ? places : s.parts > 1 ? s.parts * p.tokens : 0) * p.hidden * 4;
     const int64_t most = int64_t(UINT32_MAX) / 512;   // blocks of a launch
-    s.launchable = s.plan.blocks_up <= most && s.plan.blocks_down <= most;
+    s.launchable = s.plan.blocks_up <= most && s.plan.blocks_down <= most && p.tokens * ceil_div(p.hidden, 256) <= most;
     return s;
 }
 
@@ -210,7 +245,7 @@ int moe_layer(const gemm_moe_params *p, const void *x, const void *up, const voi
     a.weights = weights;
     a.h = workspace;
     a.h_plane = p->tokens * p->top * s.ldh;
-    if (s.parts > 1) a.ws = reinterpret_cast<float *>(static_cast<char *>(workspace) + s.h_bytes);
+    if (s.total > s.h_bytes) a.ws = reinterpret_cast<float *>(static_cast<char *>(workspace) + s.h_bytes);
     a.e = EpilogueArgs{y, nullptr, residual, nullptr, p->ldy, p->ldr, 0, 1.0f, 1.0f, GEMM_ACT_NONE,
                        p->dtype_y == GEMM_DTYPE_BF16, 0, 0};
     a.ldx = p->ldx;
@@ -223,7 +258,7 @@ int moe_layer(const gemm_moe_params *p, const void *x, const void *up, const voi
     a.hidden = (int)p->hidden;
     a.inner = (int)p->inner;
     a.experts = (int)p->experts;
-    a.top = places ? (int)p->top : 0;
+    a.top = places && p->inner > 0 ? (int)p->top : 0;
     a.act = p->act;
     a.gated = p->gated;
     a.strips_up = s.strips_up;

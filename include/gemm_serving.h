@@ -50,7 +50,7 @@ extern "C" {
  * with the sum of the two weights.
  *
  * For a few tokens: at most 512, 32 experts each out of at most 1024, hidden and
- * inner at most 2^24.  The weights are read once per 64 tokens: for long batches
+ * inner at most 2^22, ldup and lddown at most 2^24.  The weights are read once per 64 tokens: for long batches
  * sort the rows by expert and use gemm_linear.
  */
 typedef struct {

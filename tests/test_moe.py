@@ -31,8 +31,8 @@ def call(p, x=P, up=P, down=P, ids=P, weights=P, res=P + 4096, y=P + 4096, ws=P,
 
 
 BAD_PARAMS = [dict(dtype=2), dict(dtype_y=-1), dict(transw=2), dict(act=5), dict(act=-1), dict(gated=2), dict(tokens=-1),
-              dict(tokens=513), dict(hidden=-1), dict(hidden=(1 << 24) + 1, ldx=1 << 30), dict(inner=-1),
-              dict(inner=(1 << 24) + 1), dict(experts=-1), dict(experts=1025), dict(top=-1), dict(top=33), dict(ldx=63),
+              dict(tokens=513), dict(hidden=-1), dict(hidden=(1 << 22) + 1, ldx=1 << 30, ldy=1 << 30, ldr=1 << 30, lddown=1 << 23, stride_up=1 << 40, stride_down=1 << 40), dict(inner=-1),
+              dict(inner=(1 << 22) + 1, ldup=1 << 24, stride_up=1 << 40, stride_down=1 << 40), dict(ldup=(1 << 24) + 1, stride_up=1 << 40), dict(experts=-1), dict(experts=1025), dict(top=-1), dict(top=33), dict(ldx=63),
               dict(ldy=63), dict(ldup=95), dict(lddown=63), dict(transw=1, ldup=63), dict(transw=1, ldup=64, lddown=47),
               dict(stride_up=64 * 96 - 1), dict(stride_down=48 * 64 - 1), dict(ldx=(1 << 40) + 1)]
 
@@ -54,7 +54,7 @@ def test_bad_arguments():
     assert call(params(ldr=65)) == BAD      # in place with another pitch
     assert call(None) == BAD and dg.gemm_moe_layer_workspace_size(None) == BAD
     # more blocks than a launch holds
-    wide = dict(inner=1 << 24, ldup=1 << 25, stride_up=1 << 31, stride_down=1 << 30, tokens=512, experts=1024, top=32)
+    wide = dict(inner=1 << 22, ldup=1 << 23, stride_up=1 << 31, stride_down=1 << 30, tokens=512, experts=1024, top=32)
     assert call(params(**wide)) == BAD and dg.gemm_moe_layer_workspace_size(params(**wide)) == BAD
 
 
