@@ -118,7 +118,8 @@ from .layers import (  # noqa: E402,F401
     grouped_linear_grad, linear, linear_grad)
 from .layers import SIGNATURES as _LINEAR_SIGNATURES  # noqa: E402
 from .serving import (  # noqa: E402,F401
-    LogProbs, LogProbsParams, MoeParams, gemm_log_probs, gemm_log_probs_grad, gemm_log_probs_workspace_size,
+    AdapterParams, LogProbs, LogProbsParams, MoeParams, adapter_linear, gemm_adapter_linear,
+    gemm_adapter_linear_workspace_size, gemm_log_probs, gemm_log_probs_grad, gemm_log_probs_workspace_size,
     gemm_moe_layer, gemm_moe_layer_workspace_size, log_probs, log_probs_grad, moe_layer)
 from .serving import SIGNATURES as _SERVING_SIGNATURES  # noqa: E402
 

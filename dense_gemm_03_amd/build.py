@@ -33,7 +33,8 @@ SOURCES = [("gemm_api.hip", "gemm_api", []),
            ("linear_rows.hip", "linear_rows", []),
            ("serving_api.hip", "serving_api", []),
            ("log_probs.hip", "log_probs", []),
-           ("moe.hip", "moe", [])]
+           ("moe.hip", "moe", []),
+           ("adapter.hip", "adapter", [])]
 for _dtype in ("F32", "BF16"):
     for _layout in ("NN", "NT", "TN", "TT", "CF", "CW", "CFT", "CWT", "C3F", "C3W", "CFP", "CWP",
                     "C3FP", "C3WP", "CFW", "CWW", "C4F", "C4W", "C4FP", "C4WP"):
@@ -42,7 +43,12 @@ for _dtype in ("F32", "BF16"):
     # the linear layers: w as K x N, as N x K, and the weight gradient
     for _form in ("N", "T", "W"):
         SOURCES.append(("linear_instances.hip", "linear_%s_%s" % (_dtype.lower(), _form.lower()),
-                        ["DG_LIN_TABLE=DG_LIN_%s_TABLE" % _dtype, "DG_LIN_FORM=" + _form]))
+                        ["DG_LIN_TABLE=DG_LIN_%s_TABLE" % _dtype, "DG_LIN_FORM=" + _form,
+                         "DG_LIN_ARGS=LinearArgs"]))
+    for _form in ("N", "T"):    # with an adapter per row
+        SOURCES.append(("linear_instances.hip", "adapted_%s_%s" % (_dtype.lower(), _form.lower()),
+                        ["DG_LIN_TABLE=DG_LIN_%s_TABLE" % _dtype, "DG_LIN_FORM=" + _form,
+                         "DG_LIN_ARGS=AdaptedArgs"]))
 
 ARCH = "gfx950"
 HIPCC_FLAGS = [

@@ -9,6 +9,7 @@
 #include "gemm_internal.hpp"
 #include "gemm_linear.h"
 #include "linear_configs.hpp"
+#include "serving.hpp"
 
 namespace dg {
 namespace {
@@ -278,7 +279,9 @@ int copy_rows(const void **m, int64_t *ld, int64_t rows, int64_t cols, int64_t p
     return GEMM_OK;
 }
 
-int launch_plan(const Plan &pl, int dtype, LinearArgs &a, bool wgrad, void *workspace, hipStream_t stream)
+// With `ad` (first two forms): an adapter per row.
+int launch_plan(const Plan &pl, int dtype, LinearArgs &a, bool wgrad, void *workspace, hipStream_t stream,
+                const AdapterArgs *ad = nullptr)
 {
     int count = 0;
     const LinearConfig &c = linear_configs(dtype, &count)[pl.cfg];
@@ -300,7 +303,10 @@ int launch_plan(const Plan &pl, int dtype, LinearArgs &a, bool wgrad, void *work
     a.ws = pl.splits > 1 ? static_cast<float *>(workspace) : nullptr;
     a.slots = (int)piece_slots(c, dtype, device_compute_units());
     const int64_t blocks = grid_blocks(pl.tiles_m, pl.tiles_n, wgrad, a.groups, a.rows, pl.splits, a.slots);
-    if (c.fn[pl.form][x16 && w16 ? 0 : 1](a, (int)blocks, stream) != hipSuccess) return GEMM_ERR_HIP;
+    const int odd = x16 && w16 ? 0 : 1;
+    const hipError_t err = ad != nullptr ? c.adapted[pl.form][odd](AdaptedArgs{a, *ad}, (int)blocks, stream)
+                                         : c.fn[pl.form][odd](a, (int)blocks, stream);
+    if (err != hipSuccess) return GEMM_ERR_HIP;
     if (pl.splits > 1 && launch_linear_reduce(a, wgrad, stream) != hipSuccess) return GEMM_ERR_HIP;
     return GEMM_OK;
 }
@@ -355,7 +361,8 @@ int need_device()
 
 int linear(const gemm_linear_params *p, const void *x, const void *w, const int32_t *offsets,
            const void *bias, const void *residual, void *pre, void *y, void *workspace,
-           int64_t workspace_bytes, hipStream_t stream)
+           int64_t workspace_bytes, hipStream_t stream, const AdapterArgs *ad = nullptr,
+           const AdapterDownArgs *down = nullptr)
 {
     if (!valid_sizes(p) || !valid_operands(p)) return GEMM_ERR_INVALID_ARG;
     const int64_t nrow = std::max<int64_t>(p->N, 1);
@@ -377,6 +384,7 @@ int linear(const gemm_linear_params *p, const void *x, const void *w, const int3
     if (!valid_workspace(workspace, workspace_bytes, empty ? 0 : pl.ws_bytes)) return GEMM_ERR_INVALID_ARG;
     if (empty) return GEMM_OK;
     if (const int rc = need_device()) return rc;
+    if (down && launch_adapter_down(*down, p->dtype == GEMM_DTYPE_BF16, stream) != hipSuccess) return GEMM_ERR_HIP;
     LinearArgs a{};
     a.x = x;
     a.w = w;
@@ -404,7 +412,7 @@ int linear(const gemm_linear_params *p, const void *x, const void *w, const int3
                        p->dtype_y == GEMM_DTYPE_BF16, p->dtype_bias == GEMM_DTYPE_BF16, 0};
     a.e.vec = aligned16(y, p->ldy, 0, p->dtype_y) && (!residual || aligned16(residual, p->ldr, 0, p->dtype_y)) &&
               (!pre || aligned16(pre, p->ldp, 0, p->dtype_y));
-    return launch_plan(pl, p->dtype, a, false, workspace, stream);
+    return launch_plan(pl, p->dtype, a, false, workspace, stream, ad);
 }
 
 int act_grad(const gemm_linear_params *p, const void *dy, int64_t lddy, const void *pre,
@@ -595,6 +603,14 @@ int grad(const gemm_linear_params *p, const gemm_linear_grad_outputs *o, const v
 }
 
 }  // namespace
+
+int linear_with_adapters(const gemm_linear_params *p, const AdapterDownArgs *down, const AdapterArgs *ad,
+                         const void *x, const void *w, const void *bias, const void *residual, void *y,
+                         void *workspace, int64_t workspace_bytes, hipStream_t stream)
+{
+    return linear(p, x, w, nullptr, bias, residual, nullptr, y, workspace, workspace_bytes, stream, ad, down);
+}
+
 }  // namespace dg
 
 extern "C" {

@@ -16,9 +16,10 @@
 namespace dg {
 
 typedef hipError_t (*linear_fn)(const LinearArgs &args, int blocks, hipStream_t stream);
+typedef hipError_t (*adapted_fn)(const AdaptedArgs &args, int blocks, hipStream_t stream);
 
-template <bool BF16, int FORM, int W, int WV>
-hipError_t launch_few_rows(const LinearArgs &args, int blocks, hipStream_t stream);
+template <bool BF16, int FORM, int W, int WV, class Args>
+hipError_t launch_few_rows(const Args &args, int blocks, hipStream_t stream);
 
 enum { FORM_N = 0, FORM_T = 1, FORM_WGRAD = 2 };
 
@@ -27,10 +28,11 @@ struct LinearConfig {
     float step, alone, block;
     int bm, bn, bk, threads, stages, group_m;   // stages == 0: the kernel for few rows
     linear_fn fn[3][2];   // by form; [0] aligned, [1] not; nullptr where there is none
+    adapted_fn adapted[2][2];   // the first two forms with an adapter per row
 };
 
-template <bool BF16, int BM, int BN, int BK, int WM, int WN, int STAGES, int LX, int LW, bool ALIGNED>
-hipError_t launch_linear(const LinearArgs &args, int blocks, hipStream_t stream);
+template <bool BF16, int BM, int BN, int BK, int WM, int WN, int STAGES, int LX, int LW, bool ALIGNED, class Args>
+hipError_t launch_linear(const Args &args, int blocks, hipStream_t stream);
 
 // how x and w (dz) lie in memory
 #define DG_LIN_LX_N ::dg::KMAJOR
@@ -73,22 +75,27 @@ hipError_t launch_linear(const LinearArgs &args, int blocks, hipStream_t stream)
 
 #define DG_LIN_FORM_ID_N 0
 #define DG_LIN_FORM_ID_T 1
-#define DG_LIN_ROWS_FN(BF16, F, W, WV)                     \
-    {&launch_few_rows<BF16, DG_LIN_FORM_ID_##F, W, WV>,    \
-     &launch_few_rows<BF16, DG_LIN_FORM_ID_##F, W, WV>}
-#define DG_LIN_ROWS_FNS_N(...) {DG_LIN_ROWS_FN(__VA_ARGS__), DG_LIN_NOFNS, DG_LIN_NOFNS}
-#define DG_LIN_ROWS_FNS_T(...) {DG_LIN_NOFNS, DG_LIN_ROWS_FN(__VA_ARGS__), DG_LIN_NOFNS}
+#define DG_LIN_ROWS_FN(ARGS, BF16, F, W, WV)                     \
+    {&launch_few_rows<BF16, DG_LIN_FORM_ID_##F, W, WV, ARGS>,    \
+     &launch_few_rows<BF16, DG_LIN_FORM_ID_##F, W, WV, ARGS>}
+#define DG_LIN_ROWS_FNS_N(...) {DG_LIN_ROWS_FN(LinearArgs, __VA_ARGS__), DG_LIN_NOFNS, DG_LIN_NOFNS}, \
+    {DG_LIN_ROWS_FN(AdaptedArgs, __VA_ARGS__), DG_LIN_NOFNS}
+#define DG_LIN_ROWS_FNS_T(...) {DG_LIN_NOFNS, DG_LIN_ROWS_FN(LinearArgs, __VA_ARGS__), DG_LIN_NOFNS}, \
+    {DG_LIN_NOFNS, DG_LIN_ROWS_FN(AdaptedArgs, __VA_ARGS__)}
 #define DG_LIN_ROWS_ENTRY(NAME, BF16, F, W, WV) \
     LinearConfig{NAME, 0, 0, 0, 16, 16 * (W), 1, 64 * (WV), 0, 1, DG_LIN_ROWS_FNS_##F(BF16, F, W, WV)},
 
-#define DG_LIN_FNS(BF16, BM, BN, BK, WM, WN, S, F)                                              \
-    {&launch_linear<BF16, BM, BN, BK, WM, WN, S, DG_LIN_LX_##F, DG_LIN_LW_##F, true>,           \
-     &launch_linear<BF16, BM, BN, BK, WM, WN, S, DG_LIN_LX_##F, DG_LIN_LW_##F, false>}
+#define DG_LIN_FNS(ARGS, BF16, BM, BN, BK, WM, WN, S, F)                                        \
+    {&launch_linear<BF16, BM, BN, BK, WM, WN, S, DG_LIN_LX_##F, DG_LIN_LW_##F, true, ARGS>,     \
+     &launch_linear<BF16, BM, BN, BK, WM, WN, S, DG_LIN_LX_##F, DG_LIN_LW_##F, false, ARGS>}
 #define DG_LIN_NOFNS {nullptr, nullptr}
 #define DG_LIN_ENTRY(NAME, BF16, BM, BN, BK, WM, WN, S, GM, STEP, ALONE, BLOCK)                 \
     LinearConfig{NAME, STEP, ALONE, BLOCK, BM, BN, BK, 64 * (WM) * (WN), S, GM,                 \
-                 {DG_LIN_FNS(BF16, BM, BN, BK, WM, WN, S, N), DG_LIN_FNS(BF16, BM, BN, BK, WM, WN, S, T), \
-                  DG_LIN_FNS(BF16, BM, BN, BK, WM, WN, S, W)}},
+                 {DG_LIN_FNS(LinearArgs, BF16, BM, BN, BK, WM, WN, S, N),                               \
+                  DG_LIN_FNS(LinearArgs, BF16, BM, BN, BK, WM, WN, S, T),                               \
+                  DG_LIN_FNS(LinearArgs, BF16, BM, BN, BK, WM, WN, S, W)},                              \
+                 {DG_LIN_FNS(AdaptedArgs, BF16, BM, BN, BK, WM, WN, S, N),                              \
+                  DG_LIN_FNS(AdaptedArgs, BF16, BM, BN, BK, WM, WN, S, T)}},
 
 const LinearConfig *linear_configs(int dtype, int *count);
 

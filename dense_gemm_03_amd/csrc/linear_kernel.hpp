@@ -11,6 +11,7 @@
 // an output matrix, and its blocks walk that group's rows only.
 #pragma once
 
+#include "linear_adapters.hpp"
 #include "linear_pieces.hpp"
 #include "mma16.hpp"
 
@@ -50,6 +51,11 @@ struct LinearArgs {
     int group_m;
     int direct_ok;
     int slots;              // compute units per XCD (for entries of one block per unit)
+};
+
+// The same with an adapter per row.
+struct AdaptedArgs : LinearArgs {
+    AdapterArgs ad;
 };
 
 // ------------------------------------------------------------- activations --
@@ -544,8 +550,8 @@ struct TileSpec {
 // operand is w (or dz), whose rows are output columns, the second x, whose rows
 // are output rows: G is the geometry of the transposed tile.  The stages are
 // the kernel's arrays, at least as large as G's.
-template <class G, bool ALIGNED>
-__device__ __forceinline__ void linear_tile(const LinearArgs &p, const TileSpec &t, unsigned char *lds0,
+template <class G, bool ALIGNED, class Args>
+__device__ __forceinline__ void linear_tile(const Args &p, const TileSpec &t, unsigned char *lds0,
                                             unsigned char *lds1, unsigned char *lds2, unsigned char *lds3)
 {
     using In = typename G::In;
@@ -647,6 +653,11 @@ __device__ __forceinline__ void linear_tile(const LinearArgs &p, const TileSpec 
         }
     }
 
+    if constexpr (std::is_same<Args, AdaptedArgs>::value) {
+        if (t.slice == 0)
+            add_adapters<G>(p.ad, c.lane, t.row0 + c.wcol * G::WTN, t.m, t.col0 + c.wrow * G::WTM, p.N, acc);
+    }
+
     const int out_rows = WGRAD ? p.M : t.m;   // rows of this group's output
     // the last readers of the stages have passed a barrier
     unsigned char *scr = StagedTile<G, 4>::share(lds0, lds1, __builtin_amdgcn_readfirstlane(wave));
@@ -700,8 +711,9 @@ __device__ __forceinline__ void linear_tile(const LinearArgs &p, const TileSpec 
 }
 
 // BM x BN output tile, WM x WN waves; LX and LW: how x and w (dz) lie in memory.
-template <bool BF16, int BM, int BN, int BK, int WM, int WN, int STAGES, int LX, int LW, bool ALIGNED>
-__global__ void __launch_bounds__(64 * WM * WN) linear_kernel(LinearArgs p)
+template <bool BF16, int BM, int BN, int BK, int WM, int WN, int STAGES, int LX, int LW, bool ALIGNED,
+          class Args = LinearArgs>
+__global__ void __launch_bounds__(64 * WM * WN) linear_kernel(Args p)
 {
     using G = typename std::conditional<BF16, Geo16<BN, BM, BK, WN, WM, STAGES, LW, LX>,
                                         Geo<BF16, BN, BM, BK, WN, WM, STAGES, LW, LX>>::type;
@@ -944,8 +956,8 @@ struct FewRows {
     }
 };
 
-template <bool BF16, int FORM, int W, int WV>
-__global__ void __launch_bounds__(64 * WV) few_rows_kernel(LinearArgs p)
+template <bool BF16, int FORM, int W, int WV, class Args = LinearArgs>
+__global__ void __launch_bounds__(64 * WV) few_rows_kernel(Args p)
 {
     using F = FewRows<BF16, FORM, W, WV>;
     using In = typename F::In;
@@ -980,6 +992,31 @@ __global__ void __launch_bounds__(64 * WV) few_rows_kernel(LinearArgs p)
         f.template run<false>(wave, acc);
     else
         f.template run<true>(wave, acc);
+
+    if constexpr (std::is_same<Args, AdaptedArgs>::value) {
+        // the waves take the adapters of the rows in turn
+        using Op = AdapterOperand<BF16>;
+        const int id = f.c < count ? adapter_of_row(p.ad, row0 + f.c) : -1;
+        int turn = 0;
+        for (uint64_t left = __ballot(id >= 0); left != 0; turn = turn + 1 == WV ? 0 : turn + 1) {
+            const int e = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
+            left &= ~__ballot(id == e);
+            if (turn != wave) continue;
+            const In *b = static_cast<const In *>(p.ad.b) + e * p.ad.stride_b;
+            for (int k0 = 0; k0 < p.ad.rank; k0 += 4 * F::KV) {
+                const int k = k0 + f.q * F::KV;
+                u32x4 hi, lo;
+                Op::load_t(p.ad, id == e, row0 + f.c, k, hi, lo);
+#pragma unroll
+                for (int j = 0; j < W; ++j) {
+                    const int col = F::T ? f.n0 + 16 * j + f.c : f.first_col() + j;
+                    const u32x4 v = Op::load(b + (int64_t)min(col, p.N - 1) * p.ad.ldb, k, p.ad.rank);
+                    F::mma(hi, v, acc[j]);
+                    if constexpr (BF16) F::mma(lo, v, acc[j]);
+                }
+            }
+        }
+    }
 
     // sum r of a 16 x 16 fragment is row 4 q + r, column c
 #pragma unroll

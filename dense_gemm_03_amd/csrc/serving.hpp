@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "gemm_linear.h"
 #include "linear_kernel.hpp"
 
 namespace dg {
@@ -67,5 +68,25 @@ struct MoePlan {
 int moe_strip_up(bool transw, bool gated, bool wide);
 int moe_strip_down(bool transw, bool many, bool wide);
 hipError_t launch_moe(const MoeArgs &args, const MoePlan &plan, bool bf16, bool transw, hipStream_t stream);
+
+// t = scale x . a^T of each row's adapter, as AdapterArgs has it.
+struct AdapterDownArgs {
+    const void *x, *a;           // a: per adapter rank x K
+    const int32_t *ids;
+    const float *scales;         // or nullptr: 1
+    float *t;
+    int64_t ldx, lda, stride_a, t_part;
+    int rows, K, count, rank, pitch;
+    int parts, part_k;           // parts of K, of part_k values
+    int slots;                   // blocks per 64 rows and part: each takes every slots-th adapter of the rows
+};
+hipError_t launch_adapter_down(const AdapterDownArgs &args, bool bf16, hipStream_t stream);
+
+// gemm_linear with an adapter per row (linear_api.hip): launch_adapter_down(*down) once
+// the arguments are checked, then the layer with *ad.  Both nullptr: the layer alone.
+// Returns a gemm_status.
+int linear_with_adapters(const gemm_linear_params *p, const AdapterDownArgs *down, const AdapterArgs *ad,
+                         const void *x, const void *w, const void *bias, const void *residual, void *y,
+                         void *workspace, int64_t workspace_bytes, hipStream_t stream);
 
 }  // namespace dg

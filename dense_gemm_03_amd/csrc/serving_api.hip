@@ -129,6 +129,7 @@ int log_probs_grad(const gemm_log_probs_params *p, const void *logits, const int
 // ---------------------------------------------------- mixture of experts --
 
 constexpr int64_t kMaxWidth = int64_t(1) << 22;
+constexpr int64_t kMaxRank = 4096;
 constexpr int64_t kMaxWeightLd = int64_t(1) << 24;   // byte offsets inside a strip stay below 2^32
 
 int64_t up_columns(const gemm_moe_params &p) { return p.gated ? 2 * p.inner : p.inner; }
@@ -270,6 +271,127 @@ int moe_layer(const gemm_moe_params *p, const void *x, const void *up, const voi
                : GEMM_ERR_HIP;
 }
 
+// ------------------------------------------------------ low-rank adapters --
+
+bool valid(const gemm_adapter_params *p)
+{
+    if (p == nullptr || !known(p->dtype) || !known(p->dtype_y) || !known(p->dtype_bias) ||
+        (p->transw != GEMM_OP_N && p->transw != GEMM_OP_T) || p->act < GEMM_ACT_NONE || p->act > GEMM_ACT_SILU ||
+        !in_range(p->rows) || !in_range(p->N) || !in_range(p->K) || !in_range(p->adapters) || p->rank < 0 ||
+        p->rank > kMaxRank)
+        return false;
+    if (!valid_ld(p->lda, p->K) || p->lda > kMaxWeightLd || !valid_ld(p->ldb, p->rank)) return false;
+    // the adapters do not overlap
+    return p->adapters <= 1 || p->rank == 0 ||
+           ((p->K == 0 || p->stride_a >= (p->rank - 1) * p->lda + p->K) &&
+            (p->N == 0 || p->stride_b >= (p->N - 1) * p->ldb + p->rank));
+}
+
+gemm_linear_params layer_of(const gemm_adapter_params &p)
+{
+    gemm_linear_params q{};
+    q.dtype = p.dtype;
+    q.dtype_y = p.dtype_y;
+    q.dtype_bias = p.dtype_bias;
+    q.transw = p.transw;
+    q.act = p.act;
+    q.alpha = 1.0f;
+    q.rows = p.rows;
+    q.N = p.N;
+    q.K = p.K;
+    q.ldx = p.ldx;
+    q.ldw = p.ldw;
+    q.ldy = p.ldy;
+    q.ldr = p.ldr;
+    return q;
+}
+
+struct AdapterShares {
+    bool any;                  // a row may have an adapter that adds something
+    int pitch, parts, part_k, slots;
+    int64_t t_bytes, total;    // total < 0: the layer's error
+    bool launchable;
+};
+
+AdapterShares shares_of(const gemm_adapter_params &p)
+{
+    AdapterShares s{};
+    const gemm_linear_params q = layer_of(p);
+    const int64_t layer = gemm_linear_workspace_size(&q);
+    s.any = p.rows > 0 && p.N > 0 && p.K > 0 && p.rank > 0 && p.adapters > 0;
+    s.launchable = true;
+    if (layer < 0) {
+        s.total = layer;
+        return s;
+    }
+    s.parts = s.slots = 1;
+    s.part_k = (int)p.K;
+    s.pitch = (int)(ceil_div(p.rank, 8) * 8);
+    if (s.any && p.K >= 8) {
+        // A block per adapter of 64 rows (one after another where rows are many), and
+        // parts of K until there are blocks for all units; a wave has one step of 64 at
+        // least, and every tile of the product adds up the parts.
+        const int64_t groups = ceil_div(p.rows, 64), cus = device_compute_units();
+        s.slots = (int)std::max<int64_t>(1, std::min(std::min<int64_t>(p.adapters, std::min<int64_t>(p.rows, 64)),
+                                                     ceil_div(cus, groups)));
+        const int64_t want = std::min<int64_t>(std::min<int64_t>(8, ceil_div(cus, groups * s.slots)), ceil_div(p.K, 8 * 64));
+        s.part_k = (int)(ceil_div(ceil_div(p.K, want), 64) * 64);
+        s.parts = (int)ceil_div(p.K, s.part_k);
+        s.launchable = groups * s.slots * s.parts <= int64_t(UINT32_MAX) / 512;
+    }
+    s.t_bytes = s.any ? s.parts * p.rows * s.pitch * 4 : 0;   // whole 16 bytes
+    s.total = s.t_bytes + layer;
+    return s;
+}
+
+int adapter_linear(const gemm_adapter_params *p, const void *x, const void *w, const void *a, const void *b,
+                   const int32_t *ids, const float *scales, const void *bias, const void *residual, void *y,
+                   void *workspace, int64_t workspace_bytes, hipStream_t stream)
+{
+    if (!valid(p)) return GEMM_ERR_INVALID_ARG;
+    const AdapterShares s = shares_of(*p);
+    if (s.total < 0 || !s.launchable || !valid_workspace(workspace, workspace_bytes, s.total)) return GEMM_ERR_INVALID_ARG;
+    const int es = size_of(p->dtype);
+    if ((s.any && (!x || !a || !b || !ids)) || misaligned(x, es) || misaligned(a, es) || misaligned(b, es) ||
+        misaligned(ids, 4) || misaligned(scales, 4))
+        return GEMM_ERR_INVALID_ARG;
+    const gemm_linear_params q = layer_of(*p);
+    char *scratch = static_cast<char *>(workspace);
+    void *rest = s.total > s.t_bytes ? scratch + s.t_bytes : nullptr;
+    if (!s.any)
+        return linear_with_adapters(&q, nullptr, nullptr, x, w, bias, residual, y, rest, s.total - s.t_bytes, stream);
+    AdapterDownArgs d{};
+    d.x = x;
+    d.a = a;
+    d.ids = ids;
+    d.scales = scales;
+    d.t = static_cast<float *>(workspace);
+    d.ldx = p->ldx;
+    d.lda = p->lda;
+    d.stride_a = p->adapters > 1 ? p->stride_a : 0;
+    d.t_part = p->rows * s.pitch;
+    d.rows = (int)p->rows;
+    d.K = (int)p->K;
+    d.count = (int)p->adapters;
+    d.rank = (int)p->rank;
+    d.pitch = s.pitch;
+    d.parts = s.parts;
+    d.part_k = s.part_k;
+    d.slots = s.slots;
+    AdapterArgs ad{};
+    ad.t = d.t;
+    ad.b = b;
+    ad.ids = ids;
+    ad.ldb = p->ldb;
+    ad.stride_b = p->adapters > 1 ? p->stride_b : 0;
+    ad.t_part = d.t_part;
+    ad.count = d.count;
+    ad.rank = d.rank;
+    ad.pitch = s.pitch;
+    ad.parts = s.parts;
+    return linear_with_adapters(&q, &d, &ad, x, w, bias, residual, y, rest, s.total - s.t_bytes, stream);
+}
+
 }  // namespace
 }  // namespace dg
 
@@ -288,6 +410,20 @@ int gemm_moe_layer(const gemm_moe_params *p, const void *x, const void *w_up, co
                    hipStream_t stream)
 {
     return dg::moe_layer(p, x, w_up, w_down, ids, weights, residual, y, workspace, workspace_bytes, stream);
+}
+
+int64_t gemm_adapter_linear_workspace_size(const gemm_adapter_params *p)
+{
+    if (!dg::valid(p)) return GEMM_ERR_INVALID_ARG;
+    const dg::AdapterShares s = dg::shares_of(*p);
+    return s.launchable ? s.total : GEMM_ERR_INVALID_ARG;
+}
+
+int gemm_adapter_linear(const gemm_adapter_params *p, const void *x, const void *w, const void *a, const void *b,
+                        const int32_t *ids, const float *scales, const void *bias, const void *residual, void *y,
+                        void *workspace, int64_t workspace_bytes, hipStream_t stream)
+{
+    return dg::adapter_linear(p, x, w, a, b, ids, scales, bias, residual, y, workspace, workspace_bytes, stream);
 }
 
 int64_t gemm_log_probs_workspace_size(const gemm_log_probs_params *p)

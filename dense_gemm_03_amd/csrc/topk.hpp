@@ -8,6 +8,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "strip.hpp"
+
 namespace dg {
 
 // Bits of v in the order of the numbers; -0 as +0, NaN as -infinity.
@@ -103,13 +105,6 @@ __device__ __forceinline__ uint64_t merged(uint64_t a, uint64_t b)
 {
     const uint64_t r = key_xor_lane<63>(b);
     return exchanged<32, 64>(a > r ? a : r);
-}
-
-// LDS accesses of this wave before and after stay in their order.
-__device__ __forceinline__ void wave_order()
-{
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
 }
 
 struct TopList {

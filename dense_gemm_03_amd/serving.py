@@ -1,7 +1,7 @@
 """What stands around a model's products when it answers, over torch tensors:
-``moe_layer`` (a whole mixture-of-experts layer for a few tokens), ``log_probs`` (log
-probabilities of given tokens, entropy, alternatives) and its gradient
-``log_probs_grad``; a thin binding over ``include/gemm_serving.h``.  Like
+``moe_layer`` (a whole mixture-of-experts layer for a few tokens), ``adapter_linear``
+(``linear`` with a low-rank adapter per row), ``log_probs`` (log probabilities of given
+tokens, entropy, alternatives) and its gradient ``log_probs_grad``; a thin binding over ``include/gemm_serving.h``.  Like
 the rest of the package they take no part in torch's autograd.  The C entry points
 are here under their own names (``gemm_*``), taking parameters, device pointers and
 a stream."""
@@ -29,12 +29,22 @@ class MoeParams(ctypes.Structure):
             "stride_down")]
 
 
+class AdapterParams(ctypes.Structure):
+    """gemm_adapter_params of include/gemm_serving.h."""
+    _fields_ = [(name, ctypes.c_int32) for name in ("dtype", "dtype_y", "dtype_bias", "transw", "act", "reserved")] + \
+        [(name, ctypes.c_int64) for name in (
+            "rows", "N", "K", "adapters", "rank", "ldx", "ldw", "ldy", "ldr", "lda", "ldb", "stride_a", "stride_b")]
+
+
 _plp = ctypes.POINTER(LogProbsParams)
 _pmoe = ctypes.POINTER(MoeParams)
+_pad = ctypes.POINTER(AdapterParams)
 # Every symbol include/gemm_serving.h declares, with its ctypes signature.
 SIGNATURES = {
     "gemm_moe_layer_workspace_size": (_i64, [_pmoe]),
     "gemm_moe_layer": (_int, [_pmoe] + [_p] * 8 + [_i64, _p]),
+    "gemm_adapter_linear_workspace_size": (_i64, [_pad]),
+    "gemm_adapter_linear": (_int, [_pad] + [_p] * 10 + [_i64, _p]),
     "gemm_log_probs_workspace_size": (_i64, [_plp]),
     "gemm_log_probs": (_int, [_plp] + [_p] * 8 + [_i64, _p]),
     "gemm_log_probs_grad": (_int, [_plp] + [_p] * 7 + [_i64, _p]),
@@ -50,6 +60,16 @@ def gemm_moe_layer_workspace_size(params) -> int:
 def gemm_moe_layer(params, x, w_up, w_down, ids, weights, residual, y, workspace, workspace_bytes, stream=None) -> int:
     return _library().gemm_moe_layer(params, x, w_up, w_down, ids, weights, residual, y, workspace, workspace_bytes,
                                      stream)
+
+
+def gemm_adapter_linear_workspace_size(params) -> int:
+    return _library().gemm_adapter_linear_workspace_size(params)
+
+
+def gemm_adapter_linear(params, x, w, a, b, ids, scales, bias, residual, y, workspace, workspace_bytes,
+                        stream=None) -> int:
+    return _library().gemm_adapter_linear(params, x, w, a, b, ids, scales, bias, residual, y, workspace,
+                                          workspace_bytes, stream)
 
 
 def gemm_log_probs_workspace_size(params) -> int:
@@ -149,6 +169,67 @@ def moe_layer(x, w_up, w_down, ids, weights, act="silu", residual=None, *, gated
         rc = lib.gemm_moe_layer(params, x.data_ptr(), w_up.data_ptr(), w_down.data_ptr(), ids_ptr, weights_ptr,
                                 residual.data_ptr() if residual is not None else None, out.data_ptr(), ws_ptr, need,
                                 at.stream)
+    finally:
+        at.done()
+    _status(rc)
+    return out
+
+
+def adapter_linear(x, w, a, b, ids, scales=None, bias=None, act="none", residual=None, *, transb=False, out=None,
+                   out_dtype=None, stream=None):
+    """``linear`` with a low-rank adapter per row, for the rows of many requests:
+
+        y = act(x . w + bias + scales[i] (x . a[i]^T) . b[i]^T) + residual,  i = ids[row]
+
+    x (M x K), w (K x N, or N x K with ``transb``), ``a`` (adapters x rank x K) and ``b``
+    (adapters x N x rank) are all float32 or all bfloat16 with contiguous rows; ``ids``
+    is a contiguous int32 tensor of M numbers on the GPU, read there only, in any order;
+    one outside the adapters leaves its row without one.  ``scales`` (float32, one per
+    adapter) is 1 if not given.  The rest as in ``linear``."""
+    _torch()
+    t = layers.torch
+    if x.dim() != 2 or w.dim() != 2 or a.dim() != 3 or b.dim() != 3:
+        raise ValueError("x and w must be 2-D, a and b 3-D (adapters first)")
+    device = x.device
+    if device.type != "cuda":
+        raise ValueError("x must be a GPU tensor")
+    if w.device != device or a.device != device or b.device != device:
+        raise ValueError("x, w, a and b must be on the same GPU")
+    if w.dtype != x.dtype or a.dtype != x.dtype or b.dtype != x.dtype:
+        raise TypeError("x, w, a and b must all be float32 or all bfloat16")
+    dtype, act = _code(x.dtype, "x"), _activation(act)
+    rows, K = x.shape
+    K2, N, ldw, _ = _weights(w, 0, transb)
+    count, rank = a.shape[0], a.shape[1]
+    if K2 != K or tuple(a.shape) != (count, rank, K) or tuple(b.shape) != (count, N, rank):
+        raise ValueError("sizes differ: x is %dx%d, w takes %d inputs to %d, a is %s, b is %s"
+                         % (rows, K, K2, N, tuple(a.shape), tuple(b.shape)))
+    _, _, lda, stride_a = _weights(a, count, False)
+    _, _, ldb, stride_b = _weights(b, count, False)
+    ids_ptr = _vector(ids, (rows,), t.int32, device, "ids")
+    scales_ptr = _vector(scales, (count,), t.float32, device, "scales") if scales is not None else None
+    if out_dtype is None:
+        out_dtype = out.dtype if out is not None else t.float32
+    dtype_y = _code(out_dtype, "y")
+    ldr = _matrix(residual, rows, N, out_dtype, device, "residual") if residual is not None else 0
+    dtype_bias = 0
+    if bias is not None:
+        dtype_bias = _code(bias.dtype, "bias")
+        _vector(bias, (N,), bias.dtype, device, "bias")
+    ldy = _matrix(out, rows, N, out_dtype, device, "out") if out is not None else max(N, 1)
+    params = _block(AdapterParams, dtype, dtype_y, dtype_bias, 1 if transb else 0, act, 0, rows, N, K, count, rank,
+                    _pitch(x, rows, K, "x"), ldw, ldy, ldr, lda, ldb, stride_a, stride_b)
+    at = _Launch(device, stream)
+    try:
+        lib = _library()
+        need = lib.gemm_adapter_linear_workspace_size(params)
+        ws, ws_ptr = at.scratch(need)
+        if out is None:
+            out = at.empty((rows, N), out_dtype)
+        rc = lib.gemm_adapter_linear(params, x.data_ptr(), w.data_ptr(), a.data_ptr(), b.data_ptr(), ids_ptr, scales_ptr,
+                                     bias.data_ptr() if bias is not None else None,
+                                     residual.data_ptr() if residual is not None else None, out.data_ptr(), ws_ptr,
+                                     need, at.stream)
     finally:
         at.done()
     _status(rc)

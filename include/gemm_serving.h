@@ -1,7 +1,8 @@
 /*
  * What stands around the products of a model that answers, on one MI355X
- * (gfx950): a whole mixture-of-experts layer for a few tokens; log probabilities
- * of given tokens with entropy and alternatives, and their gradient.
+ * (gfx950): a whole mixture-of-experts layer for a few tokens; a linear layer
+ * with a low-rank adapter per row; log probabilities of given tokens with entropy
+ * and alternatives, and their gradient.
  *
  * Memory: every pointer is a device pointer of the caller's, aligned to its
  * element; outputs must not overlap inputs or one another, except where an
@@ -72,6 +73,48 @@ int64_t gemm_moe_layer_workspace_size(const gemm_moe_params *params);
 int gemm_moe_layer(const gemm_moe_params *params, const void *x, const void *w_up, const void *w_down,
                    const int32_t *ids, const float *weights, const void *residual, void *y,
                    void *workspace, int64_t workspace_bytes, hipStream_t stream);
+
+/* ------------------------------------------------------ low-rank adapters --
+ *
+ * gemm_linear for the rows of many requests, each with a low-rank adapter of its
+ * own beside the shared weights:
+ *
+ *     z = x . w + bias + scales[i] (x . a_i^T) . b_i^T      i = ids[row]
+ *     y = act(z) + residual
+ *
+ * ids is int32, one per row, on the device and read by the kernels alone, in any
+ * order (rows of a request side by side are fastest); an id outside 0 ..
+ * adapters-1 leaves its row without an adapter.  a_i is rank x K and b_i N x rank,
+ * row-major, stride_a and stride_b elements apart.  Adapters of a lower rank have
+ * zeros in the rest.  scales (fp32, one per adapter) may be NULL: 1.
+ *
+ * Precision as in gemm_linear; x . a^T is formed in fp32 and kept to 16 bits of
+ * mantissa (bf16 operands) or as it is (fp32) for the second product.
+ *
+ * Limits: rank at most 4096, lda at most 2^24.  gemm_linear_force_config holds
+ * for these calls, too.
+ */
+typedef struct {
+    int32_t dtype;       /* of x, w, a and b: GEMM_DTYPE_F32 or GEMM_DTYPE_BF16 */
+    int32_t dtype_y;     /* of y and residual */
+    int32_t dtype_bias;
+    int32_t transw;      /* GEMM_OP_N: w is K x N; GEMM_OP_T: w is N x K */
+    int32_t act;         /* gemm_act */
+    int32_t reserved;    /* 0 */
+    int64_t rows, N, K;
+    int64_t adapters, rank;
+    int64_t ldx, ldw, ldy, ldr;            /* x, w, y, residual */
+    int64_t lda, ldb;                      /* a, b */
+    int64_t stride_a, stride_b;            /* elements between consecutive adapters */
+} gemm_adapter_params;
+
+int64_t gemm_adapter_linear_workspace_size(const gemm_adapter_params *params);
+
+/* bias and residual may be NULL; residual may be y itself with ldr == ldy. */
+int gemm_adapter_linear(const gemm_adapter_params *params, const void *x, const void *w, const void *a,
+                        const void *b, const int32_t *ids, const float *scales, const void *bias,
+                        const void *residual, void *y, void *workspace, int64_t workspace_bytes,
+                        hipStream_t stream);
 
 /* ------------------------------------------------------ log probabilities --
  *

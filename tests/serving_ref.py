@@ -146,3 +146,41 @@ def moe_layer(x, up, down, ids, weights, act, residual, gated, transb, out_dtype
         err = err + U * (y.abs() + r.abs())
     hs = half_step(out_dtype)
     return y, err + hs * (y.abs() + err) + 1e-37
+
+
+def adapter_linear(x, w, a, b, ids, scales, bias, act, residual, transb, out_dtype):
+    """(value, bound) of the layer with adapters, float64 on the CPU.
+
+    t = scale x . a^T is off by sum_bound(K) of its magnitudes, a rounding for the
+    scale and one per part of K (8 at most); bf16 products read it as two bf16 values,
+    which keep 2^-16 of it.  The layer's sum has K + rank terms."""
+    x64 = x.cpu().double()
+    w64 = (w.T if transb else w).cpu().double()
+    z, s = x64 @ w64, x64.abs() @ w64.abs()
+    carried = torch.zeros_like(z)     # t's error through b
+    keep = 2.0 ** -16 if x.dtype == torch.bfloat16 else 0.0
+    ids = ids.cpu().long()
+    for i in range(a.shape[0]):
+        rows = torch.nonzero(ids == i)[:, 0]
+        if rows.numel() == 0:
+            continue
+        a64, b64 = a[i].cpu().double(), b[i].cpu().double()
+        f = float(scales[i]) if scales is not None else 1.0
+        t, m = f * (x64[rows] @ a64.T), abs(f) * (x64[rows].abs() @ a64.abs().T)
+        terr = (sum_bound(x.shape[1]) + 10 * U) * m + keep * t.abs()
+        z[rows] += t @ b64.T
+        s[rows] += (t.abs() + terr) @ b64.abs().T
+        carried[rows] = terr @ b64.abs().T
+    err = carried + sum_bound(x.shape[1] + 2 * a.shape[1]) * s
+    if bias is not None:
+        v = bias.cpu().double()
+        z = z + v
+        err = err + U * (s + v.abs())
+    y = act64(z, act)
+    err = 1.13 * err + (act_bound(z) if act not in ("none", "relu") else 0)
+    if residual is not None:
+        r = residual.cpu().double()
+        y = y + r
+        err = err + U * (y.abs() + r.abs())
+    hs = half_step(out_dtype)
+    return y, err + hs * (y.abs() + err) + 1e-37
