@@ -5,10 +5,14 @@
 // The ranks are a few k-steps more, so they cost the product little as MFMAs, but a
 // tile may hold rows of several adapters: it goes through the adapters of its rows, each
 // with the rows of t that are not its own as zeros.  Rows of a request lie together, so
-// that is one or two adapters for most tiles.
+// that is one or two adapters for most tiles; where every row has another one, what
+// counts is how many of their b are on the way at a time.
 //
-// t is in fp32; bf16 products read it as a sum of two bf16 values (16 bits of it: two
-// MFMAs instead of one, on the few steps that the ranks take).
+// Measured: 4096 rows of 8 requests, 4096 x 8192, rank 64: 238 us for this, 213 without
+// adapters; 1 row, 4096 x 4096, rank 16: 9.4 us and 7.6.
+//
+// bf16 products read t as a sum of two bf16 values (16 bits of it: two MFMAs instead
+// of one, on the few steps that the ranks take).
 #pragma once
 
 #include "mma16.hpp"
@@ -16,24 +20,32 @@
 namespace dg {
 
 struct AdapterArgs {
-    const float *t;         // parts x rows x pitch: sums over parts of k
+    const void *t;          // rows x pitch; bf16: the upper halves, and `plane` elements on the lower ones
     const void *b;          // per adapter N x rank
     const int32_t *ids;     // per row; outside 0 .. count-1: none
     int64_t ldb, stride_b;
-    int64_t t_part;         // elements between parts
-    int count, rank, pitch, parts;
+    int64_t plane;
+    int count, rank, pitch; // pitch: whole 16 bytes
+    // parts > 0: t is not formed yet, but the fp32 sums of parts of K, `plane` elements apart
+    // (a few rows, for which a launch costs more than adding them up where they are used;
+    // kernels of tiles larger than 64 x 64 have no registers for that)
+    int parts;
 };
 
-// KV values of k from e0 of a row, zero from `end` on; loads at the element's alignment.
+constexpr int ADAPTER_MAX_PARTS = 8;
+
+// KV values of k from e0 of a row, zero from `end` on.
 template <bool BF16>
 struct AdapterOperand {
     using In = typename std::conditional<BF16, uint16_t, float>::type;
-    static constexpr int KV = BF16 ? 8 : 4;
+    static constexpr int KV = BF16 ? 8 : 4, PLANES = BF16 ? 2 : 1;
     typedef In chunk __attribute__((ext_vector_type(KV), aligned(sizeof(In))));
 
+    // b, at the element's alignment
     static __device__ __forceinline__ u32x4 load(const In *row, int e0, int end)
     {
         if (e0 + KV <= end) return __builtin_bit_cast(u32x4, *reinterpret_cast<const chunk *>(row + e0));
+        if (e0 >= end) return u32x4{0, 0, 0, 0};
         union {
             u32x4 v;
             In e[KV];
@@ -42,100 +54,189 @@ struct AdapterOperand {
         for (int i = 0; i < KV; ++i) u.e[i] = e0 + i < end ? row[e0 + i] : In(0);
         return u.v;
     }
-    // The same of t's row, where `mine`, in two terms (fp32: the first is all).
-    static __device__ __forceinline__ void load_t(const AdapterArgs &p, bool mine, int64_t row, int e0, u32x4 &hi, u32x4 &lo)
+    // The same from parts.
+    static __device__ __forceinline__ void load_parts(const AdapterArgs &p, bool has, int64_t row, int e0, u32x4 (&v)[PLANES])
     {
-        float v[KV];
+        const float *t = static_cast<const float *>(p.t) + row * p.pitch + e0;
+        float sum[KV];
 #pragma unroll
-        for (int i = 0; i < KV; ++i) v[i] = 0.0f;
-        if (mine && e0 < p.rank) {   // the pitch covers whole chunks
-            for (int z = 0; z < p.parts; ++z) {
-                const float *t = p.t + z * p.t_part + row * p.pitch + e0;
+        for (int i = 0; i < KV; ++i) sum[i] = 0.0f;
+        if (has && e0 < p.rank) {
+            // all on the way together; behind the last part, that one again
+            u32x4 w[ADAPTER_MAX_PARTS][KV / 4];
 #pragma unroll
-                for (int h = 0; h < KV; h += 4) {
-                    const u32x4 w = load16(t + h);
+            for (int z = 0; z < ADAPTER_MAX_PARTS; ++z)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) v[h + i] += e0 + h + i < p.rank ? __uint_as_float(w[i]) : 0.0f;
-                }
-            }
+                for (int h = 0; h < KV / 4; ++h) w[z][h] = load16(t + min(z, p.parts - 1) * p.plane + 4 * h);
+#pragma unroll
+            for (int z = 0; z < ADAPTER_MAX_PARTS; ++z)
+#pragma unroll
+                for (int i = 0; i < KV; ++i)
+                    sum[i] += z < p.parts && e0 + i < p.rank ? __uint_as_float(w[z][i / 4][i % 4]) : 0.0f;
         }
 #pragma unroll
         for (int d = 0; d < 4; ++d) {
             if constexpr (BF16) {
-                const uint32_t w = f32x2_to_bf16x2_rne(v[2 * d], v[2 * d + 1]);
-                const float r0 = v[2 * d] - __uint_as_float(w << 16), r1 = v[2 * d + 1] - __uint_as_float(w & 0xFFFF0000u);
+                const uint32_t w = f32x2_to_bf16x2_rne(sum[2 * d], sum[2 * d + 1]);
+                const float a = sum[2 * d] - __uint_as_float(w << 16), b = sum[2 * d + 1] - __uint_as_float(w & 0xFFFF0000u);
                 const float inf = __builtin_inff();   // which leaves nothing for the second term
-                hi[d] = w;
-                lo[d] = f32x2_to_bf16x2_rne(fabsf(r0) < inf ? r0 : 0.0f, fabsf(r1) < inf ? r1 : 0.0f);
+                v[0][d] = w;
+                v[PLANES - 1][d] = f32x2_to_bf16x2_rne(fabsf(a) < inf ? a : 0.0f, fabsf(b) < inf ? b : 0.0f);
             } else {
-                hi[d] = __float_as_uint(v[d]);
-                lo[d] = 0;
+                v[0][d] = __float_as_uint(sum[d]);
+            }
+        }
+    }
+    // t of a row, if it `has` one.  PARTS: of parts, if there are.
+    template <bool PARTS>
+    static __device__ __forceinline__ void load_t(const AdapterArgs &p, bool has, int64_t row, int e0, u32x4 (&v)[PLANES])
+    {
+        if constexpr (PARTS) {
+            if (p.parts > 0) {
+                load_parts(p, has, row, e0, v);
+                return;
+            }
+        }
+        const In *t = static_cast<const In *>(p.t) + row * p.pitch + e0;
+#pragma unroll
+        for (int h = 0; h < PLANES; ++h) {
+            v[h] = u32x4{0, 0, 0, 0};
+            if (has && e0 < p.rank) v[h] = load16(t + h * p.plane);   // inside the pitch
+#pragma unroll
+            for (int d = 0; d < 4; ++d) {
+                if constexpr (BF16)
+                    v[h][d] &= e0 + 2 * d + 1 < p.rank ? 0xFFFFFFFFu : e0 + 2 * d < p.rank ? 0xFFFFu : 0u;
+                else
+                    v[h][d] = e0 + d < p.rank ? v[h][d] : 0u;
             }
         }
     }
 };
 
-__device__ __forceinline__ int adapter_of_row(const AdapterArgs &p, int64_t row)
-{
-    const int id = p.ids[row];
-    return (unsigned)id < (unsigned)p.count ? id : -1;
-}
-
-// Adds the adapters of a tile's rows to a wave's sums.  row0: first of the wave's rows,
-// rows: the end of those that there are; col0: first of its columns, of N.
-template <class G, class Acc>
-__device__ __forceinline__ void add_adapters(const AdapterArgs &p, int lane, int row0, int rows, int col0, int N, Acc &acc)
-{
-    using Op = AdapterOperand<G::BF16>;
-    using In = typename Op::In;
-    constexpr int FR = G::BF16 ? 16 : 32;              // rows, or columns, of a fragment
-    constexpr int STEP = Op::KV * (64 / FR);           // k values of a step
-    const int c = lane % FR, q = lane / FR;
+// The numbers of a wave's rows in a tile, loaded before its product: row0: the first of
+// the rows, rows: the end of those that there are.
+template <class G>
+struct TileAdapters {
+    static constexpr int FR = G::BF16 ? 16 : 32;   // rows, or columns, of a fragment
+    static constexpr bool PARTS = G::BM <= 64 && G::BN <= 64;
     int id[G::FN];
+
+    __device__ __forceinline__ void load(const AdapterArgs &p, int lane, int row0, int rows)
+    {
 #pragma unroll
-    for (int j = 0; j < G::FN; ++j) {
-        const int row = row0 + FR * j + c;
-        id[j] = row < rows ? adapter_of_row(p, row) : -1;
+        for (int j = 0; j < G::FN; ++j) id[j] = p.ids[min(row0 + FR * j + lane % FR, rows - 1)];
     }
-    while (true) {
-        int e = -1;   // the first adapter that is left
+
+    // Adds the adapters to the wave's sums, STEPS steps of the rank at a time; col0: first
+    // of the wave's columns, of N.  Slices of the summed axis take the adapters in turn.
+    // What takes time are loads one after another, so those of t and of the first
+    // adapters' b leave together; in smaller tiles, whose registers allow it, for two steps.
+    template <int STEPS, class Acc>
+    __device__ __forceinline__ void add(const AdapterArgs &p, int lane, int row0, int rows, int col0, int N, int slice,
+                                        int slices, Acc &acc) const
+    {
+        using Op = AdapterOperand<G::BF16>;
+        using In = typename Op::In;
+        constexpr int STEP = Op::KV * (64 / FR);           // k values of a step
+        constexpr int BATCH = 16 / G::FM / STEPS > 0 ? 16 / G::FM / STEPS : 1;   // adapters at a time
+        const int c = lane % FR, q = lane / FR;
+        uint32_t has = 0;                                  // bit j: this lane's row j has an adapter
 #pragma unroll
-        for (int j = G::FN - 1; j >= 0; --j) {
-            const uint64_t left = __ballot(id[j] >= 0);
-            if (left != 0) e = __builtin_amdgcn_readlane(id[j], __builtin_ctzll(left));
-        }
-        if (e < 0) return;
-        const In *b = static_cast<const In *>(p.b) + e * p.stride_b;
-        for (int k0 = 0; k0 < p.rank; k0 += STEP) {
-            const int k = k0 + q * Op::KV;
-            u32x4 w[G::FM];
+        for (int j = 0; j < G::FN; ++j)
+            if (row0 + FR * j + c < rows && (unsigned)id[j] < (unsigned)p.count) has |= 1u << j;
+        if (__ballot(has != 0) == 0) return;
+        for (int k0 = 0; k0 < p.rank; k0 += STEPS * STEP) {
+            const bool whole = k0 + STEPS * STEP <= p.rank;   // of all lanes
+            u32x4 t[STEPS][G::FN][Op::PLANES];
 #pragma unroll
-            for (int i = 0; i < G::FM; ++i) w[i] = Op::load(b + (int64_t)min(col0 + FR * i + c, N - 1) * p.ldb, k, p.rank);
+            for (int s = 0; s < STEPS; ++s) {
+                const int k = k0 + s * STEP + q * Op::KV;
+                if (whole && (!PARTS || p.parts == 0)) {
+                    // rows without an adapter load what is there: it is not used
 #pragma unroll
-            for (int j = 0; j < G::FN; ++j) {
-                if (__ballot(id[j] == e) == 0) continue;
-                u32x4 hi, lo;
-                Op::load_t(p, id[j] == e, row0 + FR * j + c, k, hi, lo);
+                    for (int j = 0; j < G::FN; ++j)
 #pragma unroll
-                for (int i = 0; i < G::FM; ++i) {
-                    if constexpr (G::BF16) {
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                            __builtin_bit_cast(bf16x8, w[i]), __builtin_bit_cast(bf16x8, hi), acc[i][j], 0, 0, 0);
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                            __builtin_bit_cast(bf16x8, w[i]), __builtin_bit_cast(bf16x8, lo), acc[i][j], 0, 0, 0);
-                    } else {
+                        for (int h = 0; h < Op::PLANES; ++h)
+                            t[s][j][h] = load16(static_cast<const In *>(p.t) +
+                                                (int64_t)min(row0 + FR * j + c, rows - 1) * p.pitch + k + h * p.plane);
+                } else {
 #pragma unroll
-                        for (int d = 0; d < 4; ++d)
-                            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(
-                                __uint_as_float(w[i][d]), __uint_as_float(hi[d]), acc[i][j], 0, 0, 0);
+                    for (int j = 0; j < G::FN; ++j) Op::template load_t<PARTS>(p, has >> j & 1, row0 + FR * j + c, k, t[s][j]);
+                }
+            }
+            uint32_t left = has;
+            int turn = 0;
+            while (true) {
+                int e[BATCH];
+#pragma unroll
+                for (int n = 0; n < BATCH; ++n) {
+                    // the next adapter that is left, and this slice's
+                    bool mine;
+                    do {
+                        e[n] = -1;
+#pragma unroll
+                        for (int j = G::FN - 1; j >= 0; --j) {
+                            const uint64_t some = __ballot(left >> j & 1);
+                            if (some != 0) e[n] = __builtin_amdgcn_readlane(id[j], __builtin_ctzll(some));
+                        }
+#pragma unroll
+                        for (int j = 0; j < G::FN; ++j)
+                            if (id[j] == e[n]) left &= ~(1u << j);
+                        mine = turn == slice;
+                        turn = turn + 1 == slices ? 0 : turn + 1;
+                    } while (e[n] >= 0 && !mine);
+                }
+                if (e[0] < 0) break;
+                u32x4 w[BATCH][STEPS][G::FM];
+#pragma unroll
+                for (int n = 0; n < BATCH; ++n) {
+                    if (e[n] < 0) break;
+                    const In *b = static_cast<const In *>(p.b) + e[n] * p.stride_b;
+#pragma unroll
+                    for (int i = 0; i < G::FM; ++i) {
+                        const In *row = b + (int64_t)min(col0 + FR * i + c, N - 1) * p.ldb + k0 + q * Op::KV;
+#pragma unroll
+                        for (int s = 0; s < STEPS; ++s)
+                            w[n][s][i] = whole ? __builtin_bit_cast(u32x4, *reinterpret_cast<const typename Op::chunk *>(row + s * STEP))
+                                               : Op::load(row - k0 - q * Op::KV, k0 + s * STEP + q * Op::KV, p.rank);
+                    }
+                }
+#pragma unroll
+                for (int n = 0; n < BATCH; ++n) {
+                    if (e[n] < 0) break;
+#pragma unroll
+                    for (int j = 0; j < G::FN; ++j) {
+                        const bool mine = (has >> j & 1) && id[j] == e[n];
+                        if (__ballot(mine) == 0) continue;
+#pragma unroll
+                        for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+                            for (int h = 0; h < Op::PLANES; ++h) {
+                                u32x4 v;
+#pragma unroll
+                                for (int d = 0; d < 4; ++d) v[d] = mine ? t[s][j][h][d] : 0u;
+#pragma unroll
+                                for (int i = 0; i < G::FM; ++i) {
+                                    if constexpr (G::BF16) {
+                                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                                            __builtin_bit_cast(bf16x8, w[n][s][i]), __builtin_bit_cast(bf16x8, v),
+                                            acc[i][j], 0, 0, 0);
+                                    } else {
+#pragma unroll
+                                        for (int d = 0; d < 4; ++d)
+                                            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(
+                                                __uint_as_float(w[n][s][i][d]), __uint_as_float(v[d]), acc[i][j], 0, 0, 0);
+                                    }
+                                }
+                            }
                     }
                 }
             }
         }
-#pragma unroll
-        for (int j = 0; j < G::FN; ++j)
-            if (id[j] == e) id[j] = -1;
     }
-}
+};
+
+// Without adapters: nothing.
+struct NoAdapters {};
 
 }  // namespace dg

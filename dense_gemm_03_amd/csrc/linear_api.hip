@@ -604,6 +604,16 @@ int grad(const gemm_linear_params *p, const gemm_linear_grad_outputs *o, const v
 
 }  // namespace
 
+bool adapter_sums_allowed(const gemm_linear_params *p)
+{
+    if (!valid_sizes(p)) return false;
+    const Plan pl = make_plan(*p, false);
+    int count = 0;
+    if (pl.cfg < 0) return false;
+    const LinearConfig &c = linear_configs(p->dtype, &count)[pl.cfg];
+    return c.bm <= 64 && c.bn <= 64;
+}
+
 int linear_with_adapters(const gemm_linear_params *p, const AdapterDownArgs *down, const AdapterArgs *ad,
                          const void *x, const void *w, const void *bias, const void *residual, void *y,
                          void *workspace, int64_t workspace_bytes, hipStream_t stream)

@@ -598,6 +598,10 @@ __device__ __forceinline__ void linear_tile(const Args &p, const TileSpec &t, un
 #pragma unroll
             for (int r = 0; r < SUMS; ++r) acc[fm][fn][r] = 0.0f;
 
+    constexpr bool ADAPTED = std::is_same<Args, AdaptedArgs>::value;
+    [[maybe_unused]] typename std::conditional<ADAPTED, TileAdapters<G>, NoAdapters>::type adapters;
+    if constexpr (ADAPTED) adapters.load(p.ad, c.lane, t.row0 + c.wcol * G::WTN, t.m);
+
     // The choice between the loops is that of the dense product, on the
     // group's rows: whole k-tiles through direct loads of 16 bytes per lane
     // (aligned rows) or 4 range-checked ones, the rest masked.
@@ -653,9 +657,12 @@ __device__ __forceinline__ void linear_tile(const Args &p, const TileSpec &t, un
         }
     }
 
-    if constexpr (std::is_same<Args, AdaptedArgs>::value) {
-        if (t.slice == 0)
-            add_adapters<G>(p.ad, c.lane, t.row0 + c.wcol * G::WTN, t.m, t.col0 + c.wrow * G::WTM, p.N, acc);
+    if constexpr (ADAPTED) {
+        const int row0 = t.row0 + c.wcol * G::WTN, col0 = t.col0 + c.wrow * G::WTM;
+        if (G::FM * G::FN > 16 || p.ad.rank <= (BF16 ? 32 : 8))
+            adapters.template add<1>(p.ad, c.lane, row0, t.m, col0, p.N, t.slice, p.splits, acc);
+        else
+            adapters.template add<(G::FM * G::FN > 16 ? 1 : 2)>(p.ad, c.lane, row0, t.m, col0, p.N, t.slice, p.splits, acc);
     }
 
     const int out_rows = WGRAD ? p.M : t.m;   // rows of this group's output
@@ -988,6 +995,8 @@ __global__ void __launch_bounds__(64 * WV) few_rows_kernel(Args p)
     floatx4 acc[W];
 #pragma unroll
     for (int j = 0; j < W; ++j) acc[j] = {0.0f, 0.0f, 0.0f, 0.0f};
+    [[maybe_unused]] int id = -1;   // with adapters: this lane's row's, on the way during the product
+    if constexpr (std::is_same<Args, AdaptedArgs>::value) id = p.ad.ids[row0 + min(f.c, count - 1)];
     if (F::T || p.N >= W)
         f.template run<false>(wave, acc);
     else
@@ -996,24 +1005,26 @@ __global__ void __launch_bounds__(64 * WV) few_rows_kernel(Args p)
     if constexpr (std::is_same<Args, AdaptedArgs>::value) {
         // the waves take the adapters of the rows in turn
         using Op = AdapterOperand<BF16>;
-        const int id = f.c < count ? adapter_of_row(p.ad, row0 + f.c) : -1;
-        int turn = 0;
-        for (uint64_t left = __ballot(id >= 0); left != 0; turn = turn + 1 == WV ? 0 : turn + 1) {
-            const int e = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
-            left &= ~__ballot(id == e);
-            if (turn != wave) continue;
-            const In *b = static_cast<const In *>(p.ad.b) + e * p.ad.stride_b;
-            for (int k0 = 0; k0 < p.ad.rank; k0 += 4 * F::KV) {
-                const int k = k0 + f.q * F::KV;
-                u32x4 hi, lo;
-                Op::load_t(p.ad, id == e, row0 + f.c, k, hi, lo);
+        if (f.c >= count || (unsigned)id >= (unsigned)p.ad.count) id = -1;
+        for (int k0 = 0; k0 < p.ad.rank; k0 += 4 * F::KV) {
+            const int k = k0 + f.q * F::KV;
+            int turn = 0;
+            for (uint64_t left = __ballot(id >= 0); left != 0; turn = turn + 1 == WV ? 0 : turn + 1) {
+                const int e = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
+                left &= ~__ballot(id == e);
+                if (turn != wave) continue;
+                const In *b = static_cast<const In *>(p.ad.b) + e * p.ad.stride_b;
+                u32x4 w[W], t[Op::PLANES];
 #pragma unroll
                 for (int j = 0; j < W; ++j) {
                     const int col = F::T ? f.n0 + 16 * j + f.c : f.first_col() + j;
-                    const u32x4 v = Op::load(b + (int64_t)min(col, p.N - 1) * p.ad.ldb, k, p.ad.rank);
-                    F::mma(hi, v, acc[j]);
-                    if constexpr (BF16) F::mma(lo, v, acc[j]);
+                    w[j] = Op::load(b + (int64_t)min(col, p.N - 1) * p.ad.ldb, k, p.ad.rank);
                 }
+                Op::template load_t<true>(p.ad, id == e, row0 + f.c, k, t);   // zeros in the other rows
+#pragma unroll
+                for (int h = 0; h < Op::PLANES; ++h)
+#pragma unroll
+                    for (int j = 0; j < W; ++j) F::mma(t[h], w[j], acc[j]);
             }
         }
     }

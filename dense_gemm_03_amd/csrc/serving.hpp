@@ -74,13 +74,18 @@ struct AdapterDownArgs {
     const void *x, *a;           // a: per adapter rank x K
     const int32_t *ids;
     const float *scales;         // or nullptr: 1
-    float *t;
-    int64_t ldx, lda, stride_a, t_part;
+    void *t;
+    float *ws;                   // sums of more than one part: parts x rows x pitch
+    int64_t ldx, lda, stride_a, plane;
     int rows, K, count, rank, pitch;
     int parts, part_k;           // parts of K, of part_k values
+    int join;                    // whether to form t of more than one part, or leave the sums
     int slots;                   // blocks per 64 rows and part: each takes every slots-th adapter of the rows
 };
 hipError_t launch_adapter_down(const AdapterDownArgs &args, bool bf16, hipStream_t stream);
+
+// Whether the kernel that this layer takes can add up the adapters' sums of parts.
+bool adapter_sums_allowed(const gemm_linear_params *p);
 
 // gemm_linear with an adapter per row (linear_api.hip): launch_adapter_down(*down) once
 // the arguments are checked, then the layer with *ad.  Both nullptr: the layer alone.

@@ -308,8 +308,9 @@ gemm_linear_params layer_of(const gemm_adapter_params &p)
 
 struct AdapterShares {
     bool any;                  // a row may have an adapter that adds something
+    bool join;                 // parts are joined before the product
     int pitch, parts, part_k, slots;
-    int64_t t_bytes, total;    // total < 0: the layer's error
+    int64_t t_bytes, ws_bytes, total;    // total < 0: the layer's error
     bool launchable;
 };
 
@@ -328,18 +329,24 @@ AdapterShares shares_of(const gemm_adapter_params &p)
     s.part_k = (int)p.K;
     s.pitch = (int)(ceil_div(p.rank, 8) * 8);
     if (s.any && p.K >= 8) {
-        // A block per adapter of 64 rows (one after another where rows are many), and
-        // parts of K until there are blocks for all units; a wave has one step of 64 at
-        // least, and every tile of the product adds up the parts.
+        // A block has 64 rows, a part of K and, of the rows' adapters, every slots-th (blocks
+        // behind a group's last adapter end at once).  x and a come to it at 25 KB per us
+        // (one row, rank 16, K = 4096: 8.9 us in one part, 5.9 in eight).
         const int64_t groups = ceil_div(p.rows, 64), cus = device_compute_units();
+        const int64_t bytes = (std::min<int64_t>(p.rows, 64) + p.rank) * p.K * size_of(p.dtype);
+        int64_t want = 1;
+        while (want < ADAPTER_MAX_PARTS && bytes / want > 24 * 1024 && 2 * want * groups <= cus && p.K >= 512 * want) want *= 2;
         s.slots = (int)std::max<int64_t>(1, std::min(std::min<int64_t>(p.adapters, std::min<int64_t>(p.rows, 64)),
-                                                     ceil_div(cus, groups)));
-        const int64_t want = std::min<int64_t>(std::min<int64_t>(8, ceil_div(cus, groups * s.slots)), ceil_div(p.K, 8 * 64));
+                                                     2 * cus / (groups * want)));
         s.part_k = (int)(ceil_div(ceil_div(p.K, want), 64) * 64);
         s.parts = (int)ceil_div(p.K, s.part_k);
         s.launchable = groups * s.slots * s.parts <= int64_t(UINT32_MAX) / 512;
     }
-    s.t_bytes = s.any ? s.parts * p.rows * s.pitch * 4 : 0;   // whole 16 bytes
+    // the sums of a few rows' parts are added up by the product's blocks, if they can
+    s.join = s.parts > 1 && (p.rows > 64 || !adapter_sums_allowed(&q));
+    const int64_t values = p.rows * s.pitch;       // whole 16 bytes, as bf16 too
+    s.ws_bytes = s.any && s.parts > 1 ? s.parts * values * 4 : 0;
+    s.t_bytes = s.ws_bytes + (s.any && (s.parts == 1 || s.join) ? values * 4 : 0);   // two bf16 values, or one in fp32
     s.total = s.t_bytes + layer;
     return s;
 }
@@ -365,11 +372,13 @@ int adapter_linear(const gemm_adapter_params *p, const void *x, const void *w, c
     d.a = a;
     d.ids = ids;
     d.scales = scales;
-    d.t = static_cast<float *>(workspace);
+    d.ws = static_cast<float *>(workspace);
+    d.t = scratch + s.ws_bytes;
+    d.join = s.join;
     d.ldx = p->ldx;
     d.lda = p->lda;
     d.stride_a = p->adapters > 1 ? p->stride_a : 0;
-    d.t_part = p->rows * s.pitch;
+    d.plane = p->rows * s.pitch;
     d.rows = (int)p->rows;
     d.K = (int)p->K;
     d.count = (int)p->adapters;
@@ -379,16 +388,17 @@ int adapter_linear(const gemm_adapter_params *p, const void *x, const void *w, c
     d.part_k = s.part_k;
     d.slots = s.slots;
     AdapterArgs ad{};
-    ad.t = d.t;
+    const bool sums = s.parts > 1 && !s.join;
+    ad.t = sums ? workspace : d.t;
+    ad.parts = sums ? s.parts : 0;
     ad.b = b;
     ad.ids = ids;
     ad.ldb = p->ldb;
     ad.stride_b = p->adapters > 1 ? p->stride_b : 0;
-    ad.t_part = d.t_part;
+    ad.plane = d.plane;
     ad.count = d.count;
     ad.rank = d.rank;
     ad.pitch = s.pitch;
-    ad.parts = s.parts;
     return linear_with_adapters(&q, &d, &ad, x, w, bias, residual, y, rest, s.total - s.t_bytes, stream);
 }
 
