@@ -148,6 +148,34 @@ def test_ranks(cuda, dtype, rank):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows", [1, 17, 64, 65, 300, 1000])
+def test_parts_of_the_summed_axis(cuda, dtype, rows):
+    """Long rows, whose first product is cut into parts: added up by the second's blocks for
+    a few rows, joined before it for more."""
+    for k, n, rank, kind in ((1100, 136, 5, "mixed"), (4099, 72, 16, "each"), (4096, 264, 72, "runs"), (2048, 40, 33, "mixed")):
+        check(dtype, rows, k, n, rank, kind=kind, transb=rank != 16, residual=True)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_parts_through_every_kernel(cuda, dtype):
+    """The same where the entry is forced: small tiles and few rows add up parts, large tiles do not."""
+    code = dg.GEMM_DTYPE_F32 if dtype == "f32" else dg.GEMM_DTYPE_BF16
+    try:
+        for cfg in range(dg.gemm_linear_num_configs(code)):
+            forms = dg.gemm_linear_config_forms(code, cfg)
+            for split in (1, 3):
+                for transb in (False, True):
+                    if forms >> transb & 1:
+                        log(dg.gemm_linear_config_name(code, cfg), split, transb)
+                        assert dg.gemm_linear_force_config(cfg, split) == 0
+                        check(dtype, 50, 2048, 136, 40, kind="mixed", transb=transb)
+    finally:
+        dg.gemm_linear_force_config()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("transb", [False, True])
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("width", [(1, 1), (3, 5), (7, 40), (8, 16), (9, 33), (65, 1), (67, 130), (515, 257), (2055, 72),
@@ -295,6 +323,25 @@ def test_streams_and_graphs(cuda):
         eager = run(1)
         torch.cuda.synchronize()
         assert torch.equal(out, want[k % 2]) and torch.equal(eager, want[1])
+
+
+@pytest.mark.gpu
+def test_two_streams_at_once(cuda):
+    """Calls on two streams at a time, of rows whose parts are joined and of few rows."""
+    jobs = []
+    for rows, seed in ((300, 1), (20, 7)):
+        jobs.append((rand(rows, 2048, dtype="bf16", seed=seed), rand(256, 2048, dtype="bf16", seed=seed + 1),
+                     rand(4, 16, 2048, dtype="bf16", seed=seed + 2), rand(4, 256, 16, dtype="bf16", seed=seed + 3),
+                     requests(rows, 4, "mixed")))
+    want = [dg.adapter_linear(*j, transb=True) for j in jobs]
+    streams = [torch.cuda.Stream() for _ in jobs]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(20):
+        got = [dg.adapter_linear(*j, transb=True, stream=s.cuda_stream) for j, s in zip(jobs, streams)]
+        for s in streams:
+            s.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
 @pytest.mark.gpu

@@ -379,6 +379,23 @@ def test_streams_and_graphs(cuda):
 
 
 @pytest.mark.gpu
+def test_two_streams_at_once(cuda):
+    """Calls on two streams at a time, of rows in parts and of whole rows."""
+    zs = [rand(3, 100003, "bf16", 9), rand(2100, 5003, "f32", 8)]
+    ts = [token_row(3, 100003), token_row(2100, 5003)]
+    want = [dg.log_probs(z, t, 20) for z, t in zip(zs, ts)]
+    streams = [torch.cuda.Stream() for _ in zs]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(10):
+        got = [dg.log_probs(z, t, 20, stream=s.cuda_stream) for z, t, s in zip(zs, ts, streams)]
+        for s in streams:
+            s.synchronize()
+        for g, w in zip(got, want):
+            assert all(torch.equal(a, b) for a, b in zip(g, w))
+
+
+@pytest.mark.gpu
 def test_helper_checks(cuda):
     z, t = rand(4, 100, "f32", 1), token_row(4, 100)
     for bad in (lambda: dg.log_probs(z, t.long()), lambda: dg.log_probs(z.half(), t)):

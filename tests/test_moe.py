@@ -136,6 +136,18 @@ def test_tokens(cuda, dtype, transb, tokens):
     check(dtype, tokens, 100, 72, 5, 2, transb=transb, ids=ids, weights=torch.rand(tokens, 2, device="cuda"))
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("transb", [False, True])
+@pytest.mark.parametrize("tokens", [300, 512])
+def test_most_tokens(cuda, transb, tokens):
+    """Experts with more rows than a block takes at a time, and the most ids there can be."""
+    check("bf16", tokens, 72, 56, 8, 3, transb=transb, residual=True, absent=0.1)
+    ids = torch.tensor([[1, 3]], dtype=torch.int32, device="cuda").repeat(tokens, 1)
+    ids[5] = -1
+    check("f32", tokens, 40, 72, 5, 2, transb=transb, ids=ids, weights=torch.rand(tokens, 2, device="cuda"))
+    check("bf16", tokens, 40, 24, 1024, 32, transb=transb)
+
+
 WIDTHS = [(1, 1), (2, 3), (1, 40), (7, 5), (15, 17), (16, 16), (33, 31), (64, 130), (129, 64), (257, 255), (515, 33),
           (40, 1030), (2048, 96)]
 
