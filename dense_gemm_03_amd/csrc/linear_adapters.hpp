@@ -41,6 +41,53 @@ struct AdapterOperand {
     static constexpr int KV = BF16 ? 8 : 4, PLANES = BF16 ? 2 : 1;
     typedef In chunk __attribute__((ext_vector_type(KV), aligned(sizeof(In))));
 
+    static constexpr uint32_t LARGE = BF16 ? 0x7F007F00u : 0x7F000000u;      // 2^127: its square is infinite
+    static constexpr uint32_t EXPONENT = BF16 ? 0x7F807F80u : 0x7F800000u;   // all ones: infinity or NaN
+
+    // The largest exponents of `so_far` and v (bf16: of each half).
+    static __device__ __forceinline__ uint32_t largest(uint32_t so_far, const u32x4 &v)
+    {
+        typedef uint16_t pair __attribute__((ext_vector_type(2)));
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+            const uint32_t e = v[d] & EXPONENT;
+            so_far = BF16 ? __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(pair, so_far),
+                                                                                   __builtin_bit_cast(pair, e)))
+                          : max(so_far, e);
+        }
+        return so_far;
+    }
+    static __device__ __forceinline__ bool infinite(uint32_t exponents)
+    {
+        return BF16 ? exponents >> 16 == 0x7F80u || (exponents & 0xFFFFu) == 0x7F80u : exponents == EXPONENT;
+    }
+    static __device__ __forceinline__ uint32_t not_finite(uint32_t v)   // all ones in the places of such values
+    {
+        if (!BF16) return infinite(v & EXPONENT) ? ~0u : 0u;
+        return (infinite(v & 0x7F80u) ? 0xFFFFu : 0u) | (infinite(v & 0x7F800000u) ? 0xFFFF0000u : 0u);
+    }
+    // v with zeros for values that are not finite; or their marks: LARGE in their places, else 0.
+    static __device__ __forceinline__ u32x4 apart(u32x4 v, bool marks)
+    {
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+            const uint32_t out = not_finite(v[d]);
+            v[d] = marks ? LARGE & out : v[d] & ~out;
+        }
+        return v;
+    }
+    template <class Sum>
+    static __device__ __forceinline__ void mma(const u32x4 &a, const u32x4 &v, Sum &sum)
+    {
+        if constexpr (BF16) {
+            sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, v), sum,
+                                                          0, 0, 0);
+        } else {
+#pragma unroll
+            for (int d = 0; d < 4; ++d)
+                sum = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a[d]), __uint_as_float(v[d]), sum, 0, 0, 0);
+        }
+    }
     // b, at the element's alignment
     static __device__ __forceinline__ u32x4 load(const In *row, int e0, int end)
     {
@@ -130,7 +177,8 @@ struct TileAdapters {
     // Adds the adapters to the wave's sums, STEPS steps of the rank at a time; col0: first
     // of the wave's columns, of N.  Slices of the summed axis take the adapters in turn.
     // What takes time are loads one after another, so those of t and of the first
-    // adapters' b leave together; in smaller tiles, whose registers allow it, for two steps.
+    // adapters' b leave together, in smaller tiles, whose registers allow it, for two steps.
+    // Large tiles' accumulators leave registers for one adapter's b.
     template <int STEPS, class Acc>
     __device__ __forceinline__ void add(const AdapterArgs &p, int lane, int row0, int rows, int col0, int N, int slice,
                                         int slices, Acc &acc) const
@@ -138,7 +186,7 @@ struct TileAdapters {
         using Op = AdapterOperand<G::BF16>;
         using In = typename Op::In;
         constexpr int STEP = Op::KV * (64 / FR);           // k values of a step
-        constexpr int BATCH = 16 / G::FM / STEPS > 0 ? 16 / G::FM / STEPS : 1;   // adapters at a time
+        constexpr int BATCH = G::FM * G::FN > 16 ? 1 : 16 / G::FM / STEPS;   // adapters at a time
         const int c = lane % FR, q = lane / FR;
         uint32_t has = 0;                                  // bit j: this lane's row j has an adapter
 #pragma unroll
@@ -164,73 +212,88 @@ struct TileAdapters {
                     for (int j = 0; j < G::FN; ++j) Op::template load_t<PARTS>(p, has >> j & 1, row0 + FR * j + c, k, t[s][j]);
                 }
             }
-            uint32_t left = has;
-            int turn = 0;
-            while (true) {
-                int e[BATCH];
+            // Other adapters' rows must not see what one holds, and zeros for their t would make
+            // NaN of its infinities.  So values of b that are not finite are left out, and in a
+            // second turn their columns of the adapter's own rows become infinite, by products
+            // of large numbers.  (Sums selected by row take the accumulators twice, which large
+            // tiles have no registers for: 4096 rows of 8 requests, 4096 x 8192, rank 64: 765 us,
+            // so 258.)
+            bool finite = true;   // what this lane has read of the adapters
+#pragma nounroll
+            for (bool marked = false;; marked = true) {
+                uint32_t left = has;
+                int turn = 0;
+                while (true) {
+                    int e[BATCH];
 #pragma unroll
-                for (int n = 0; n < BATCH; ++n) {
-                    // the next adapter that is left, and this slice's
-                    bool mine;
-                    do {
-                        e[n] = -1;
+                    for (int n = 0; n < BATCH; ++n) {
+                        // the next adapter that is left, and this slice's
+                        bool mine;
+                        do {
+                            e[n] = -1;
 #pragma unroll
-                        for (int j = G::FN - 1; j >= 0; --j) {
-                            const uint64_t some = __ballot(left >> j & 1);
-                            if (some != 0) e[n] = __builtin_amdgcn_readlane(id[j], __builtin_ctzll(some));
+                            for (int j = G::FN - 1; j >= 0; --j) {
+                                const uint64_t some = __ballot(left >> j & 1);
+                                if (some != 0) e[n] = __builtin_amdgcn_readlane(id[j], __builtin_ctzll(some));
+                            }
+#pragma unroll
+                            for (int j = 0; j < G::FN; ++j)
+                                if (id[j] == e[n]) left &= ~(1u << j);
+                            mine = turn == slice;
+                            turn = turn + 1 == slices ? 0 : turn + 1;
+                        } while (e[n] >= 0 && !mine);
+                    }
+                    if (e[0] < 0) break;
+                    u32x4 w[BATCH][STEPS][G::FM];
+#pragma unroll
+                    for (int n = 0; n < BATCH; ++n) {
+                        if (e[n] < 0) break;
+                        const In *b = static_cast<const In *>(p.b) + e[n] * p.stride_b;
+#pragma unroll
+                        for (int i = 0; i < G::FM; ++i) {
+                            const In *row = b + (int64_t)min(col0 + FR * i + c, N - 1) * p.ldb + k0 + q * Op::KV;
+#pragma unroll
+                            for (int s = 0; s < STEPS; ++s)
+                                w[n][s][i] = whole ? __builtin_bit_cast(u32x4, *reinterpret_cast<const typename Op::chunk *>(row + s * STEP))
+                                                   : Op::load(row - k0 - q * Op::KV, k0 + s * STEP + q * Op::KV, p.rank);
+                        }
+                    }
+#pragma unroll
+                    for (int n = 0; n < BATCH; ++n) {
+                        if (e[n] < 0) break;
+                        uint32_t exponents = 0;
+#pragma unroll
+                        for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+                            for (int i = 0; i < G::FM; ++i) exponents = Op::largest(exponents, w[n][s][i]);
+                        if (__ballot(Op::infinite(exponents)) != 0 || marked) {
+                            finite = finite && !Op::infinite(exponents);
+#pragma unroll
+                            for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+                                for (int i = 0; i < G::FM; ++i) w[n][s][i] = Op::apart(w[n][s][i], marked);
                         }
 #pragma unroll
-                        for (int j = 0; j < G::FN; ++j)
-                            if (id[j] == e[n]) left &= ~(1u << j);
-                        mine = turn == slice;
-                        turn = turn + 1 == slices ? 0 : turn + 1;
-                    } while (e[n] >= 0 && !mine);
-                }
-                if (e[0] < 0) break;
-                u32x4 w[BATCH][STEPS][G::FM];
+                        for (int j = 0; j < G::FN; ++j) {
+                            const bool mine = (has >> j & 1) && id[j] == e[n];
+                            if (__ballot(mine) == 0) continue;
 #pragma unroll
-                for (int n = 0; n < BATCH; ++n) {
-                    if (e[n] < 0) break;
-                    const In *b = static_cast<const In *>(p.b) + e[n] * p.stride_b;
+                            for (int s = 0; s < STEPS; ++s)
 #pragma unroll
-                    for (int i = 0; i < G::FM; ++i) {
-                        const In *row = b + (int64_t)min(col0 + FR * i + c, N - 1) * p.ldb + k0 + q * Op::KV;
+                                for (int h = 0; h < Op::PLANES; ++h) {
+                                    u32x4 v;
 #pragma unroll
-                        for (int s = 0; s < STEPS; ++s)
-                            w[n][s][i] = whole ? __builtin_bit_cast(u32x4, *reinterpret_cast<const typename Op::chunk *>(row + s * STEP))
-                                               : Op::load(row - k0 - q * Op::KV, k0 + s * STEP + q * Op::KV, p.rank);
-                    }
-                }
-#pragma unroll
-                for (int n = 0; n < BATCH; ++n) {
-                    if (e[n] < 0) break;
-#pragma unroll
-                    for (int j = 0; j < G::FN; ++j) {
-                        const bool mine = (has >> j & 1) && id[j] == e[n];
-                        if (__ballot(mine) == 0) continue;
-#pragma unroll
-                        for (int s = 0; s < STEPS; ++s)
-#pragma unroll
-                            for (int h = 0; h < Op::PLANES; ++h) {
-                                u32x4 v;
-#pragma unroll
-                                for (int d = 0; d < 4; ++d) v[d] = mine ? t[s][j][h][d] : 0u;
-#pragma unroll
-                                for (int i = 0; i < G::FM; ++i) {
-                                    if constexpr (G::BF16) {
-                                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                                            __builtin_bit_cast(bf16x8, w[n][s][i]), __builtin_bit_cast(bf16x8, v),
-                                            acc[i][j], 0, 0, 0);
-                                    } else {
-#pragma unroll
-                                        for (int d = 0; d < 4; ++d)
-                                            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(
-                                                __uint_as_float(w[n][s][i][d]), __uint_as_float(v[d]), acc[i][j], 0, 0, 0);
+                                    for (int d = 0; d < 4; ++d) {
+                                        v[d] = marked ? Op::LARGE : t[s][j][h][d];
+                                        v[d] = mine ? v[d] : 0u;
                                     }
+#pragma unroll
+                                    for (int i = 0; i < G::FM; ++i) Op::mma(w[n][s][i], v, acc[i][j]);
                                 }
-                            }
+                        }
                     }
                 }
+                if (marked || __ballot(!finite) == 0) break;
             }
         }
     }

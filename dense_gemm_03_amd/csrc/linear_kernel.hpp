@@ -1011,7 +1011,8 @@ __global__ void __launch_bounds__(64 * WV) few_rows_kernel(Args p)
             int turn = 0;
             for (uint64_t left = __ballot(id >= 0); left != 0; turn = turn + 1 == WV ? 0 : turn + 1) {
                 const int e = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
-                left &= ~__ballot(id == e);
+                const uint64_t rows_of_it = __ballot(id == e);
+                left &= ~rows_of_it;
                 if (turn != wave) continue;
                 const In *b = static_cast<const In *>(p.ad.b) + e * p.ad.stride_b;
                 u32x4 w[W], t[Op::PLANES];
@@ -1020,11 +1021,16 @@ __global__ void __launch_bounds__(64 * WV) few_rows_kernel(Args p)
                     const int col = F::T ? f.n0 + 16 * j + f.c : f.first_col() + j;
                     w[j] = Op::load(b + (int64_t)min(col, p.N - 1) * p.ad.ldb, k, p.ad.rank);
                 }
-                Op::template load_t<true>(p.ad, id == e, row0 + f.c, k, t);   // zeros in the other rows
+                Op::template load_t<true>(p.ad, id == e, row0 + f.c, k, t);
 #pragma unroll
-                for (int h = 0; h < Op::PLANES; ++h)
+                for (int j = 0; j < W; ++j) {
+                    floatx4 sum = acc[j];
 #pragma unroll
-                    for (int j = 0; j < W; ++j) F::mma(t[h], w[j], acc[j]);
+                    for (int h = 0; h < Op::PLANES; ++h) F::mma(t[h], w[j], sum);
+                    // the other rows' sums stay as they are, whatever the adapter holds
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) acc[j][r] = rows_of_it >> (4 * f.q + r) & 1 ? sum[r] : acc[j][r];
+                }
             }
         }
     }

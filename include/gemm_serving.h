@@ -86,7 +86,9 @@ int gemm_moe_layer(const gemm_moe_params *params, const void *x, const void *w_u
  * order (rows of a request side by side are fastest); an id outside 0 ..
  * adapters-1 leaves its row without an adapter.  a_i is rank x K and b_i N x rank,
  * row-major, stride_a and stride_b elements apart.  Adapters of a lower rank have
- * zeros in the rest.  scales (fp32, one per adapter) may be NULL: 1.
+ * zeros in the rest.  scales (fp32, one per adapter) may be NULL: 1.  An adapter that
+ * holds infinities or NaN makes infinities or NaN of its own rows alone (of a value in
+ * b, in its column).
  *
  * Precision as in gemm_linear; x . a^T is formed in fp32 and kept to 16 bits of
  * mantissa (bf16 operands) or as it is (fp32) for the second product.

@@ -276,6 +276,43 @@ def test_other_adapters_are_not_read(cuda):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_broken_adapters_keep_to_their_rows(cuda, dtype):
+    """NaN and infinities of one request's adapter reach no row of another's, nor rows without
+    one, in any kernel: those are what they are with a whole adapter, bit for bit."""
+    code = dg.GEMM_DTYPE_F32 if dtype == "f32" else dg.GEMM_DTYPE_BF16
+    k, n, rank = 200, 264, 24
+    for rows in (14, 290):
+        x, w = rand(rows, k, dtype=dtype, seed=1), rand(n, k, dtype=dtype, seed=2)
+        a, b = rand(5, rank, k, dtype=dtype, seed=3), rand(5, n, rank, dtype=dtype, seed=4)
+        ids = requests(rows, 5, "mixed")
+        own = ids == 2
+        assert own.any() and not own.all()
+        broken_b, broken_a = b.clone(), a.clone()
+        broken_b[2, ::3], broken_b[2, 1::3, 5] = math.nan, math.inf
+        broken_a[2, 3], broken_a[2, 4] = math.nan, math.inf
+        try:
+            for cfg in range(-1, dg.gemm_linear_num_configs(code)):
+                for split in (1, 3):
+                    for transb in (False, True):
+                        if cfg >= 0 and not dg.gemm_linear_config_forms(code, cfg) >> transb & 1:
+                            continue
+                        assert dg.gemm_linear_force_config(cfg, split if cfg >= 0 else 0) == 0
+                        args = (x, w if transb else w.T.contiguous())
+                        want = dg.adapter_linear(*args, a, b, ids, transb=transb)
+                        got = dg.adapter_linear(*args, broken_a, broken_b, ids, transb=transb)
+                        what = "%d rows, entry %d, %d slices, transb %s" % (rows, cfg, split, transb)
+                        assert torch.equal(got[~own], want[~own]), what
+                        assert torch.isnan(got[own]).all(), what
+                        # b alone: those of its columns that are broken
+                        got = dg.adapter_linear(*args, a, broken_b, ids, transb=transb)
+                        assert torch.equal(got[~own], want[~own]) and torch.equal(got[own][:, 2::3], want[own][:, 2::3]), what
+                        assert not (got[own][:, ::3].isfinite().any() or got[own][:, 1::3].isfinite().any()), what
+        finally:
+            dg.gemm_linear_force_config()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("rows", [4, 300])
 def test_in_place_of_the_residual(cuda, rows):
     x, w = rand(rows, 256, dtype="bf16", seed=1), rand(128, 256, dtype="bf16", seed=2)
