@@ -22,9 +22,15 @@ constexpr int CHUNK = 64 * 32;   // logits per wave and step: 32 per lane
 // multiplied, so that a forbidden place (t = -infinity) adds 0 and not NaN.
 __device__ __forceinline__ float bounded(float t) { return fmaxf(t, -200.0f); }
 
-// Whether c = a m is out of fp32's range, or so near its end that some a z may be.
-// Distances are then formed before they are scaled, and c is a m itself.
-__device__ __forceinline__ bool huge(float m, float a) { return !(fabsf(a * m) < 1e38f); }
+// Whether a m is so large that what c lacks of it, half a unit, may be an exponent of
+// more than 1/2.  Distances are then formed before they are scaled, and c is a m itself.
+__device__ __forceinline__ bool huge(float m, float a) { return !(fabsf(a * m) < 16777216.0f); }
+// a m - c
+__device__ __forceinline__ float lacking(float m, float a)
+{
+    const float c = a * m;
+    return huge(m, a) ? 0.0f : __builtin_fmaf(a, m, -c);
+}
 
 struct Sums {
     float m = kLowest, s = 0.0f, u = 0.0f;   // m is a number even where nothing or -infinity was read
@@ -33,7 +39,7 @@ struct Sums {
     __device__ __forceinline__ void move(float to, float a)
     {
 #pragma clang fp contract(off)   // a m and a to are the c's that the sums were formed with
-        const float t = bounded(huge(m, a) || huge(to, a) ? a * (m - to) : a * m - a * to);
+        const float t = bounded(huge(m, a) || huge(to, a) ? a * (m - to) - lacking(m, a) + lacking(to, a) : a * m - a * to);
         const float f = __builtin_amdgcn_exp2f(t);
         u = __builtin_fmaf(s, t, u) * f;
         s *= f;
@@ -70,8 +76,8 @@ __device__ __forceinline__ void finish_row(const LogProbsArgs &p, int64_t row, c
     const bool empty = x.s == 0.0f;   // the largest logit adds about 1, so: nothing but -infinity
     const float none = -__builtin_inff();
     const float log_s = logf(x.s);    // -infinity of 0
-    const float a = p.scale * kLog2e, c = a * x.m;
-    const float total = huge(x.m, a) ? log_s : __builtin_fmaf(-kLn2, __builtin_fmaf(a, x.m, -c), log_s);
+    const float a = p.scale * kLog2e;
+    const float total = __builtin_fmaf(-kLn2, lacking(x.m, a), log_s);
     if (lane == 0) {
         if (p.tokens != nullptr) {
             const int t = p.tokens[row];
@@ -185,7 +191,7 @@ __global__ void __launch_bounds__(256) log_probs_kernel(LogProbsArgs p)
             if (__ballot(huge(x.m, a)) == 0) {
                 terms([&](float v) { return __builtin_fmaf(a, v, -c_m); });
             } else {
-                const float rest = huge(x.m, a) ? 0.0f : __builtin_fmaf(a, x.m, -c_m);
+                const float rest = lacking(x.m, a);
                 terms([&](float v) { return a * (v - x.m) + rest; });
             }
             x.s += (s[0] + s[1]) + (s[2] + s[3]);

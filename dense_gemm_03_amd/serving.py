@@ -1,10 +1,10 @@
 """What stands around a model's products when it answers, over torch tensors:
 ``moe_layer`` (a whole mixture-of-experts layer for a few tokens), ``adapter_linear``
 (``linear`` with a low-rank adapter per row), ``log_probs`` (log probabilities of given
-tokens, entropy, alternatives) and its gradient ``log_probs_grad``; a thin binding over ``include/gemm_serving.h``.  Like
-the rest of the package they take no part in torch's autograd.  The C entry points
-are here under their own names (``gemm_*``), taking parameters, device pointers and
-a stream."""
+tokens, entropy, alternatives) and its gradient ``log_probs_grad``; a thin binding over
+``include/gemm_serving.h``.  Like the rest of the package they take no part in torch's
+autograd.  The C entry points are here under their own names (``gemm_*``), taking
+parameters, device pointers and a stream."""
 from __future__ import annotations
 
 import collections
@@ -253,7 +253,7 @@ def log_probs(logits, tokens=None, top=0, *, scale=1.0, stream=None):
     and most likely alternatives.
 
     ``logits`` (rows x vocabulary, float32 or bfloat16, contiguous rows) are
-    multiplied by ``scale`` (1 / temperature, > 0) first.  ``tokens`` is an int32
+    multiplied by ``scale`` (1 / temperature, > 0, at most 2^64) first.  ``tokens`` is an int32
     tensor of one place per row; one outside the vocabulary is padding.  ``top`` (0
     to 64) alternatives come in falling order, equal logits by the lower place.
     Returns ``LogProbs``, float32 but for the places (int32):
@@ -278,7 +278,7 @@ def log_probs(logits, tokens=None, top=0, *, scale=1.0, stream=None):
     lib = _library()
     need = lib.gemm_log_probs_workspace_size(params)
     if need < 0:
-        raise ValueError("top must be 0 .. 64 and at most the vocabulary, scale finite and positive; not %r and %r"
+        raise ValueError("top must be 0 .. 64 and at most the vocabulary, scale positive and at most 2^64; not %r and %r"
                          % (top, scale))
     at = _Launch(device, stream)
     try:

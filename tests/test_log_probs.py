@@ -28,7 +28,7 @@ def params(**kw):
 # ------------------------------------------------------------ without a GPU --
 
 BAD_PARAMS = [dict(dtype=2), dict(dtype=-1), dict(top=-1), dict(top=65), dict(top=20, vocab=19), dict(scale=0.0),
-              dict(scale=-1.0), dict(scale=INF), dict(scale=math.nan), dict(rows=-1), dict(rows=(1 << 30) + 1),
+              dict(scale=-1.0), dict(scale=INF), dict(scale=math.nan), dict(scale=2.0 ** 65), dict(rows=-1), dict(rows=(1 << 30) + 1),
               dict(vocab=0, top=0), dict(vocab=(1 << 30) + 1, ld=1 << 31), dict(ld=999), dict(ld=(1 << 40) + 1)]
 
 
@@ -306,6 +306,35 @@ def test_gradient_in_place(cuda, dtype):
     want = dg.log_probs_grad(z, t, f.stats, f.entropy, g, h)
     got = dg.log_probs_grad(z, t, f.stats, f.entropy, g, h, out=z)
     assert got is z and torch.equal(got, want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("base", [1e4, 1e6, 1e7, 1.2e7, 3e7, 1e9, 1e13, 1e20, 1e30, 1e37, -1e7, -1e20])
+def test_large_logits_close_together(cuda, dtype, base):
+    """Logits of any size whose scaled distances are ordinary, or large: rows of one sign,
+    and rows that climb from small values to large ones."""
+    gen = torch.Generator().manual_seed(5)
+    step = abs(base) * torch.finfo(dtype).eps
+    z = base + step * torch.randint(-40, 41, (6, 3001), generator=gen).double()
+    z[4, :2000] = torch.linspace(0, 1, 2000).double() * base
+    z[5] = base * torch.linspace(0.5, 1, 3001).double()
+    z = z.to(dtype).cuda()
+    t = torch.tensor([0, 5, 2999, -1, 2500, 3000], dtype=torch.int32, device="cuda")
+    for rows in (6, 1):
+        for scale in (0.3, 3.0, 7.0, 30.0, 300.0, 1e6, 1e15):
+            if scale / step <= 2.0 ** 64:
+                check(z[-rows:], t[-rows:], 5, scale=scale / step)
+        check_grad(z[-rows:], t[-rows:], scale=0.3 / step)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("scale", [2.0 ** 64, 2.0 ** 40, 2.0 ** -60, 2.0 ** -140])
+def test_extreme_scales(cuda, scale):
+    z = torch.randn(5, 2500, generator=torch.Generator().manual_seed(2)).cuda()
+    t = torch.tensor([0, 7, 100, 2499, 3], dtype=torch.int32, device="cuda")
+    t[1] = z[1].argmax()
+    check(z, t, 3, scale=scale)
 
 
 @pytest.mark.gpu
