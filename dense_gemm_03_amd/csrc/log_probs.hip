@@ -7,7 +7,12 @@
 // known exactly (a m - c is another), so a large m costs no digits.
 //
 // One pass over the logits: each lane keeps (m, s, u) of what it has read and moves
-// them to a larger m when it finds one, 32 logits at a time.
+// them to a larger m when it finds one, 32 logits at a time, which are loaded while the
+// 32 before are summed.
+//
+// Bound by HBM and by the exponents' arithmetic alike with many rows (4001 x 50021 bf16, 5
+// alternatives: 84 us, 4.7 TB/s), by latency with few: 1 x 131072 fp32 takes 4.7 us for the
+// parts and 2.8 us to join them, with 20 alternatives 9.7 and 5.5.
 #include "serving.hpp"
 #include "topk.hpp"
 
@@ -276,8 +281,8 @@ __global__ void __launch_bounds__(256) log_probs_join_kernel(LogProbsArgs p)
 //     dz_j = p_j (c + b t_j) [+ scale g at the token],   t_j = log2 p_j,  p_j = 2^t_j
 //     c = -scale (g + h entropy),   b = -scale h ln2
 //
-// Bound by HBM: one read and one write of the logits.  A wave takes 64 * U vectors
-// of a row.
+// Bound by HBM: one read and one write of the logits (4096 x 32768 bf16, 537 MB: 85 us,
+// 6.3 TB/s, part of it from the memory-side cache).  A wave takes 64 * U vectors of a row.
 template <bool BF16>
 __global__ void __launch_bounds__(256) log_probs_grad_kernel(LogProbsGradArgs p, int segments)
 {

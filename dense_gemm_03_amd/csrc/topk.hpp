@@ -31,7 +31,7 @@ __device__ __forceinline__ int place_of(uint64_t key) { return (int)~(uint32_t)k
 
 // v of the lane whose number differs in the bits `mask`, through the vector unit:
 // DPP within 16 lanes, swaps of rows and halves beyond.  (Through LDS, as a shuffle, a
-// sort took twice as long: 131072 logits with 20 alternatives 16.5 us, now 14.)
+// sort took twice as long: 131072 logits with 20 alternatives 16.5 us, then 14.)
 template <int MASK>
 __device__ __forceinline__ uint32_t xor_lane(uint32_t v)
 {
@@ -126,9 +126,9 @@ struct TopList {
         list = lane < at ? list : lane == at ? key : below;
         least = key_at(list, top - 1);
     }
-    // N values per lane, v[j] at place(first, j) (not below 0 and below n, or the
-    // value does not count and is -infinity), `largest` the lane's largest, as fmaxf finds it.  If
-    // many lanes have something for the list, their largest go in at once, sorted,
+    // N values per lane, v[j] at place(first, j) (not below 0 and below n, or the value
+    // does not count and is -infinity), `largest` the lane's largest, as fmaxf finds it.
+    // If many lanes have something for the list, their largest go in at once, sorted,
     // which leaves little above the new bound.  The lanes that have something (else),
     // mostly one or two, are gone through one by one, their N values spread over the
     // lanes through `row` (LDS, N floats of this wave's own).
@@ -170,7 +170,9 @@ struct TopList {
     }
 
 private:
-    static constexpr int MANY = 6;   // lanes from which a sort costs less than insertions
+    // Lanes from which a sort costs less than insertions: 27 exchanges against one
+    // insertion per value.
+    static constexpr int MANY = 6;
 
     // each lane's key, one by one
     __device__ __forceinline__ void insert_lanes(uint64_t k)
