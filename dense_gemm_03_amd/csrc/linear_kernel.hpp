@@ -661,6 +661,8 @@ __device__ __forceinline__ void linear_tile(const Args &p, const TileSpec &t, un
         const int row0 = t.row0 + c.wcol * G::WTN, col0 = t.col0 + c.wrow * G::WTM;
         if (G::FM * G::FN > 16 || p.ad.rank <= (BF16 ? 32 : 8))
             adapters.template add<1>(p.ad, c.lane, row0, t.m, col0, p.N, t.slice, p.splits, acc);
+        else if (!BF16 && G::FM * G::FN <= 2 && p.ad.rank > 16)   // steps of 8 ranks: 614 x 443 -> 5740, rank 64, 82 us, by two 88
+            adapters.template add<(!BF16 && G::FM * G::FN <= 2 ? 4 : 1)>(p.ad, c.lane, row0, t.m, col0, p.N, t.slice, p.splits, acc);
         else
             adapters.template add<(G::FM * G::FN > 16 ? 1 : 2)>(p.ad, c.lane, row0, t.m, col0, p.N, t.slice, p.splits, acc);
     }
